@@ -386,6 +386,102 @@ mxfp4_status_t mxfp4_grouped_matmul(int32_t group_type, int64_t M, int64_t N, in
                                     int32_t group_list_type, int64_t k_blocks,
                                     int32_t out_dtype, void *c, int64_t ldc, void *stream);
 
+/* ---- mixture of experts: tokens to experts and back ------------------------ */
+
+enum { MXMOE_SOFTMAX = 0, MXMOE_SIGMOID = 1 };
+
+typedef struct mxfp4_moe_route {
+  int32_t dtype;        /* logits: MXFP4_BF16 or MXFP4_F32                     */
+  int32_t score;        /* MXMOE_SOFTMAX or MXMOE_SIGMOID                      */
+  int32_t renormalize;  /* 1: the chosen weights are divided by their sum      */
+  int32_t experts;      /* 1 .. 1024                                           */
+  int64_t tokens;
+  int32_t k;            /* experts a token: 1 .. 64                            */
+  int32_t num_groups;   /* 1: no groups; at most 64, dividing experts          */
+  int32_t topk_groups;  /* groups that stay                                    */
+  float scale;          /* factor of every weight                              */
+  int32_t reserved;     /* must be 0                                           */
+} mxfp4_moe_route_t;
+
+/*
+ * Expert choice.  Per token: scores s = softmax(logits) or 1 / (1 + exp(-l)),
+ * in fp32.  The experts are ordered by v = s + bias when a bias [experts] or
+ * groups are given (the bias moves the choice only, not the weights), else by
+ * the logits, which order them as s does.  With groups (num_groups equal runs
+ * of consecutive experts), a group's value is the sum of its two largest v,
+ * and only the topk_groups best groups stay.  The k largest v are chosen, in
+ * descending order; equal values, of experts or groups, go to the lowest
+ * index.  An expert whose logit, or whose v, is -inf or NaN is never chosen; a
+ * slot for which no expert is left (a masked token) gets id -1 and weight 0.
+ *   weights [tokens, k] fp32: scale * s, or scale * s / sum of the chosen s
+ *           (0 where that sum is 0);   ids [tokens, k] int32.
+ * logits aligned to one element; weights, ids and bias to 4 bytes.
+ */
+mxfp4_status_t mxfp4_moe_route(const mxfp4_moe_route_t *desc, const void *logits, const float *bias,
+                               float *weights, int32_t *ids, void *stream);
+
+/*
+ * Gradient of the weights with respect to the logits, the choice being
+ * constant: grad_logits [tokens, experts] (the logits' type) from grad_weights
+ * and ids [tokens, k] as mxfp4_moe_route returned them (distinct, or -1).
+ * Without renormalisation a softmax row's gradient is dense; otherwise only
+ * the chosen experts' entries differ from 0.  num_groups and topk_groups have
+ * no influence.
+ */
+mxfp4_status_t mxfp4_moe_route_bwd(const mxfp4_moe_route_t *desc, const float *grad_weights,
+                                   const void *logits, const int32_t *ids, void *grad_logits,
+                                   void *stream);
+
+/*
+ * Order of the slots by expert: slot i = token * k + choice of ids [slots].
+ *   group_list [experts] int64: slots of each expert (the counts, type 1, that
+ *              the grouped calls take);
+ *   rows [slots] int32: the slot's row when the slots are sorted by expert,
+ *              equal experts in slot order; -1 for an id outside [0, experts).
+ * workspace: mxfp4_moe_plan_workspace(slots, experts) bytes (0 for few slots;
+ * -1 for arguments that the plan refuses), 4-byte aligned, in use until the
+ * call's kernels are done.  experts 1 .. 1024.
+ */
+int64_t mxfp4_moe_plan_workspace(int64_t slots, int32_t experts);
+mxfp4_status_t mxfp4_moe_plan(int64_t slots, int32_t experts, const int32_t *ids, int64_t *group_list,
+                              int32_t *rows, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Token rows x (desc->rows tokens x desc->cols) to their slots' rows: for every
+ * slot with 0 <= rows[t, j] < out_rows, output row rows[t, j] becomes x[t],
+ *   y [out_rows, cols] as it is (x's type), and / or
+ *   q [out_rows, cols] + scales [out_rows, ceil(cols / block)] as MXFP8 (fmt,
+ *   desc->block 32 or 128, the rule of mxfp8_quant: the same codes as
+ *   quantizing the copied rows).
+ * Other output rows are not written.  k <= 64.  Any alignment of whole
+ * elements; no aliasing.
+ */
+mxfp4_status_t mxfp4_moe_dispatch(const mxfp4_desc_t *desc, int32_t fmt, const void *x,
+                                  const int32_t *rows, int32_t k, int64_t out_rows, void *y,
+                                  uint8_t *q, uint8_t *scales, void *stream);
+
+/*
+ * Expert rows back to the tokens: y[t] = residual[t] + sum_j weights[t, j] *
+ * h[rows[t, j]], summed in fp32 in the order of j and rounded once; a slot whose
+ * row is outside [0, in_rows) adds nothing.  weights NULL: 1 (the gradient of
+ * dispatch).  residual NULL: none; y may be the residual.  h [in_rows, cols],
+ * y and residual [tokens, cols], all of `dtype`; k <= 64.
+ */
+mxfp4_status_t mxfp4_moe_combine(int32_t dtype, int64_t tokens, int64_t cols, int32_t k, int64_t in_rows,
+                                 const void *h, const int32_t *rows, const float *weights,
+                                 const void *residual, void *y, void *stream);
+
+/*
+ * Gradients of combine: grad_h[rows[t, j]] = weights[t, j] * grad_y[t] (NULL:
+ * not wanted; rows of no slot are not written) and grad_weights[t, j] =
+ * <grad_y[t], h[rows[t, j]]> in fp32 (NULL: not wanted, h may be NULL then; 0
+ * for a slot without a row).  The residual's gradient is grad_y itself.
+ */
+mxfp4_status_t mxfp4_moe_combine_bwd(int32_t dtype, int64_t tokens, int64_t cols, int32_t k,
+                                     int64_t in_rows, const void *grad_y, const void *h,
+                                     const int32_t *rows, const float *weights, void *grad_h,
+                                     float *grad_weights, void *stream);
+
 /* Message for the calling thread's most recent failed call ("" if none). */
 const char *mxfp4_last_error(void);
 

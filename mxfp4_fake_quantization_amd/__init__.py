@@ -609,3 +609,10 @@ def kmajor_k_blocks(rows: int, block: int, num_groups=None, align: bool = True) 
         if nb and (nb * block // 2) % 4096 == 0:
             nb += step
     return nb
+
+
+# The mixture-of-experts calls build on the marshalling above.
+from . import moe_ops as _moe_ops  # noqa: E402
+from .moe_ops import *  # noqa: E402,F401,F403
+
+__all__ += _moe_ops.__all__

@@ -1,0 +1,179 @@
+// api_moe.hip -- the extern "C" entry points of the mixture-of-experts
+// operators (include/mxfp4.h).  As in api.hip: arguments are validated on the
+// host before anything is enqueued, the kernels run on the caller's stream,
+// nothing is allocated or synchronized.
+#include "api_common.h"
+#include "moe_kernels.h"
+#include "mxfp4_kernels.h"
+
+using namespace mxfp4_api;
+
+namespace {
+
+mxfp4_status_t check_dtype(int32_t dtype) {
+  if (dtype != MXFP4_BF16 && dtype != MXFP4_F32)
+    return fail(MXFP4_EUNSUPPORTED, "dtype %d is not MXFP4_BF16 or MXFP4_F32", dtype);
+  return MXFP4_OK;
+}
+
+// Pointers of elements: aligned to one element.
+mxfp4_status_t check_elems(const void *p, int32_t dtype, const char *what) {
+  return check_ptr(p, dtype == MXFP4_F32 ? 4 : 2, what);
+}
+
+mxfp4_status_t check_route(const mxfp4_moe_route_t *d) {
+  if (!d) return fail(MXFP4_EINVAL, "desc is NULL");
+  MXFP4_TRY(check_dtype(d->dtype));
+  if (d->score != MXMOE_SOFTMAX && d->score != MXMOE_SIGMOID)
+    return fail(MXFP4_EINVAL, "score %d is not MXMOE_SOFTMAX or MXMOE_SIGMOID", d->score);
+  if (d->renormalize != 0 && d->renormalize != 1)
+    return fail(MXFP4_EINVAL, "renormalize must be 0 or 1 (got %d)", d->renormalize);
+  if (d->tokens < 0) return fail(MXFP4_EINVAL, "negative tokens %lld", (long long)d->tokens);
+  if (d->experts < 1 || d->experts > mxfp4::kRouteMaxExperts)
+    return fail(MXFP4_EUNSUPPORTED, "experts %d is not in [1, %d]", d->experts, mxfp4::kRouteMaxExperts);
+  if (d->k < 1 || d->k > mxfp4::kRouteMaxK || d->k > d->experts)
+    return fail(MXFP4_EUNSUPPORTED, "k %d is not in [1, %d] or above the %d experts", d->k, mxfp4::kRouteMaxK,
+                d->experts);
+  if (d->num_groups < 1 || d->num_groups > mxfp4::kRouteMaxGroups || d->experts % d->num_groups != 0)
+    return fail(MXFP4_EINVAL, "num_groups %d is not in [1, %d] or does not divide the %d experts", d->num_groups,
+                mxfp4::kRouteMaxGroups, d->experts);
+  if (d->topk_groups < 1 || d->topk_groups > d->num_groups)
+    return fail(MXFP4_EINVAL, "topk_groups %d is not in [1, %d]", d->topk_groups, d->num_groups);
+  if ((int64_t)d->topk_groups * (d->experts / d->num_groups) < d->k)
+    return fail(MXFP4_EINVAL, "%d groups of %d experts hold fewer than k = %d", d->topk_groups,
+                d->experts / d->num_groups, d->k);
+  if (d->tokens > INT64_MAX / 8 / d->experts) return fail(MXFP4_EINVAL, "tokens * experts overflows");
+  if (d->reserved != 0) return fail(MXFP4_EINVAL, "reserved fields must be 0");
+  return MXFP4_OK;
+}
+
+mxfp4_status_t check_slots(int64_t tokens, int32_t k, int64_t cols, int64_t n_rows, const char *what) {
+  if (tokens < 0 || cols < 0 || n_rows < 0)
+    return fail(MXFP4_EINVAL, "negative shape: tokens %lld, cols %lld, %s %lld", (long long)tokens, (long long)cols,
+                what, (long long)n_rows);
+  if (k < 1 || k > mxfp4::kRouteMaxK)
+    return fail(MXFP4_EUNSUPPORTED, "k %d is not in [1, %d]", k, mxfp4::kRouteMaxK);
+  const int64_t most = tokens > n_rows ? tokens : n_rows;
+  if (cols > 0 && most > INT64_MAX / 8 / cols) return fail(MXFP4_EINVAL, "rows * cols overflows");
+  if (n_rows > INT32_MAX) return fail(MXFP4_EUNSUPPORTED, "%s %lld is above 2^31 - 1", what, (long long)n_rows);
+  return MXFP4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mxfp4_status_t mxfp4_moe_route(const mxfp4_moe_route_t *desc, const void *logits, const float *bias, float *weights,
+                               int32_t *ids, void *stream) {
+  MXFP4_TRY(check_route(desc));
+  if (desc->tokens == 0) return ok();
+  MXFP4_TRY(check_elems(logits, desc->dtype, "logits"));
+  MXFP4_TRY(check_opt(bias, 4, "bias"));
+  MXFP4_TRY(check_ptr(weights, 4, "weights"));
+  MXFP4_TRY(check_ptr(ids, 4, "ids"));
+  if (!distinct({logits, bias, weights, ids})) return fail(MXFP4_EINVAL, "outputs alias each other or an input");
+  mxfp4::RouteLaunch L{desc->dtype, desc->score, desc->renormalize, desc->tokens, desc->experts, desc->k,
+                       desc->num_groups, desc->topk_groups, desc->scale, logits, bias, weights, ids};
+  return hip_status(mxfp4::launch_route(L, static_cast<hipStream_t>(stream)), "routing launch");
+}
+
+mxfp4_status_t mxfp4_moe_route_bwd(const mxfp4_moe_route_t *desc, const float *grad_weights, const void *logits,
+                                   const int32_t *ids, void *grad_logits, void *stream) {
+  MXFP4_TRY(check_route(desc));
+  if (desc->tokens == 0) return ok();
+  MXFP4_TRY(check_ptr(grad_weights, 4, "grad_weights"));
+  MXFP4_TRY(check_elems(logits, desc->dtype, "logits"));
+  MXFP4_TRY(check_ptr(ids, 4, "ids"));
+  MXFP4_TRY(check_elems(grad_logits, desc->dtype, "grad_logits"));
+  if (!distinct({grad_weights, logits, ids, grad_logits})) return fail(MXFP4_EINVAL, "grad_logits aliases an input");
+  mxfp4::RouteBwdLaunch L{desc->dtype, desc->score, desc->renormalize, desc->tokens, desc->experts, desc->k,
+                          desc->scale, grad_weights, logits, ids, grad_logits};
+  return hip_status(mxfp4::launch_route_bwd(L, static_cast<hipStream_t>(stream)), "routing backward launch");
+}
+
+int64_t mxfp4_moe_plan_workspace(int64_t slots, int32_t experts) {
+  if (slots < 0 || slots > INT32_MAX || experts < 1 || experts > mxfp4::kRouteMaxExperts) return -1;
+  return 4 * mxfp4::plan_workspace(slots, experts);
+}
+
+mxfp4_status_t mxfp4_moe_plan(int64_t slots, int32_t experts, const int32_t *ids, int64_t *group_list, int32_t *rows,
+                              void *workspace, int64_t workspace_bytes, void *stream) {
+  if (slots < 0) return fail(MXFP4_EINVAL, "negative slots %lld", (long long)slots);
+  if (slots > INT32_MAX) return fail(MXFP4_EUNSUPPORTED, "slots %lld is above 2^31 - 1", (long long)slots);
+  if (experts < 1 || experts > mxfp4::kRouteMaxExperts)
+    return fail(MXFP4_EUNSUPPORTED, "experts %d is not in [1, %d]", experts, mxfp4::kRouteMaxExperts);
+  MXFP4_TRY(check_ptr(group_list, 8, "group_list"));
+  if (slots > 0) {
+    MXFP4_TRY(check_ptr(ids, 4, "ids"));
+    MXFP4_TRY(check_ptr(rows, 4, "rows"));
+  }
+  const int64_t need = 4 * mxfp4::plan_workspace(slots, experts);
+  if (need > 0) {
+    MXFP4_TRY(check_ptr(workspace, 4, "workspace"));
+    if (workspace_bytes < need)
+      return fail(MXFP4_EINVAL, "workspace holds %lld bytes; the call needs %lld", (long long)workspace_bytes,
+                  (long long)need);
+  }
+  if (!distinct({ids, group_list, rows, need > 0 ? workspace : nullptr}))
+    return fail(MXFP4_EINVAL, "outputs alias each other or ids");
+  mxfp4::PlanLaunch L{slots, experts, ids, group_list, rows, static_cast<int32_t *>(workspace)};
+  return hip_status(mxfp4::launch_plan(L, static_cast<hipStream_t>(stream)), "plan launch");
+}
+
+mxfp4_status_t mxfp4_moe_dispatch(const mxfp4_desc_t *desc, int32_t fmt, const void *x, const int32_t *rows, int32_t k,
+                                  int64_t out_rows, void *y, uint8_t *q, uint8_t *scales, void *stream) {
+  int64_t n;
+  MXFP4_TRY(check_desc(desc, false, &n));
+  MXFP4_TRY(check_slots(desc->rows, k, desc->cols, out_rows, "out_rows"));
+  if (!y && !q) return fail(MXFP4_EINVAL, "no output given");
+  if (!q != !scales) return fail(MXFP4_EINVAL, "q and scales come together");
+  if (q && fmt != MXFP8_E4M3 && fmt != MXFP8_E5M2)
+    return fail(MXFP4_EINVAL, "fmt %d is not MXFP8_E4M3 or MXFP8_E5M2", fmt);
+  if (n == 0 || out_rows == 0) return ok();
+  MXFP4_TRY(check_elems(x, desc->dtype, "x"));
+  MXFP4_TRY(check_ptr(rows, 4, "rows"));
+  if (y) MXFP4_TRY(check_elems(y, desc->dtype, "y"));
+  if (!distinct({x, rows, y, q, scales})) return fail(MXFP4_EINVAL, "outputs alias each other or an input");
+  mxfp4::DispatchLaunch L{desc->dtype, fmt, desc->block, desc->rows, desc->cols, out_rows, k, x, rows, y, q, scales};
+  return hip_status(mxfp4::launch_dispatch(L, static_cast<hipStream_t>(stream)), "dispatch launch");
+}
+
+mxfp4_status_t mxfp4_moe_combine(int32_t dtype, int64_t tokens, int64_t cols, int32_t k, int64_t in_rows, const void *h,
+                                 const int32_t *rows, const float *weights, const void *residual, void *y,
+                                 void *stream) {
+  MXFP4_TRY(check_dtype(dtype));
+  MXFP4_TRY(check_slots(tokens, k, cols, in_rows, "in_rows"));
+  if (tokens == 0 || cols == 0) return ok();
+  if (in_rows > 0) MXFP4_TRY(check_elems(h, dtype, "h"));
+  MXFP4_TRY(check_ptr(rows, 4, "rows"));
+  MXFP4_TRY(check_opt(weights, 4, "weights"));
+  if (residual) MXFP4_TRY(check_elems(residual, dtype, "residual"));
+  MXFP4_TRY(check_elems(y, dtype, "y"));
+  // y may be the residual (the token's row is read before it is written)
+  if (!distinct({h, rows, weights, residual == y ? nullptr : residual, y}))
+    return fail(MXFP4_EINVAL, "y aliases an input");
+  mxfp4::CombineLaunch L{dtype, tokens, cols, in_rows, k, h, rows, weights, residual, y};
+  return hip_status(mxfp4::launch_combine(L, static_cast<hipStream_t>(stream)), "combine launch");
+}
+
+mxfp4_status_t mxfp4_moe_combine_bwd(int32_t dtype, int64_t tokens, int64_t cols, int32_t k, int64_t in_rows,
+                                     const void *grad_y, const void *h, const int32_t *rows, const float *weights,
+                                     void *grad_h, float *grad_weights, void *stream) {
+  MXFP4_TRY(check_dtype(dtype));
+  MXFP4_TRY(check_slots(tokens, k, cols, in_rows, "in_rows"));
+  if (!grad_h && !grad_weights) return fail(MXFP4_EINVAL, "no output given");
+  const bool empty = cols == 0;  // every dot product is 0 then
+  if (tokens == 0 || (empty && !grad_weights)) return ok();
+  if (!empty) MXFP4_TRY(check_elems(grad_y, dtype, "grad_y"));
+  MXFP4_TRY(check_ptr(rows, 4, "rows"));
+  if (grad_weights && in_rows > 0 && !empty) MXFP4_TRY(check_elems(h, dtype, "h"));
+  MXFP4_TRY(check_opt(weights, 4, "weights"));
+  if (grad_h && in_rows > 0 && !empty) MXFP4_TRY(check_elems(grad_h, dtype, "grad_h"));
+  MXFP4_TRY(check_opt(grad_weights, 4, "grad_weights"));
+  if (!distinct({grad_y, grad_weights ? h : nullptr, rows, weights, grad_h, grad_weights}))
+    return fail(MXFP4_EINVAL, "outputs alias each other or an input");
+  mxfp4::CombineBwdLaunch L{dtype, tokens, cols, in_rows, k, grad_y, h, rows, weights, grad_h, grad_weights};
+  return hip_status(mxfp4::launch_combine_bwd(L, static_cast<hipStream_t>(stream)), "combine backward launch");
+}
+
+}  // extern "C"

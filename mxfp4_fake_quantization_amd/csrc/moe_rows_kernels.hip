@@ -1,0 +1,518 @@
+// moe_rows_kernels.hip -- tokens into expert order and back on gfx950.
+//
+// The experts' product takes the rows of expert 0, then of expert 1, ... (its
+// group_list holds the counts).  The plan ranks the slots (token t, choice j)
+// in that order, equal experts by slot: rows[t, j] is the slot's row, -1 for a
+// slot without an expert.  Dispatch writes a token's row to its k rows (as it
+// is, or as MXFP8, quantized once); combine sums a token's k rows with its
+// weights.  Everything is addressed by token, so no kernel needs the inverse
+// order and no sum uses atomics: results do not depend on timing.
+#include "moe_kernels.h"
+#include "mxfp4_device.h"
+#include "mxfp4_kernels.h"
+
+namespace mxfp4 {
+namespace {
+
+// Rows of any length start at any element: 16-byte accesses with the
+// element's alignment (the hardware takes unaligned global accesses).
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
+
+template <int DT>
+struct Row8 {  // 8 consecutive elements of a row
+  static constexpr int ES = DT == kBF16 ? 2 : 4, NW = 2 * ES;
+};
+
+template <int DT>
+__device__ __forceinline__ void load8(uint32_t (&w)[Row8<DT>::NW], const uint8_t *p, int n) {
+  if (n >= 8) {
+#pragma unroll
+    for (int q = 0; q < Row8<DT>::NW / 4; ++q) {
+      const u32x4 v = *reinterpret_cast<const u32x4_a2 *>(p + 16 * q);
+      w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < Row8<DT>::NW; ++q) w[q] = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) {
+      if (DT == kBF16) w[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[j] << (16 * (j & 1));
+      else w[j % Row8<DT>::NW] = reinterpret_cast<const uint32_t *>(p)[j];
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(uint8_t *p, const uint32_t (&w)[Row8<DT>::NW], int n) {
+  if (n >= 8) {
+#pragma unroll
+    for (int q = 0; q < Row8<DT>::NW / 4; ++q) {
+      const u32x4 v = {w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2 *>(p + 16 * q));
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) {
+      if (DT == kBF16) reinterpret_cast<uint16_t *>(p)[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+      else reinterpret_cast<uint32_t *>(p)[j] = w[j % Row8<DT>::NW];
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ float elem(const uint32_t (&w)[Row8<DT>::NW], int j) {
+  if (DT == kBF16) return bits_f32(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+  return bits_f32(w[j % Row8<DT>::NW]);
+}
+
+__device__ __forceinline__ uint32_t bf16_rne(float f) {
+  uint32_t u = __builtin_bit_cast(uint32_t, f);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
+  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+
+template <int DT>
+__device__ __forceinline__ void pack8(uint32_t (&w)[Row8<DT>::NW], const float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < Row8<DT>::NW; ++j)
+    w[j] = DT == kBF16 ? bf16_rne(f[(2 * j) % 8]) | (bf16_rne(f[(2 * j + 1) % 8]) << 16)
+                       : __builtin_bit_cast(uint32_t, f[j % 8]);
+}
+
+// ---- plan --------------------------------------------------------------------
+//
+// A stable counting sort by expert.  A workgroup of 16 waves takes a chunk of
+// consecutive slots, each wave a consecutive part of it, 64 at a time: the
+// lanes of a step that hold the same expert are found by one ballot per bit
+// of the expert number, which gives a slot's rank among them, and the wave's
+// running counts (one row of LDS counters per wave) the rank before the step.
+// One chunk (up to kPlanOne slots): one launch.  More: a first launch counts
+// every chunk, the second adds the counts of the chunks before its own (read
+// in order, from L2).
+
+constexpr int kPlanWaves = 16, kPlanThreads = 64 * kPlanWaves;
+constexpr int64_t kPlanOne = 8192;
+constexpr int kPlanMaxChunks = 256;
+
+int64_t plan_chunk(int64_t slots) {
+  if (slots <= kPlanOne) return kPlanOne;
+  const int64_t per = (slots + kPlanMaxChunks - 1) / kPlanMaxChunks;
+  const int64_t c = (per + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
+  return c < 2048 ? 2048 : c;
+}
+
+struct PlanArgs {
+  const int32_t *ids;
+  int64_t *group_list;
+  int32_t *rows, *hist;  // hist [chunks, experts]
+  int64_t slots, chunk;
+  int experts, bits, chunks;
+};
+
+__device__ __forceinline__ int plan_id(const PlanArgs &A, int64_t i, int64_t end) {
+  if (i >= end) return A.experts;
+  const int e = A.ids[i];
+  return e >= 0 && e < A.experts ? e : A.experts;  // the last number: slots without an expert
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs A) {
+  __shared__ int32_t cnt[kRouteMaxExperts];
+  for (int e = threadIdx.x; e < A.experts; e += kPlanThreads) cnt[e] = 0;
+  __syncthreads();
+  const int64_t lo = (int64_t)blockIdx.x * A.chunk;
+  const int64_t end = lo + A.chunk < A.slots ? lo + A.chunk : A.slots;
+  for (int64_t i = lo + threadIdx.x; i < end; i += kPlanThreads) {
+    const int e = plan_id(A, i, end);
+    if (e < A.experts) atomicAdd(&cnt[e], 1);  // a count: the order of the additions does not matter
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < A.experts; e += kPlanThreads) A.hist[(int64_t)blockIdx.x * A.experts + e] = cnt[e];
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs A) {
+  __shared__ int32_t cnt[kPlanWaves][kRouteMaxExperts];
+  __shared__ int32_t wsum[kPlanWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int i = tid; i < kPlanWaves * A.experts; i += kPlanThreads) cnt[i / A.experts][i % A.experts] = 0;
+  __syncthreads();
+  const int64_t lo = (int64_t)blockIdx.x * A.chunk;
+  const int64_t end = lo + A.chunk < A.slots ? lo + A.chunk : A.slots;
+  const int64_t part = A.chunk / kPlanWaves;  // a multiple of 64
+  const int64_t wlo = lo + wave * part;
+  const int64_t wend = wlo + part < end ? wlo + part : end;
+  for (int64_t i = wlo + lane; i < wend; i += 64) {
+    const int e = plan_id(A, i, wend);
+    if (e < A.experts) atomicAdd(&cnt[wave][e], 1);
+  }
+  __syncthreads();
+  // expert e (one a thread): its rows before this chunk, and all of them
+  int32_t mine = 0, before = 0, total = 0;
+  if (tid < A.experts) {
+    for (int w = 0; w < kPlanWaves; ++w) mine += cnt[w][tid];
+    if (A.chunks == 1) {
+      total = mine;
+    } else {
+      for (int b = 0; b < A.chunks; ++b) {
+        const int32_t c = A.hist[(int64_t)b * A.experts + tid];
+        before += b < (int)blockIdx.x ? c : 0;
+        total += c;
+      }
+    }
+    if (blockIdx.x == 0) A.group_list[tid] = total;
+  }
+  // exclusive scan of the totals over the experts
+  int32_t incl = total;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t o = __shfl_up(incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 63) wsum[wave] = incl;
+  __syncthreads();
+  int32_t at = incl - total + before;
+  for (int w = 0; w < wave; ++w) at += wsum[w];
+  if (tid < A.experts) {
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int32_t c = cnt[w][tid];
+      cnt[w][tid] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  // Every lane of a wave takes part in the ballots: the loop count is the wave's.
+  for (int64_t base = wlo; base < wend; base += 64) {
+    const int64_t i = base + lane;
+    const int e = plan_id(A, i, wend);
+    uint64_t same = ~0ull;
+    for (int b = 0; b < A.bits; ++b) {
+      const uint64_t on = __ballot((e >> b) & 1);
+      same &= (e >> b) & 1 ? on : ~on;
+    }
+    const uint64_t below = (1ull << lane) - 1;
+    if (e < A.experts) {
+      const int32_t first = cnt[wave][e];
+      A.rows[i] = first + (int32_t)__popcll(same & below);
+      // the group's last lane moves the count on (a wave's LDS operations keep
+      // their order: the reads above come first)
+      if ((same >> lane) == 1ull) cnt[wave][e] = first + (int32_t)__popcll(same);
+    } else if (i < wend) {
+      A.rows[i] = -1;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ---- dispatch ------------------------------------------------------------------
+//
+// A workgroup takes 1024 elements of one token, 8 a lane, quantizes them once
+// (the OCP MX rule of the row-wise MXFP8 kernel: E8M0 scale from the exponent
+// of the block's largest magnitude, exact scaling, hardware conversion) and
+// stores them to the token's k rows, 512 contiguous bytes a wave.  Bound by
+// the bytes written.
+
+struct DispatchArgs {
+  const uint8_t *x;
+  const int32_t *rows;
+  uint8_t *y, *q, *scales;
+  int64_t cols, nb, out_rows;
+  int k, chunks;  // workgroups a token
+};
+
+constexpr int kDispatchThreads = 128;
+
+// Row of slot i (-1 outside [0, n)) and its weight.  i is the same for the
+// workgroup, so these are scalar loads, which the branches around them, taken
+// lane by lane at the end of a row, do not touch.
+typedef const int32_t __attribute__((address_space(4))) *scalar_i32;
+typedef const float __attribute__((address_space(4))) *scalar_f32;
+__device__ __forceinline__ int slot_row(const int32_t *rows, int64_t i, int64_t n) {
+  const int r = ((scalar_i32)(uint64_t)rows)[i];
+  return r >= 0 && r < n ? r : -1;
+}
+__device__ __forceinline__ float slot_weight(const float *weights, int64_t i) {
+  return weights ? ((scalar_f32)(uint64_t)weights)[i] : 1.0f;
+}
+
+template <int DT, int FMT, int G>
+__global__ __launch_bounds__(kDispatchThreads) void dispatch_kernel(DispatchArgs A) {
+  constexpr int ES = Row8<DT>::ES;
+  constexpr float MAXN = FMT == kE4M3 ? 448.0f : 57344.0f;
+  constexpr int EMAX = FMT == kE4M3 ? 8 : 15;
+  const int64_t t = blockIdx.x / A.chunks;
+  const int64_t c0 = ((int64_t)(blockIdx.x % A.chunks) * kDispatchThreads + threadIdx.x) * 8;
+  const int64_t left = A.cols - c0;
+  const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+  uint32_t w[Row8<DT>::NW];
+  load8<DT>(w, A.x + (t * A.cols + c0) * ES, n);
+  uint32_t lo = 0, hi = 0, e8 = 0;
+  if (A.q) {
+    uint32_t am = 0;
+    if (DT == kBF16) {
+      const uint32_t m = pk_max(pk_max(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                pk_max(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+      am = max32(m & 0xFFFFu, m >> 16) << 16;
+    } else {
+#pragma unroll
+      for (int j = 0; j < Row8<DT>::NW; ++j) am = max32(am, w[j] & 0x7FFFFFFFu);
+    }
+    am = group_max<G>(am);
+    const int eb = (int)(am >> 23);
+    e8 = eb > EMAX ? (uint32_t)(eb - EMAX) : 0u;
+    const float s = bits_f32((254u - e8) << 23);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __builtin_amdgcn_fmed3f(elem<DT>(w, j) * s, -MAXN, MAXN);
+    auto two = [](float a, float b, uint32_t old, auto high) {
+      constexpr bool HI = decltype(high)::value;
+      return FMT == kE4M3 ? (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)old, HI)
+                          : (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(a, b, (int)old, HI);
+    };
+    lo = two(v[2], v[3], two(v[0], v[1], 0, std::false_type{}), std::true_type{});
+    hi = two(v[6], v[7], two(v[4], v[5], 0, std::false_type{}), std::true_type{});
+  }
+  if (n == 0) return;
+  const bool head = (threadIdx.x & (G - 1)) == 0;
+  for (int j = 0; j < A.k; ++j) {
+    const int64_t r = slot_row(A.rows, t * A.k + j, A.out_rows);
+    if (r < 0) continue;
+    if (A.y) store8<DT>(A.y + (r * A.cols + c0) * ES, w, n);
+    if (A.q) {
+      uint8_t *dst = A.q + r * A.cols + c0;
+      if (n == 8) {
+        const u32x2 pk = {lo, hi};
+        __builtin_nontemporal_store(pk, reinterpret_cast<u32x2_a1 *>(dst));
+      } else {
+        const uint64_t pk = (uint64_t)lo | ((uint64_t)hi << 32);
+        for (int b = 0; b < n; ++b) dst[b] = (uint8_t)(pk >> (8 * b));
+      }
+      if (head) A.scales[r * A.nb + c0 / (8 * G)] = (uint8_t)e8;
+    }
+  }
+}
+
+// ---- combine -------------------------------------------------------------------
+//
+// A lane sums 8 elements of a token over its k rows in 32 bits, in the order
+// of the choices; the rows' loads are independent, four in flight at a time.
+// Bound by the bytes read.
+
+struct CombineArgs {
+  const uint8_t *h;
+  const int32_t *rows;
+  const float *weights;
+  const uint8_t *residual;
+  uint8_t *y;
+  int64_t cols, in_rows;
+  int k, chunks;
+};
+
+constexpr int kCombineThreads = 128;
+
+template <int DT>
+__global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs A) {
+  constexpr int ES = Row8<DT>::ES;
+  const int64_t t = blockIdx.x / A.chunks;
+  const int64_t c0 = ((int64_t)(blockIdx.x % A.chunks) * kCombineThreads + threadIdx.x) * 8;
+  const int64_t left = A.cols - c0;
+  const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+  for (int j0 = 0; j0 < A.k; j0 += 4) {
+    uint32_t w[4][Row8<DT>::NW];
+    int r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      r[u] = j0 + u < A.k ? slot_row(A.rows, t * A.k + j0 + u, A.in_rows) : -1;
+      if (r[u] >= 0) load8<DT>(w[u], A.h + ((int64_t)r[u] * A.cols + c0) * ES, n);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (r[u] < 0) continue;
+      const float wt = slot_weight(A.weights, t * A.k + j0 + u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += wt * elem<DT>(w[u], j);
+    }
+  }
+  if (n == 0) return;
+  if (A.residual) {
+    uint32_t w[Row8<DT>::NW];
+    load8<DT>(w, A.residual + (t * A.cols + c0) * ES, n);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] += elem<DT>(w, j);
+  }
+  uint32_t o[Row8<DT>::NW];
+  pack8<DT>(o, acc);
+  store8<DT>(A.y + (t * A.cols + c0) * ES, o, n);
+}
+
+// ---- combine backward ------------------------------------------------------------
+//
+// A workgroup takes one token: its gradient row once, 8 elements a lane and
+// 2048 a pass, and up to 8 of its rows at a time: grad_h = w * dy leaves as it
+// is formed, and the dot products of dy with the rows stay in registers until
+// the end of the row, where the waves' sums meet in LDS.  Bound by the bytes.
+
+struct CombineBwdArgs {
+  const uint8_t *gy, *h;
+  const int32_t *rows;
+  const float *weights;
+  uint8_t *gh;
+  float *gw;
+  int64_t cols, in_rows;
+  int k;
+};
+
+constexpr int kCombineBwdThreads = 256;
+
+template <int DT>
+__global__ __launch_bounds__(kCombineBwdThreads) void combine_bwd_kernel(CombineBwdArgs A) {
+  constexpr int ES = Row8<DT>::ES, KB = 8;
+  __shared__ float part[kCombineBwdThreads / 64][KB];
+  const int64_t t = blockIdx.x;
+  const int lane = (int)__lane_id(), wave = threadIdx.x >> 6;
+  for (int j0 = 0; j0 < A.k; j0 += KB) {
+    float dot[KB];
+#pragma unroll
+    for (int u = 0; u < KB; ++u) dot[u] = 0.0f;
+    for (int64_t c0 = (int64_t)threadIdx.x * 8; c0 < A.cols; c0 += kCombineBwdThreads * 8) {
+      const int n = A.cols - c0 >= 8 ? 8 : (int)(A.cols - c0);
+      uint32_t wy[Row8<DT>::NW];
+      load8<DT>(wy, A.gy + (t * A.cols + c0) * ES, n);
+#pragma unroll
+      for (int u = 0; u < KB; ++u) {
+        if (j0 + u >= A.k) break;
+        const int64_t r = slot_row(A.rows, t * A.k + j0 + u, A.in_rows);
+        if (r < 0) continue;
+        const int64_t at = (r * A.cols + c0) * ES;
+        if (A.gw) {
+          uint32_t wh[Row8<DT>::NW];
+          load8<DT>(wh, A.h + at, n);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dot[u] += elem<DT>(wy, j) * elem<DT>(wh, j);
+        }
+        if (A.gh) {
+          const float wt = slot_weight(A.weights, t * A.k + j0 + u);
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = wt * elem<DT>(wy, j);
+          uint32_t o[Row8<DT>::NW];
+          pack8<DT>(o, f);
+          store8<DT>(A.gh + at, o, n);
+        }
+      }
+    }
+    if (!A.gw) continue;  // the same for the whole launch
+#pragma unroll
+    for (int u = 0; u < KB; ++u) {
+      float s = dot[u];
+      for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+      if (lane == 0) part[wave][u] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x < KB && j0 + (int)threadIdx.x < A.k) {
+      float s = 0.0f;
+      for (int w = 0; w < kCombineBwdThreads / 64; ++w) s += part[w][threadIdx.x];
+      A.gw[t * A.k + j0 + threadIdx.x] = s;
+    }
+    __syncthreads();
+  }
+}
+
+template <int DT, int FMT>
+hipError_t dispatch_one(const DispatchArgs &a, int block, int64_t grid, hipStream_t st) {
+  if (block == 128)
+    hipLaunchKernelGGL((dispatch_kernel<DT, FMT, 16>), dim3((unsigned)grid), dim3(kDispatchThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((dispatch_kernel<DT, FMT, 4>), dim3((unsigned)grid), dim3(kDispatchThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t plan_workspace(int64_t slots, int experts) {
+  const int64_t c = plan_chunk(slots), n = (slots + c - 1) / c;
+  return n > 1 ? n * experts : 0;
+}
+
+hipError_t launch_plan(const PlanLaunch &L, hipStream_t st) {
+  PlanArgs a{};
+  a.ids = L.ids;
+  a.group_list = L.group_list;
+  a.rows = L.rows;
+  a.hist = L.workspace;
+  a.slots = L.slots;
+  a.chunk = plan_chunk(L.slots);
+  a.experts = L.experts;
+  while ((1 << a.bits) <= L.experts) ++a.bits;  // numbers 0 .. experts
+  a.chunks = L.slots > 0 ? (int)((L.slots + a.chunk - 1) / a.chunk) : 1;
+  if (a.chunks > 1) {
+    hipLaunchKernelGGL(plan_count_kernel, dim3(a.chunks), dim3(kPlanThreads), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(plan_kernel, dim3(a.chunks), dim3(kPlanThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch(const DispatchLaunch &L, hipStream_t st) {
+  DispatchArgs a{};
+  a.x = static_cast<const uint8_t *>(L.x);
+  a.rows = L.rows;
+  a.y = static_cast<uint8_t *>(L.y);
+  a.q = L.q;
+  a.scales = L.scales;
+  a.cols = L.cols;
+  a.nb = (L.cols + L.block - 1) / L.block;
+  a.out_rows = L.out_rows;
+  a.k = L.k;
+  const int64_t chunks = (L.cols + 8 * kDispatchThreads - 1) / (8 * kDispatchThreads);
+  const int64_t grid = chunks * L.tokens;
+  if (chunks > 0x7FFFFFFF || grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  a.chunks = (int)chunks;
+  if (L.dtype == kBF16)
+    return L.fmt == kE4M3 ? dispatch_one<kBF16, kE4M3>(a, L.block, grid, st) : dispatch_one<kBF16, kE5M2>(a, L.block, grid, st);
+  return L.fmt == kE4M3 ? dispatch_one<kF32, kE4M3>(a, L.block, grid, st) : dispatch_one<kF32, kE5M2>(a, L.block, grid, st);
+}
+
+hipError_t launch_combine(const CombineLaunch &L, hipStream_t st) {
+  CombineArgs a{};
+  a.h = static_cast<const uint8_t *>(L.h);
+  a.rows = L.rows;
+  a.weights = L.weights;
+  a.residual = static_cast<const uint8_t *>(L.residual);
+  a.y = static_cast<uint8_t *>(L.y);
+  a.cols = L.cols;
+  a.in_rows = L.in_rows;
+  a.k = L.k;
+  const int64_t chunks = (L.cols + 8 * kCombineThreads - 1) / (8 * kCombineThreads);
+  const int64_t grid = chunks * L.tokens;
+  if (chunks > 0x7FFFFFFF || grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  a.chunks = (int)chunks;
+  if (L.dtype == kBF16) hipLaunchKernelGGL((combine_kernel<kBF16>), dim3((unsigned)grid), dim3(kCombineThreads), 0, st, a);
+  else hipLaunchKernelGGL((combine_kernel<kF32>), dim3((unsigned)grid), dim3(kCombineThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_bwd(const CombineBwdLaunch &L, hipStream_t st) {
+  CombineBwdArgs a{};
+  a.gy = static_cast<const uint8_t *>(L.grad_y);
+  a.h = static_cast<const uint8_t *>(L.h);
+  a.rows = L.rows;
+  a.weights = L.weights;
+  a.gh = static_cast<uint8_t *>(L.grad_h);
+  a.gw = L.grad_weights;
+  a.cols = L.cols;
+  a.in_rows = L.in_rows;
+  a.k = L.k;
+  if (L.tokens > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (L.dtype == kBF16) hipLaunchKernelGGL((combine_bwd_kernel<kBF16>), dim3((unsigned)L.tokens), dim3(kCombineBwdThreads), 0, st, a);
+  else hipLaunchKernelGGL((combine_bwd_kernel<kF32>), dim3((unsigned)L.tokens), dim3(kCombineBwdThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace mxfp4
