@@ -482,6 +482,59 @@ mxfp4_status_t mxfp4_moe_combine_bwd(int32_t dtype, int64_t tokens, int64_t cols
                                      const int32_t *rows, const float *weights, void *grad_h,
                                      float *grad_weights, void *stream);
 
+/* ---- the grouped product with bias, activation and residual ----------------- */
+
+/* activations; the gated forms act(gate) * up */
+enum { MXACT_NONE = 0, MXACT_RELU = 1, MXACT_SILU = 2, MXACT_GELU = 3, MXACT_SWIGLU = 6, MXACT_GEGLU = 7 };
+
+typedef struct mxfp4_epilogue {
+  int32_t act;           /* MXACT_...                                            */
+  int32_t reserved;      /* must be 0                                            */
+  const float *bias;     /* fp32, one value per row of B, or NULL                */
+  int64_t bias_stride;   /* elements from group g's bias to group g+1's (0: one) */
+  const void *residual;  /* [M, ld_residual] of the output type, or NULL         */
+  int64_t ld_residual;   /* elements                                             */
+  void *z;               /* [M, ld_z] of the output type, or NULL: the products
+                            before the activation, for the backward pass         */
+  int64_t ld_z;          /* elements                                             */
+} mxfp4_epilogue_t;
+
+/*
+ * mxfp4_grouped_matmul with MXGEMM_GROUP_ROWS and an epilogue in the same pass:
+ *     z = A B_g^T + bias_g,   c = act(z) + residual              (B_g [N, K])
+ *     gated: B_g [2 N, K] holds the N gate rows, then the N up rows;
+ *     z = (gate, up) [M, 2 N],   c = act(gate) * up + residual.
+ * silu(x) = x / (1 + exp(-x)); gelu(x) = x Phi(x) with the normal distribution
+ * function Phi.  Products and epilogue in fp32; c and z are rounded once, each
+ * from the fp32 value (act sees the unrounded z).  Operands, group_list and
+ * rows past the groups' total (not written) as in mxfp4_grouped_matmul; b->fmt
+ * E2M1 or E4M3.  c, z and residual aligned to one element, at any row length;
+ * c may be the residual.  Few rows per group take kernels of their own.
+ */
+mxfp4_status_t mxfp4_grouped_matmul_act(int64_t M, int64_t N, int64_t K, const mxfp4_mx_operand_t *a,
+                                        const mxfp4_mx_operand_t *b, const int64_t *group_list,
+                                        int32_t num_groups, int32_t group_list_type,
+                                        const mxfp4_epilogue_t *ep, int32_t out_dtype, void *c,
+                                        int64_t ldc, void *stream);
+
+/*
+ * Backward of that epilogue: from grad_c [rows, cols] and z (as it was written;
+ * [rows, cols], gated [rows, 2 cols]), grad_z of z's shape, and grad_bias fp32
+ * [num_groups, columns of z] (NULL: not wanted): the sums of each group's rows
+ * of grad_z before its rounding, 0 for an empty group.  group_list NULL: one
+ * group of all rows; rows past the groups' total are not written.  The
+ * residual's gradient is grad_c itself; grad_z goes on into the quantizers and
+ * the products of the backward pass.  workspace (grad_bias only):
+ * mxfp4_act_bwd_workspace bytes (num_groups 0 without a group_list; -1 for
+ * refused arguments), in use until the call's kernels are done.  Contiguous
+ * rows; without a gate grad_z may be grad_c or z.
+ */
+int64_t mxfp4_act_bwd_workspace(int32_t act, int64_t rows, int64_t cols, int32_t num_groups);
+mxfp4_status_t mxfp4_act_bwd(int32_t dtype, int32_t act, int64_t rows, int64_t cols, const void *grad_c,
+                             const void *z, void *grad_z, float *grad_bias, const int64_t *group_list,
+                             int32_t num_groups, int32_t group_list_type, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+
 /* Message for the calling thread's most recent failed call ("" if none). */
 const char *mxfp4_last_error(void);
 

@@ -23,7 +23,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 SOURCES = ["api.hip", "row_kernels.hip", "col_kernels.hip", "ste_kernels.hip",
            "kmajor_kernels.hip", "mxfp8_kernels.hip", "mxgemm_kernels.hip",
-           "api_moe.hip", "moe_route_kernels.hip", "moe_rows_kernels.hip"]
+           "api_moe.hip", "moe_route_kernels.hip", "moe_rows_kernels.hip",
+           "mxgemm_act_kernels.hip", "mxgemm_gated_kernels.hip", "mxgemm_rows_kernels.hip", "act_bwd_kernels.hip"]
 CFLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 

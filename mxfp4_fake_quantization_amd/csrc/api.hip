@@ -260,41 +260,6 @@ mxfp4_status_t mxfp8_quant(const mxfp4_desc_t *desc, int32_t fmt, const void *x,
   return hip_status(mxfp4::launch_mxfp8_rows(L, static_cast<hipStream_t>(stream)), "MXFP8 launch");
 }
 
-}  // extern "C"
-
-namespace {
-
-mxfp4_status_t check_operand(const mxfp4_mx_operand_t *o, const char *what, bool rows_split, int64_t K,
-                             int64_t k_blocks, bool is_a) {
-  if (!o) return fail(MXFP4_EINVAL, "%s is NULL", what);
-  if (is_a ? (o->fmt != MXGEMM_E4M3 && o->fmt != MXGEMM_E5M2)
-           : (o->fmt != MXGEMM_E4M3 && o->fmt != MXGEMM_E5M2 && o->fmt != MXGEMM_E2M1))
-    return fail(MXFP4_EUNSUPPORTED, "%s->fmt %d is not supported", what, o->fmt);
-  if (o->block != 32 && o->block != 128)
-    return fail(MXFP4_EUNSUPPORTED, "%s->block %d is not 32 or 128", what, o->block);
-  if (!rows_split && o->block != 32)
-    return fail(MXFP4_EUNSUPPORTED, "%s->block must be 32 when groups split K", what);
-  MXFP4_TRY(check_ptr(o->data, 16, what));
-  if (!o->scales) return fail(MXFP4_EINVAL, "%s->scales is NULL", what);
-  const int64_t kel = rows_split ? K : k_blocks * 32;  // K extent of a row
-  const int64_t row_bytes = o->fmt == MXGEMM_E2M1 ? kel / 2 : kel;
-  const int64_t nblk = (kel + o->block - 1) / o->block;
-  if (o->ld % 16 != 0 || o->ld < row_bytes)
-    return fail(MXFP4_EINVAL, "%s->ld %lld must be a multiple of 16 and >= %lld", what, (long long)o->ld,
-                (long long)row_bytes);
-  if (o->ld > (int64_t)1 << 24) return fail(MXFP4_EUNSUPPORTED, "%s->ld is above 2^24 bytes", what);
-  if (o->ld_scales < nblk || o->ld_scales > (int64_t)1 << 24)
-    return fail(MXFP4_EINVAL, "%s->ld_scales %lld must be >= %lld (and below 2^24)", what,
-                (long long)o->ld_scales, (long long)nblk);
-  if (o->group_stride < 0 || o->group_stride_scales < 0 || o->group_stride % 16 != 0)
-    return fail(MXFP4_EINVAL, "%s group strides must be >= 0 (data: a multiple of 16)", what);
-  return MXFP4_OK;
-}
-
-}  // namespace
-
-extern "C" {
-
 mxfp4_status_t mxfp4_grouped_matmul(int32_t group_type, int64_t M, int64_t N, int64_t K,
                                     const mxfp4_mx_operand_t *a, const mxfp4_mx_operand_t *b,
                                     const int64_t *group_list, int32_t num_groups,

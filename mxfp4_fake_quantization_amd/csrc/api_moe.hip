@@ -5,6 +5,7 @@
 #include "api_common.h"
 #include "moe_kernels.h"
 #include "mxfp4_kernels.h"
+#include "mxgemm_act.h"
 
 using namespace mxfp4_api;
 
@@ -16,9 +17,25 @@ mxfp4_status_t check_dtype(int32_t dtype) {
   return MXFP4_OK;
 }
 
+// Outputs apart from each other and from every input (NULL entries are
+// skipped); inputs may share memory.
+bool apart(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
+  if (!distinct(outs)) return false;
+  for (const void *o : outs)
+    for (const void *i : ins)
+      if (o && o == i) return false;
+  return true;
+}
+
 // Pointers of elements: aligned to one element.
 mxfp4_status_t check_elems(const void *p, int32_t dtype, const char *what) {
   return check_ptr(p, dtype == MXFP4_F32 ? 4 : 2, what);
+}
+
+mxfp4_status_t check_act(int32_t act) {
+  if ((act < MXACT_NONE || act > MXACT_GELU) && act != MXACT_SWIGLU && act != MXACT_GEGLU)
+    return fail(MXFP4_EUNSUPPORTED, "act %d is not one of the MXACT_ activations", act);
+  return MXFP4_OK;
 }
 
 mxfp4_status_t check_route(const mxfp4_moe_route_t *d) {
@@ -71,7 +88,7 @@ mxfp4_status_t mxfp4_moe_route(const mxfp4_moe_route_t *desc, const void *logits
   MXFP4_TRY(check_opt(bias, 4, "bias"));
   MXFP4_TRY(check_ptr(weights, 4, "weights"));
   MXFP4_TRY(check_ptr(ids, 4, "ids"));
-  if (!distinct({logits, bias, weights, ids})) return fail(MXFP4_EINVAL, "outputs alias each other or an input");
+  if (!apart({weights, ids}, {logits, bias})) return fail(MXFP4_EINVAL, "outputs alias each other or an input");
   mxfp4::RouteLaunch L{desc->dtype, desc->score, desc->renormalize, desc->tokens, desc->experts, desc->k,
                        desc->num_groups, desc->topk_groups, desc->scale, logits, bias, weights, ids};
   return hip_status(mxfp4::launch_route(L, static_cast<hipStream_t>(stream)), "routing launch");
@@ -85,7 +102,7 @@ mxfp4_status_t mxfp4_moe_route_bwd(const mxfp4_moe_route_t *desc, const float *g
   MXFP4_TRY(check_elems(logits, desc->dtype, "logits"));
   MXFP4_TRY(check_ptr(ids, 4, "ids"));
   MXFP4_TRY(check_elems(grad_logits, desc->dtype, "grad_logits"));
-  if (!distinct({grad_weights, logits, ids, grad_logits})) return fail(MXFP4_EINVAL, "grad_logits aliases an input");
+  if (!apart({grad_logits}, {grad_weights, logits, ids})) return fail(MXFP4_EINVAL, "grad_logits aliases an input");
   mxfp4::RouteBwdLaunch L{desc->dtype, desc->score, desc->renormalize, desc->tokens, desc->experts, desc->k,
                           desc->scale, grad_weights, logits, ids, grad_logits};
   return hip_status(mxfp4::launch_route_bwd(L, static_cast<hipStream_t>(stream)), "routing backward launch");
@@ -114,7 +131,7 @@ mxfp4_status_t mxfp4_moe_plan(int64_t slots, int32_t experts, const int32_t *ids
       return fail(MXFP4_EINVAL, "workspace holds %lld bytes; the call needs %lld", (long long)workspace_bytes,
                   (long long)need);
   }
-  if (!distinct({ids, group_list, rows, need > 0 ? workspace : nullptr}))
+  if (!apart({group_list, rows, need > 0 ? workspace : nullptr}, {ids}))
     return fail(MXFP4_EINVAL, "outputs alias each other or ids");
   mxfp4::PlanLaunch L{slots, experts, ids, group_list, rows, static_cast<int32_t *>(workspace)};
   return hip_status(mxfp4::launch_plan(L, static_cast<hipStream_t>(stream)), "plan launch");
@@ -133,7 +150,7 @@ mxfp4_status_t mxfp4_moe_dispatch(const mxfp4_desc_t *desc, int32_t fmt, const v
   MXFP4_TRY(check_elems(x, desc->dtype, "x"));
   MXFP4_TRY(check_ptr(rows, 4, "rows"));
   if (y) MXFP4_TRY(check_elems(y, desc->dtype, "y"));
-  if (!distinct({x, rows, y, q, scales})) return fail(MXFP4_EINVAL, "outputs alias each other or an input");
+  if (!apart({y, q, scales}, {x, rows})) return fail(MXFP4_EINVAL, "outputs alias each other or an input");
   mxfp4::DispatchLaunch L{desc->dtype, fmt, desc->block, desc->rows, desc->cols, out_rows, k, x, rows, y, q, scales};
   return hip_status(mxfp4::launch_dispatch(L, static_cast<hipStream_t>(stream)), "dispatch launch");
 }
@@ -150,7 +167,7 @@ mxfp4_status_t mxfp4_moe_combine(int32_t dtype, int64_t tokens, int64_t cols, in
   if (residual) MXFP4_TRY(check_elems(residual, dtype, "residual"));
   MXFP4_TRY(check_elems(y, dtype, "y"));
   // y may be the residual (the token's row is read before it is written)
-  if (!distinct({h, rows, weights, residual == y ? nullptr : residual, y}))
+  if (!apart({y}, {h, rows, weights, residual == y ? nullptr : residual}))
     return fail(MXFP4_EINVAL, "y aliases an input");
   mxfp4::CombineLaunch L{dtype, tokens, cols, in_rows, k, h, rows, weights, residual, y};
   return hip_status(mxfp4::launch_combine(L, static_cast<hipStream_t>(stream)), "combine launch");
@@ -170,10 +187,121 @@ mxfp4_status_t mxfp4_moe_combine_bwd(int32_t dtype, int64_t tokens, int64_t cols
   MXFP4_TRY(check_opt(weights, 4, "weights"));
   if (grad_h && in_rows > 0 && !empty) MXFP4_TRY(check_elems(grad_h, dtype, "grad_h"));
   MXFP4_TRY(check_opt(grad_weights, 4, "grad_weights"));
-  if (!distinct({grad_y, grad_weights ? h : nullptr, rows, weights, grad_h, grad_weights}))
+  if (!apart({grad_h, grad_weights}, {grad_y, grad_weights ? h : nullptr, rows, weights}))
     return fail(MXFP4_EINVAL, "outputs alias each other or an input");
   mxfp4::CombineBwdLaunch L{dtype, tokens, cols, in_rows, k, grad_y, h, rows, weights, grad_h, grad_weights};
   return hip_status(mxfp4::launch_combine_bwd(L, static_cast<hipStream_t>(stream)), "combine backward launch");
+}
+
+mxfp4_status_t mxfp4_grouped_matmul_act(int64_t M, int64_t N, int64_t K, const mxfp4_mx_operand_t *a,
+                                        const mxfp4_mx_operand_t *b, const int64_t *group_list, int32_t num_groups,
+                                        int32_t group_list_type, const mxfp4_epilogue_t *ep, int32_t out_dtype, void *c,
+                                        int64_t ldc, void *stream) {
+  if (M < 0 || N < 0 || K < 0) return fail(MXFP4_EINVAL, "negative shape");
+  if (K % 32 != 0) return fail(MXFP4_EINVAL, "K %lld is not a multiple of 32", (long long)K);
+  if (group_list && (num_groups < 1 || (group_list_type != 0 && group_list_type != 1)))
+    return fail(MXFP4_EINVAL, "num_groups must be >= 1 and group_list_type 0 or 1");
+  if (!ep) return fail(MXFP4_EINVAL, "epilogue is NULL");
+  MXFP4_TRY(check_act(ep->act));
+  if (ep->reserved != 0) return fail(MXFP4_EINVAL, "reserved fields must be 0");
+  if (out_dtype != MXGEMM_OUT_BF16 && out_dtype != MXGEMM_OUT_F32)
+    return fail(MXFP4_EUNSUPPORTED, "out_dtype %d is not MXGEMM_OUT_BF16 or MXGEMM_OUT_F32", out_dtype);
+  const bool gated = ep->act & 4;
+  const int32_t dtype = out_dtype == MXGEMM_OUT_F32 ? MXFP4_F32 : MXFP4_BF16;
+  if (M == 0 || N == 0) return ok();
+  if (K == 0) return fail(MXFP4_EUNSUPPORTED, "K must be > 0");
+  MXFP4_TRY(check_opt(group_list, 8, "group_list"));
+  MXFP4_TRY(check_operand(a, "a", true, K, 0, true));
+  MXFP4_TRY(check_operand(b, "b", true, K, 0, false));
+  if (b->fmt == MXGEMM_E5M2) return fail(MXFP4_EUNSUPPORTED, "b->fmt must be MXGEMM_E2M1 or MXGEMM_E4M3");
+  // gated: the up rows are reached by 32-bit offsets from the gate rows
+  if (gated && (N > (1 << 24) || (N + 256) * (b->ld > b->ld_scales ? b->ld : b->ld_scales) >= (int64_t)1 << 32))
+    return fail(MXFP4_EUNSUPPORTED, "the gate half of b (N * ld) must stay below 2^32 bytes");
+  MXFP4_TRY(check_elems(c, dtype, "c"));
+  if (ldc < N) return fail(MXFP4_EINVAL, "ldc %lld < N %lld", (long long)ldc, (long long)N);
+  MXFP4_TRY(check_opt(ep->bias, 4, "bias"));
+  if (ep->bias_stride < 0) return fail(MXFP4_EINVAL, "bias_stride must be >= 0");
+  if (ep->residual) {
+    MXFP4_TRY(check_elems(ep->residual, dtype, "residual"));
+    if (ep->ld_residual < N) return fail(MXFP4_EINVAL, "ld_residual %lld < N %lld", (long long)ep->ld_residual, (long long)N);
+    if (ep->residual == c && ep->ld_residual != ldc) return fail(MXFP4_EINVAL, "c over the residual needs the same ld");
+  }
+  if (ep->z) {
+    MXFP4_TRY(check_elems(ep->z, dtype, "z"));
+    if (ep->ld_z < (gated ? 2 : 1) * N)
+      return fail(MXFP4_EINVAL, "ld_z %lld is below the %lld columns of z", (long long)ep->ld_z, (long long)((gated ? 2 : 1) * N));
+  }
+  if (!apart({c, ep->z}, {a->data, a->scales, b->data, b->scales, group_list, ep->bias,
+                          ep->residual == c ? nullptr : ep->residual}))
+    return fail(MXFP4_EINVAL, "an output aliases an input or another output");
+  mxfp4::GemmLaunch L{};
+  L.a_fmt = a->fmt;
+  L.b_fmt = b->fmt;
+  L.a_block = a->block;
+  L.b_block = b->block;
+  L.out_f32 = out_dtype == MXGEMM_OUT_F32;
+  L.M = M;
+  L.N = N;
+  L.K = K;
+  L.a = static_cast<const uint8_t *>(a->data);
+  L.as = a->scales;
+  L.b = static_cast<const uint8_t *>(b->data);
+  L.bs = b->scales;
+  L.lda = a->ld;
+  L.ldas = a->ld_scales;
+  L.ldb = b->ld;
+  L.ldbs = b->ld_scales;
+  L.b_gs = b->group_stride;
+  L.b_gss = b->group_stride_scales;
+  L.ldc = ldc;
+  L.c = c;
+  L.group_list = group_list;
+  L.num_groups = group_list ? num_groups : 1;
+  L.list_type = group_list_type;
+  const mxfp4::ActArgs e{ep->bias, ep->bias_stride, ep->residual, ep->ld_residual, ep->z, ep->ld_z, ep->act & 3};
+  return hip_status(mxfp4::launch_gemm_act(L, e, gated, static_cast<hipStream_t>(stream)), "grouped matmul launch");
+}
+
+int64_t mxfp4_act_bwd_workspace(int32_t act, int64_t rows, int64_t cols, int32_t num_groups) {
+  if (check_act(act) != MXFP4_OK || rows < 0 || cols < 0 || num_groups < 0) return -1;
+  const int64_t zc = cols * (act & 4 ? 2 : 1);
+  if (zc > 0 && rows / 32 + num_groups + 2 > INT64_MAX / 8 / zc) return -1;
+  return 4 * mxfp4::act_bwd_workspace(rows, zc, num_groups);
+}
+
+mxfp4_status_t mxfp4_act_bwd(int32_t dtype, int32_t act, int64_t rows, int64_t cols, const void *grad_c, const void *z,
+                             void *grad_z, float *grad_bias, const int64_t *group_list, int32_t num_groups,
+                             int32_t group_list_type, void *workspace, int64_t workspace_bytes, void *stream) {
+  MXFP4_TRY(check_dtype(dtype));
+  MXFP4_TRY(check_act(act));
+  if (rows < 0 || cols < 0) return fail(MXFP4_EINVAL, "negative shape %lld x %lld", (long long)rows, (long long)cols);
+  if (cols > 0 && rows > INT64_MAX / 16 / cols) return fail(MXFP4_EINVAL, "rows * cols overflows");
+  if (group_list && (num_groups < 1 || (group_list_type != 0 && group_list_type != 1)))
+    return fail(MXFP4_EINVAL, "num_groups must be >= 1 and group_list_type 0 or 1");
+  MXFP4_TRY(check_opt(group_list, 8, "group_list"));
+  if (cols == 0 || (rows == 0 && !grad_bias)) return ok();
+  if (rows > 0) {
+    MXFP4_TRY(check_elems(grad_c, dtype, "grad_c"));
+    MXFP4_TRY(check_elems(z, dtype, "z"));
+    MXFP4_TRY(check_elems(grad_z, dtype, "grad_z"));
+  }
+  const int32_t groups = group_list ? num_groups : 0;
+  if (grad_bias) {
+    MXFP4_TRY(check_ptr(grad_bias, 4, "grad_bias"));
+    const int64_t need = mxfp4_act_bwd_workspace(act, rows, cols, groups);
+    if (need > 0) MXFP4_TRY(check_ptr(workspace, 4, "workspace"));
+    if (workspace_bytes < need)
+      return fail(MXFP4_EINVAL, "workspace holds %lld bytes; the call needs %lld", (long long)workspace_bytes,
+                  (long long)need);
+  }
+  // plain activations: grad_z may be grad_c or z (an element is read before it is written)
+  const bool in_place = !(act & 4);
+  if (!apart({grad_z, grad_bias, grad_bias ? workspace : nullptr},
+             {in_place && grad_z == grad_c ? nullptr : grad_c, in_place && grad_z == z ? nullptr : z, group_list}))
+    return fail(MXFP4_EINVAL, "an output aliases an input or another output");
+  mxfp4::ActBwdLaunch L{dtype, act, rows, cols, grad_c, z, grad_z, grad_bias, group_list, groups, group_list_type,
+                        static_cast<float *>(workspace)};
+  return hip_status(mxfp4::launch_act_bwd(L, static_cast<hipStream_t>(stream)), "activation backward launch");
 }
 
 }  // extern "C"

@@ -83,4 +83,26 @@ struct CombineBwdLaunch {
 };
 hipError_t launch_combine_bwd(const CombineBwdLaunch &L, hipStream_t stream);
 
+// The grouped MX product (rows-split groups) with its epilogue; act: kind
+// (0 none, 1 relu, 2 silu, 3 gelu) + 4 for the gated form, in which B has 2 N rows.
+struct GemmLaunch;
+struct ActArgs;
+hipError_t launch_act_tiles(const GemmLaunch &L, const ActArgs &e, hipStream_t stream);
+hipError_t launch_gated_tiles(const GemmLaunch &L, const ActArgs &e, hipStream_t stream);
+hipError_t launch_gemm_act(const GemmLaunch &L, const ActArgs &e, bool gated, hipStream_t stream);
+
+// Backward of the epilogue: grad_z = grad_c * act'(z), and its column sums per group.
+struct ActBwdLaunch {
+  int dtype, act;
+  int64_t rows, cols;     // cols: of grad_c; z and grad_z have twice as many when gated
+  const void *grad_c, *z;
+  void *grad_z;
+  float *grad_bias;       // [groups, columns of z] or NULL
+  const int64_t *group_list;
+  int num_groups, list_type;
+  float *workspace;       // act_bwd_workspace floats when grad_bias is given
+};
+int64_t act_bwd_workspace(int64_t rows, int64_t zcols, int num_groups);
+hipError_t launch_act_bwd(const ActBwdLaunch &L, hipStream_t stream);
+
 }  // namespace mxfp4

@@ -18,6 +18,7 @@
 // Bound by the VALU work of the k steps, not by the logits' bytes.
 #include "moe_kernels.h"
 #include "mxfp4_device.h"
+#include "mxfp4_rows8.h"
 
 namespace mxfp4 {
 namespace {
@@ -73,12 +74,6 @@ template <int DT>
 __device__ __forceinline__ float load_one(const uint8_t *p, int64_t i) {
   if (DT == kBF16) return bits_f32((uint32_t)reinterpret_cast<const uint16_t *>(p)[i] << 16);
   return reinterpret_cast<const float *>(p)[i];
-}
-
-__device__ __forceinline__ uint32_t bf16_rne(float f) {
-  uint32_t u = fbits(f);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
 // V consecutive elements from element `at`; those past cnt read as -inf.
@@ -339,7 +334,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(RouteBwdArgs A
       words w;
 #pragma unroll
       for (int j = 0; j < P::PW; ++j)
-        w[j] = DT == kBF16 ? bf16_rne(o[(q * P::PE + 2 * j) % V]) | (bf16_rne(o[(q * P::PE + 2 * j + 1) % V]) << 16)
+        w[j] = DT == kBF16 ? f32_to_bf16_rne(o[(q * P::PE + 2 * j) % V]) |
+                                ((uint32_t)f32_to_bf16_rne(o[(q * P::PE + 2 * j + 1) % V]) << 16)
                            : fbits(o[(q * P::PE + j) % V]);
       *reinterpret_cast<words *>(A.gl + (row + e0 + q * P::PE) * P::ES) = w;
     }
@@ -347,7 +343,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(RouteBwdArgs A
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (j >= cnt) break;
-      if (DT == kBF16) reinterpret_cast<uint16_t *>(A.gl)[row + e0 + j] = (uint16_t)bf16_rne(o[j]);
+      if (DT == kBF16) reinterpret_cast<uint16_t *>(A.gl)[row + e0 + j] = f32_to_bf16_rne(o[j]);
       else reinterpret_cast<float *>(A.gl)[row + e0 + j] = o[j];
     }
   }

@@ -1,0 +1,211 @@
+// mxgemm_act.h -- activations, and the epilogue of the grouped MX product:
+// bias, pre-activation output, activation (gated or not), residual.
+#pragma once
+
+#include "mxfp4_rows8.h"
+
+namespace mxfp4 {
+
+enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+
+// Arguments of the epilogue; res and z are of the output's type.
+struct ActArgs {
+  const float *bias;  // [groups, columns of B] or NULL
+  int64_t bias_gs;    // elements between groups (0: one row for all)
+  const void *res;    // [M, ldr] or NULL
+  int64_t ldr;
+  void *z;            // [M, ldz]: A B^T + bias, or NULL
+  int64_t ldz;
+  int act;
+};
+
+// 1 / (1 + exp(-x)) on the hardware 2^x and reciprocal (1 ulp each): the
+// product with log2 e rounds the exponent, a relative error of |x| 2^-24.
+__device__ __forceinline__ float sigmoid_f(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * x));
+}
+
+// Phi(x) of the normal distribution, and exp(-x^2 / 2): the polynomial in
+// 1 / (1 + p |x| / sqrt 2) of Abramowitz and Stegun 7.1.26 times that
+// exponential, within 1.5e-7 / 2 of Phi everywhere, without a branch.
+__device__ __forceinline__ float normal_cdf(float x, float *gauss) {
+  const float a = fabsf(x) * 0.707106781f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, a, 1.0f));
+  const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                           0.254829592f);
+  *gauss = __builtin_amdgcn_exp2f(-1.44269504f * (a * a));
+  const float tail = 0.5f * p * *gauss;
+  return x > 0.0f ? 1.0f - tail : tail;
+}
+
+// Act(x): x, max(x, 0), x sigmoid(x), x Phi(x).
+template <int ACT>
+__device__ __forceinline__ float act_value(float x) {
+  float gauss;
+  if (ACT == kActRelu) return x < 0.0f ? 0.0f : x;
+  if (ACT == kActSilu) return x * sigmoid_f(x);
+  if (ACT == kActGelu) return x * normal_cdf(x, &gauss);
+  return x;
+}
+
+// Calls f with the activation as a compile-time number.
+template <int V>
+struct ActT {
+  static constexpr int value = V;
+};
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {  // the same for the whole launch
+    case kActRelu: f(ActT<kActRelu>{}); break;
+    case kActSilu: f(ActT<kActSilu>{}); break;
+    case kActGelu: f(ActT<kActGelu>{}); break;
+    default: f(ActT<kActNone>{}); break;
+  }
+}
+
+// The accumulators of a tile of mxgemm_tile.h (row 8(v/4) + 4h + v%4, column
+// l32 of each 32 x 32) to the outputs.  bf16 outputs are staged in LDS, the
+// first half of the rows in the A buffers, the second in the B buffers, and
+// leave in 16-byte row pieces (any alignment of elements); the residual comes
+// in through the same places, so that its sum with the activation is rounded
+// once.  fp32 outputs are written as they lie, 128 bytes a half-wave.
+template <int EPI, int BM, int BN, int NT, int WM, int WN, int RS, typename ACC>
+__device__ __forceinline__ void act_epilogue(void *c, int64_t ldc, int out_f32, const ActArgs &E, ACC &acc,
+                                             uint8_t *bufa, uint8_t *bufb, int64_t m0, int64_t mlen, int64_t n0,
+                                             int64_t nlen, int64_t N, int g, int wr0, int wc0, int lane, int tid) {
+  constexpr bool GATED = EPI == 2;
+  constexpr int H = GATED ? WN / 2 : WN;          // MFMA tiles of output columns
+  constexpr int BNO = GATED ? BN / 2 : BN;
+  typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+  const int h = lane >> 5, l32 = lane & 31;
+  const int oc0 = GATED ? wc0 / 2 : wc0;           // the wave's first output column
+
+  // without a bias 0 is added: a branch around it would have to merge the
+  // accumulators' register tuples, which spilled
+  const float *b = E.bias + (E.bias ? (int64_t)g * E.bias_gs + n0 : 0);
+#pragma unroll
+  for (int j = 0; j < WN; ++j) {
+    const int col = oc0 + 32 * (j % H) + l32;
+    const float bj = E.bias && col < nlen ? b[col + (j >= H ? N : 0)] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] += bj;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  constexpr int OS = 2 * BN + 16, HR = BM / 2;
+  static_assert(HR * OS <= 2 * BM * RS && HR * OS <= 2 * BN * RS, "output staging");
+  auto lds_row = [&](int r) { return (r < HR ? bufa : bufb) + (r & (HR - 1)) * OS; };
+  // row of a lane's value v of MFMA tile i, without the wave's and half's part
+  auto tile_row = [&](int i, int v) { return 32 * i + 8 * (v >> 2) + (v & 3); };
+  const int row0 = wr0 + 4 * h;
+  // the lane's places in the stage: a wave's rows lie in one half
+  static_assert(HR % (32 * WM) == 0, "a wave's rows in one half");
+  uint8_t *const mine = (wr0 < HR ? bufa : bufb) + ((wr0 & (HR - 1)) + 4 * h) * OS + 2 * l32;
+
+  // Pieces of 8 columns of the staged rows, W columns wide; f(row, column in
+  // the stage, valid elements).
+  auto pieces = [&](auto width, auto f) {
+    constexpr int W = decltype(width)::value, CH = W / 8, RPI = NT / CH;
+    const int ch = tid % CH;
+#pragma unroll 2  // the accumulators are live
+    for (int k = 0; k < BM / RPI; ++k) {
+      const int row = tid / CH + RPI * k;
+      if (row < mlen) f(row, 8 * ch);
+    }
+  };
+  auto put = [&](void *dst, int64_t ld, int row, int stage_col, int64_t out_col, int left) {
+    if (left <= 0) return;
+    const uint8_t *src = lds_row(row) + 2 * stage_col;
+    uint16_t *d = static_cast<uint16_t *>(dst) + (m0 + row) * ld + out_col;
+    if (left >= 8) {
+      __builtin_nontemporal_store(*reinterpret_cast<const u32x4 *>(src), reinterpret_cast<u32x4_a2 *>(d));
+    } else {
+      for (int e = 0; e < left; ++e) d[e] = reinterpret_cast<const uint16_t *>(src)[e];
+    }
+  };
+
+  if (E.z) {
+    if (!out_f32) {
+      __syncthreads();  // every wave is past its last fragment read
+#pragma unroll
+      for (int i = 0; i < WM; ++i)
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            *reinterpret_cast<uint16_t *>(mine + 2 * wc0 + tile_row(i, v) * OS + 64 * j) = f32_to_bf16_rne(acc[i][j][v]);
+            if ((v & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+          }
+      __syncthreads();
+      pieces(ActT<BN>{}, [&](int row, int sc) {
+        const int q = sc >> 5, j = q % WN;
+        const int col = GATED ? q / WN * (16 * WN) + 32 * (j % H) + (sc & 31) : sc;
+        put(E.z, E.ldz, row, sc, n0 + col + (GATED && j >= H ? N : 0), (int)(nlen - col));
+      });
+    } else {
+#pragma unroll
+      for (int i = 0; i < WM; ++i)
+#pragma unroll
+        for (int j = 0; j < WN; ++j) {
+          const int col = oc0 + 32 * (j % H) + l32;
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int row = row0 + tile_row(i, v);
+            if (row < mlen && col < nlen)
+              static_cast<float *>(E.z)[(m0 + row) * E.ldz + n0 + col + (j >= H ? N : 0)] = acc[i][j][v];
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+    }
+  }
+
+  if (E.res && !out_f32) {
+    __syncthreads();
+    pieces(ActT<BNO>{}, [&](int row, int sc) {
+      const int left = (int)(nlen - sc);
+      if (left <= 0) return;
+      const uint16_t *src = static_cast<const uint16_t *>(E.res) + (m0 + row) * E.ldr + n0 + sc;
+      uint8_t *d = lds_row(row) + 2 * sc;
+      if (left >= 8) {
+        *reinterpret_cast<u32x4 *>(d) = *reinterpret_cast<const u32x4_a2 *>(src);
+      } else {
+        for (int e = 0; e < left; ++e) reinterpret_cast<uint16_t *>(d)[e] = src[e];
+      }
+    });
+  }
+  __syncthreads();
+  with_act(E.act, [&](auto a) {
+    constexpr int ACT = decltype(a)::value;
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        const int col = oc0 + 32 * j + l32;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          float x = act_value<ACT>(acc[i][j][v]);
+          if (GATED) x *= acc[i][(j + H) % WN][v];
+          if (!out_f32) {
+            uint16_t *at = reinterpret_cast<uint16_t *>(mine + 2 * oc0 + tile_row(i, v) * OS + 64 * j);
+            // places past the tile's edge hold what was there before, and are not stored
+            if (E.res) x += bits_f32((uint32_t)*at << 16);
+            *at = f32_to_bf16_rne(x);
+          } else {
+            const int row = row0 + tile_row(i, v);
+            if (row < mlen && col < nlen) {
+              if (E.res) x += static_cast<const float *>(E.res)[(m0 + row) * E.ldr + n0 + col];
+              static_cast<float *>(c)[(m0 + row) * ldc + n0 + col] = x;
+            }
+          }
+          if ((v & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // few temporaries beside the accumulators
+        }
+      }
+  });
+  if (out_f32) return;
+  __syncthreads();
+  pieces(ActT<BNO>{}, [&](int row, int sc) { put(c, ldc, row, sc, n0 + sc, (int)(nlen - sc)); });
+}
+
+}  // namespace mxfp4

@@ -1,0 +1,54 @@
+// mxgemm_act_launch.h -- launches of the tiled product with an epilogue; each
+// epilogue form (EPI of mxgemm_tile.h) is instantiated in a source of its own.
+#pragma once
+
+#include "mxgemm_tile.h"
+
+namespace mxfp4 {
+namespace {
+
+template <int AF, int BF, bool S4, bool SMALL, int EPI>
+__global__ __launch_bounds__((GemmShape<BF, SMALL>::threads), (GemmShape<BF, SMALL>::per_cu)) void mxgemm_act_kernel(
+    GemmArgs P, ActArgs E) {
+  mxgemm_tile<AF, BF, S4, SMALL, EPI>(P, E);
+}
+
+template <int AF, int BF, bool SMALL, int EPI>
+hipError_t act_tiles_one(const GemmArgs &a, const ActArgs &e, int64_t grid, hipStream_t st) {
+  const dim3 block(GemmShape<BF, SMALL>::threads);
+  if (a.s4)
+    hipLaunchKernelGGL((mxgemm_act_kernel<AF, BF, true, SMALL, EPI>), dim3((unsigned)grid), block, 0, st, a, e);
+  else
+    hipLaunchKernelGGL((mxgemm_act_kernel<AF, BF, false, SMALL, EPI>), dim3((unsigned)grid), block, 0, st, a, e);
+  return hipGetLastError();
+}
+
+// The tiles as in the plain product (row split): see gemm_launch.
+template <int AF, int BF, int EPI>
+hipError_t act_tiles(const GemmArgs &a0, const ActArgs &e, hipStream_t st) {
+  GemmArgs a = a0;
+  constexpr int64_t BM = GemmShape<BF>::BM, BNO = GemmShape<BF>::BN / (EPI == 2 ? 2 : 1);
+  a.tiles_n = (a.N + BNO - 1) / BNO;
+  a.tiles_m = (a.M + BM - 1) / BM + (a.gl ? a.G : 0);
+  a.total = a.tiles_m * a.tiles_n;
+  if (a.total > 0x7FFFFFFF) return hipErrorInvalidValue;
+  a.ncu = device_cus();
+  const int64_t half = a.ncu / 2;
+  if (a.total > half || a.tiles_n > 8) {
+    const hipError_t r = act_tiles_one<AF, BF, false, EPI>(a, e, a.total, st);
+    if (r != hipSuccess) return r;
+  }
+  const int64_t small = 4 * (a.total < half ? a.total : half);
+  return a.tiles_n <= 8 ? act_tiles_one<AF, BF, true, EPI>(a, e, small, st) : hipSuccess;
+}
+
+template <int EPI>
+hipError_t act_tiles_any(const GemmLaunch &L, const ActArgs &e, hipStream_t st) {
+  const GemmArgs a = gemm_args(L);
+  if (L.a_fmt == kFmtE4M3)
+    return L.b_fmt == kFmtE2M1 ? act_tiles<kFmtE4M3, kFmtE2M1, EPI>(a, e, st) : act_tiles<kFmtE4M3, kFmtE4M3, EPI>(a, e, st);
+  return L.b_fmt == kFmtE2M1 ? act_tiles<kFmtE5M2, kFmtE2M1, EPI>(a, e, st) : act_tiles<kFmtE5M2, kFmtE4M3, EPI>(a, e, st);
+}
+
+}  // namespace
+}  // namespace mxfp4

@@ -13,6 +13,9 @@ the library, no CPU path.
     mxfp4_moe_combine(h, rows, y, weights=None, residual=None)
     mxfp4_moe_combine_bwd(grad_y, h, rows, weights=None, grad_h=None,
                           grad_weights=None)
+    mxfp4_grouped_matmul_act(a, a_scales, b, b_scales, c, group_list=None,
+                             act="none", bias=None, residual=None, z=None)
+    mxfp4_act_bwd(grad_c, z, grad_z, act="none", grad_bias=None, group_list=None)
 
 logits, x, h, y and gradients are bfloat16 or float32; weights, biases and
 their gradients float32; ids and rows int32 [tokens, k]; group_list int64
@@ -24,11 +27,14 @@ import ctypes
 
 import torch
 
-from . import _FP8, FLOOR, _check, _Desc, _dtype, _load, _need, _ptr, _shape2d, _stream
+from . import (_FP8, FLOOR, _check, _Desc, _dtype, _group_list, _load, _MxOperand, _need, _operand, _ptr, _stream)
 
 __all__ = ["mxfp4_moe_route", "mxfp4_moe_route_bwd", "mxfp4_moe_plan", "mxfp4_moe_plan_workspace",
-           "mxfp4_moe_dispatch", "mxfp4_moe_combine", "mxfp4_moe_combine_bwd"]
+           "mxfp4_moe_dispatch", "mxfp4_moe_combine", "mxfp4_moe_combine_bwd", "ACTIVATIONS",
+           "mxfp4_grouped_matmul_act", "mxfp4_act_bwd"]
 
+# the last two are gated: act(gate) * up
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 6, "geglu": 7}
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
@@ -38,6 +44,13 @@ class _Route(ctypes.Structure):
                 ("experts", ctypes.c_int32), ("tokens", ctypes.c_int64), ("k", ctypes.c_int32),
                 ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("reserved", ctypes.c_int32)]
+
+
+class _Epilogue(ctypes.Structure):
+    """mxfp4_epilogue_t (include/mxfp4.h)."""
+    _fields_ = [("act", ctypes.c_int32), ("reserved", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("bias_stride", ctypes.c_int64), ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+                ("z", ctypes.c_void_p), ("ld_z", ctypes.c_int64)]
 
 
 _typed = False
@@ -57,7 +70,13 @@ def _lib():
         lib.mxfp4_moe_dispatch.argtypes = [dp, i32, vp, vp, i32, i64, vp, vp, vp, vp]
         lib.mxfp4_moe_combine.argtypes = [i32, i64, i64, i32, i64, vp, vp, vp, vp, vp, vp]
         lib.mxfp4_moe_combine_bwd.argtypes = [i32, i64, i64, i32, i64, vp, vp, vp, vp, vp, vp, vp]
-        for f in ("mxfp4_moe_route", "mxfp4_moe_route_bwd", "mxfp4_moe_plan", "mxfp4_moe_dispatch",
+        op = ctypes.POINTER(_MxOperand)
+        lib.mxfp4_grouped_matmul_act.argtypes = [i64, i64, i64, op, op, vp, i32, i32, ctypes.POINTER(_Epilogue), i32, vp,
+                                                 i64, vp]
+        lib.mxfp4_act_bwd_workspace.argtypes = [i32, i64, i64, i32]
+        lib.mxfp4_act_bwd_workspace.restype = i64
+        lib.mxfp4_act_bwd.argtypes = [i32, i32, i64, i64, vp, vp, vp, vp, vp, i32, i32, vp, i64, vp]
+        for f in ("mxfp4_grouped_matmul_act", "mxfp4_act_bwd", "mxfp4_moe_route", "mxfp4_moe_route_bwd", "mxfp4_moe_plan", "mxfp4_moe_dispatch",
                   "mxfp4_moe_combine", "mxfp4_moe_combine_bwd"):
             getattr(lib, f).restype = ctypes.c_int32
         _typed = True
@@ -206,3 +225,87 @@ def mxfp4_moe_combine_bwd(grad_y, h, rows, weights=None, grad_h=None, grad_weigh
                                       _typed_ptr(grad_h, grad_y.dtype, "grad_h"),
                                       _typed_ptr(grad_weights, torch.float32, "grad_weights"), _stream())
     _check(st, "mxfp4_moe_combine_bwd")
+
+
+def _act(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def mxfp4_grouped_matmul_act(a, a_scales, b, b_scales, c, group_list=None, act="none", bias=None, residual=None, z=None,
+                             K=None, group_list_type=1, a_fmt="e4m3", b_fmt="e2m1", a_block=32, b_block=32):
+    """Grouped MX product with its epilogue, c = act(A B_g^T + bias_g) + residual.
+
+    a [M, lda] fp8 codes + a_scales; b [N, ldb] or [G, N, ldb] codes + scales of
+    the same rank; c bf16 / f32 [M, N], for the gated "swiglu" and "geglu" [M, N
+    / 2] with b's first N / 2 rows the gate; bias float32 [N] or [G, N]; residual
+    c's shape and type (c itself may be given); z [M, N] of c's type receives
+    the products before the activation.  K defaults to a's row length."""
+    code = _act(act)
+    if c is None or c.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("c must be a bfloat16 or float32 tensor")
+    M = _matrix(a, "a")[0]
+    n_list = 0 if group_list is None else (group_list.numel() if isinstance(group_list, torch.Tensor)
+                                           else len(group_list))
+    if a_scales is None or a_scales.dim() != 2 or a_scales.shape[0] < M:
+        raise ValueError(f"a_scales must have M={M} rows")
+    if b is None or b_scales is None or b.dim() < 2 or b_scales.dim() < 2 or b_scales.shape[-2] != b.shape[-2]:
+        raise ValueError("b_scales must have as many rows as b")
+    groups = max(n_list, 1)
+    if b.dim() == 3 and (b.shape[0] < groups or b_scales.shape[0] < groups):
+        raise ValueError(f"b and b_scales must hold one matrix per group ({groups})")
+    nb = b.shape[-2]
+    if code & 4 and nb % 2:
+        raise ValueError(f"a gated activation needs an even number of rows of b, got {nb}")
+    N = nb // 2 if code & 4 else nb
+    _same_shape(c, (M, N), "c")
+    _same_shape(residual, (M, N), "residual")
+    _same_shape(z, (M, nb), "z")
+    if bias is not None and tuple(bias.shape) not in ((nb,), (groups, nb)):
+        raise ValueError(f"bias must be [{nb}] or [{groups}, {nb}], got {list(bias.shape)}")
+    if K is None:
+        K = a.shape[1]
+    oa = _operand(a, a_scales, a_fmt, a_block)
+    ob = _operand(b, b_scales, b_fmt, b_block)
+    gl = _group_list(group_list, M, group_list_type)
+    ep = _Epilogue(code, 0, _value(_typed_ptr(bias, torch.float32, "bias")),
+                   nb if bias is not None and bias.dim() == 2 else 0,
+                   _value(_typed_ptr(residual, c.dtype, "residual")), N, _value(_typed_ptr(z, c.dtype, "z")), nb)
+    st = _lib().mxfp4_grouped_matmul_act(M, N, int(K), ctypes.byref(oa), ctypes.byref(ob), _ptr(gl, "i64"),
+                                         0 if gl is None else gl.numel(), int(group_list_type), ctypes.byref(ep),
+                                         1 if c.dtype == torch.float32 else 0, _ptr(c), N, _stream())
+    _check(st, "mxfp4_grouped_matmul_act")
+
+
+def _value(p):
+    return None if p is None else p.value
+
+
+def mxfp4_act_bwd(grad_c, z, grad_z, act="none", grad_bias=None, group_list=None, group_list_type=1, workspace=None):
+    """Backward of the epilogue: grad_z (z's shape) from grad_c and z, and
+    grad_bias float32 [columns of z] or [G, columns of z].  workspace: a uint8
+    tensor of mxfp4_act_bwd_workspace bytes for grad_bias; allocated from torch
+    when None."""
+    code = _act(act)
+    rows, cols = _matrix(grad_c, "grad_c")
+    zc = cols * (2 if code & 4 else 1)
+    _same_shape(z, (rows, zc), "z")
+    _same_shape(grad_z, (rows, zc), "grad_z")
+    if z is None or grad_z is None:
+        raise ValueError("z and grad_z are required")
+    gl = _group_list(group_list, rows, group_list_type)
+    groups = 0 if gl is None else gl.numel()
+    need = 0
+    if grad_bias is not None:
+        if tuple(grad_bias.shape) not in ((max(groups, 1), zc),) + (((zc,),) if groups <= 1 else ()):
+            raise ValueError(f"grad_bias must be [{groups or 1}, {zc}], got {list(grad_bias.shape)}")
+        need = int(_lib().mxfp4_act_bwd_workspace(code, rows, cols, groups))
+        if workspace is None:
+            workspace = torch.empty(max(need, 4), dtype=torch.uint8, device=grad_c.device)
+        _need(workspace, need, "workspace")
+    st = _lib().mxfp4_act_bwd(_dtype(grad_c), code, rows, cols, _ptr(grad_c), _typed_ptr(z, grad_c.dtype, "z"),
+                              _typed_ptr(grad_z, grad_c.dtype, "grad_z"),
+                              _typed_ptr(grad_bias, torch.float32, "grad_bias"), _ptr(gl, "i64"), groups,
+                              int(group_list_type), _ptr(workspace, "u8") if need else None, need, _stream())
+    _check(st, "mxfp4_act_bwd")
