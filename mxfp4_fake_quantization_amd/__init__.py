@@ -181,8 +181,15 @@ def _desc(x: torch.Tensor, block: int, rule, scale_factor: float) -> _Desc:
     return _Desc(_dtype(x), int(block), _rule(rule), 0, rows, cols, float(scale_factor), 0)
 
 
+# The current stream's handle without a torch.cuda.Stream object around it
+# (0.1 us against 2.7 us a call; a small launch takes 3 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(status: int, what: str):

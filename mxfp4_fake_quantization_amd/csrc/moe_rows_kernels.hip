@@ -150,33 +150,50 @@ struct DispatchArgs {
   const uint8_t *x;
   const int32_t *rows;
   uint8_t *y, *q, *scales;
-  int64_t cols, nb, out_rows;
-  int k, chunks;  // workgroups a token
+  int64_t tokens, cols, nb, out_rows;
+  int k, chunks;  // workgroups a row of tokens
+  int tx_log;
 };
 
-constexpr int kDispatchThreads = 128;
+constexpr int kDispatchThreads = 128, kDispatchLog = 7;
 
-// Row of slot i (-1 outside [0, n)) and its weight.  i is the same for the
-// workgroup, so these are scalar loads, which the branches around them, taken
-// lane by lane at the end of a row, do not touch.
+// Lanes of a workgroup: 2^tx_log side by side in a token's row, the tokens
+// below each other.  WIDE: one token a workgroup, so slots are the same for all
+// lanes and their rows and weights come by scalar loads, which the branches
+// around them, taken lane by lane at the end of a row, do not touch.
 typedef const int32_t __attribute__((address_space(4))) *scalar_i32;
 typedef const float __attribute__((address_space(4))) *scalar_f32;
+
+// Row of slot i, -1 outside [0, n), and its weight.
+template <bool WIDE>
 __device__ __forceinline__ int slot_row(const int32_t *rows, int64_t i, int64_t n) {
-  const int r = ((scalar_i32)(uint64_t)rows)[i];
+  const int r = WIDE ? ((scalar_i32)(uint64_t)rows)[i] : rows[i];
   return r >= 0 && r < n ? r : -1;
 }
+template <bool WIDE>
 __device__ __forceinline__ float slot_weight(const float *weights, int64_t i) {
-  return weights ? ((scalar_f32)(uint64_t)weights)[i] : 1.0f;
+  if (!weights) return 1.0f;
+  return WIDE ? ((scalar_f32)(uint64_t)weights)[i] : weights[i];
 }
 
-template <int DT, int FMT, int G>
+// log2 of the lanes side by side: as many as the row has 8-element pieces, at
+// least 4 (a 32-element block), at most `most`.
+int lanes_log(int64_t cols, int least, int most) {
+  int l = least;
+  while (l < most && ((int64_t)8 << l) < cols) ++l;
+  return l;
+}
+
+template <int DT, int FMT, int G, bool WIDE>
 __global__ __launch_bounds__(kDispatchThreads) void dispatch_kernel(DispatchArgs A) {
   constexpr int ES = Row8<DT>::ES;
   constexpr float MAXN = FMT == kE4M3 ? 448.0f : 57344.0f;
   constexpr int EMAX = FMT == kE4M3 ? 8 : 15;
-  const int64_t t = blockIdx.x / A.chunks;
-  const int64_t c0 = ((int64_t)(blockIdx.x % A.chunks) * kDispatchThreads + threadIdx.x) * 8;
-  const int64_t left = A.cols - c0;
+  const int tx_log = WIDE ? kDispatchLog : A.tx_log;
+  int64_t t = blockIdx.x / A.chunks;
+  if (!WIDE) t = (t << (kDispatchLog - tx_log)) + (threadIdx.x >> tx_log);
+  const int64_t c0 = ((int64_t)(blockIdx.x % A.chunks << tx_log) + (threadIdx.x & ((1 << tx_log) - 1))) * 8;
+  const int64_t left = WIDE || t < A.tokens ? A.cols - c0 : 0;
   const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
   uint32_t w[Row8<DT>::NW];
   load8<DT>(w, A.x + (t * A.cols + c0) * ES, n);
@@ -209,7 +226,7 @@ __global__ __launch_bounds__(kDispatchThreads) void dispatch_kernel(DispatchArgs
   if (n == 0) return;
   const bool head = (threadIdx.x & (G - 1)) == 0;
   for (int j = 0; j < A.k; ++j) {
-    const int64_t r = slot_row(A.rows, t * A.k + j, A.out_rows);
+    const int64_t r = slot_row<WIDE>(A.rows, t * A.k + j, A.out_rows);
     if (r < 0) continue;
     if (A.y) store8<DT>(A.y + (r * A.cols + c0) * ES, w, n);
     if (A.q) {
@@ -229,7 +246,7 @@ __global__ __launch_bounds__(kDispatchThreads) void dispatch_kernel(DispatchArgs
 // ---- combine -------------------------------------------------------------------
 //
 // A lane sums 8 elements of a token over its k rows in 32 bits, in the order
-// of the choices; the rows' loads are independent, four in flight at a time.
+// of the choices; the rows' loads are independent, eight in flight at a time.
 // Bound by the bytes read.
 
 struct CombineArgs {
@@ -238,34 +255,38 @@ struct CombineArgs {
   const float *weights;
   const uint8_t *residual;
   uint8_t *y;
-  int64_t cols, in_rows;
-  int k, chunks;
+  int64_t tokens, cols, in_rows;
+  int k, chunks, tx_log;
 };
 
-constexpr int kCombineThreads = 128;
+constexpr int kCombineThreads = 128, kCombineLog = 7;
+constexpr int kAhead = 8;
 
-template <int DT>
+template <int DT, bool WIDE>
 __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs A) {
   constexpr int ES = Row8<DT>::ES;
-  const int64_t t = blockIdx.x / A.chunks;
-  const int64_t c0 = ((int64_t)(blockIdx.x % A.chunks) * kCombineThreads + threadIdx.x) * 8;
+  const int tx_log = WIDE ? kCombineLog : A.tx_log;
+  int64_t t = blockIdx.x / A.chunks;
+  if (!WIDE) t = (t << (kCombineLog - tx_log)) + (threadIdx.x >> tx_log);
+  if (!WIDE && t >= A.tokens) return;
+  const int64_t c0 = ((int64_t)(blockIdx.x % A.chunks << tx_log) + (threadIdx.x & ((1 << tx_log) - 1))) * 8;
   const int64_t left = A.cols - c0;
   const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
   float acc[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-  for (int j0 = 0; j0 < A.k; j0 += 4) {
-    uint32_t w[4][Row8<DT>::NW];
-    int r[4];
+  for (int j0 = 0; j0 < A.k; j0 += kAhead) {
+    uint32_t w[kAhead][Row8<DT>::NW];
+    int r[kAhead];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      r[u] = j0 + u < A.k ? slot_row(A.rows, t * A.k + j0 + u, A.in_rows) : -1;
+    for (int u = 0; u < kAhead; ++u) {
+      r[u] = j0 + u < A.k ? slot_row<WIDE>(A.rows, t * A.k + j0 + u, A.in_rows) : -1;
       if (r[u] >= 0) load8<DT>(w[u], A.h + ((int64_t)r[u] * A.cols + c0) * ES, n);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       if (r[u] < 0) continue;
-      const float wt = slot_weight(A.weights, t * A.k + j0 + u);
+      const float wt = slot_weight<WIDE>(A.weights, t * A.k + j0 + u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] += wt * elem<DT>(w[u], j);
     }
@@ -284,10 +305,12 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs A)
 
 // ---- combine backward ------------------------------------------------------------
 //
-// A workgroup takes one token: its gradient row once, 8 elements a lane and
-// 2048 a pass, and up to 8 of its rows at a time: grad_h = w * dy leaves as it
-// is formed, and the dot products of dy with the rows stay in registers until
-// the end of the row, where the waves' sums meet in LDS.  Bound by the bytes.
+// grad_h = w * dy leaves as it is formed; the dot products of dy with up to 8
+// rows at a time stay in registers until the end of the row.  Rows of up to
+// 512 elements: one piece a lane, tokens below each other in a wave, the sums
+// by lane exchanges.  Longer ones: a workgroup a token, 2048 elements a pass,
+// where the waves' sums meet in LDS.  Both add in an order fixed by the shape.
+// Bound by the bytes.
 
 struct CombineBwdArgs {
   const uint8_t *gy, *h;
@@ -295,58 +318,65 @@ struct CombineBwdArgs {
   const float *weights;
   uint8_t *gh;
   float *gw;
-  int64_t cols, in_rows;
-  int k;
+  int64_t tokens, cols, in_rows;
+  int k, tx_log;
 };
 
-constexpr int kCombineBwdThreads = 256;
+constexpr int kCombineBwdThreads = 256, kDots = 8;
+
+// One piece of dy against slots j0 .. j0 + 7 of token t: rows out, dots on.
+template <int DT, bool WIDE>
+__device__ __forceinline__ void combine_bwd_piece(const CombineBwdArgs &A, int64_t t, int j0, int64_t c0, int n,
+                                                  float (&dot)[kDots]) {
+  constexpr int ES = Row8<DT>::ES;
+  uint32_t wy[Row8<DT>::NW], wh[kDots][Row8<DT>::NW];
+  int r[kDots];
+  // every load before the first store, which may not move over them
+  load8<DT>(wy, A.gy + (t * A.cols + c0) * ES, n);
+#pragma unroll
+  for (int u = 0; u < kDots; ++u) {
+    r[u] = j0 + u < A.k ? slot_row<WIDE>(A.rows, t * A.k + j0 + u, A.in_rows) : -1;
+    if (A.gw && r[u] >= 0) load8<DT>(wh[u], A.h + ((int64_t)r[u] * A.cols + c0) * ES, n);
+  }
+#pragma unroll
+  for (int u = 0; u < kDots; ++u) {
+    if (r[u] < 0) continue;
+    if (A.gw) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dot[u] += elem<DT>(wy, j) * elem<DT>(wh[u], j);
+    }
+    if (A.gh) {
+      const float wt = slot_weight<WIDE>(A.weights, t * A.k + j0 + u);
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = wt * elem<DT>(wy, j);
+      uint32_t o[Row8<DT>::NW];
+      pack8<DT>(o, f);
+      store8<DT>(A.gh + ((int64_t)r[u] * A.cols + c0) * ES, o, n);
+    }
+  }
+}
 
 template <int DT>
 __global__ __launch_bounds__(kCombineBwdThreads) void combine_bwd_kernel(CombineBwdArgs A) {
-  constexpr int ES = Row8<DT>::ES, KB = 8;
-  __shared__ float part[kCombineBwdThreads / 64][KB];
+  __shared__ float part[kCombineBwdThreads / 64][kDots];
   const int64_t t = blockIdx.x;
-  const int lane = (int)__lane_id(), wave = threadIdx.x >> 6;
-  for (int j0 = 0; j0 < A.k; j0 += KB) {
-    float dot[KB];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int j0 = 0; j0 < A.k; j0 += kDots) {
+    float dot[kDots];
 #pragma unroll
-    for (int u = 0; u < KB; ++u) dot[u] = 0.0f;
-    for (int64_t c0 = (int64_t)threadIdx.x * 8; c0 < A.cols; c0 += kCombineBwdThreads * 8) {
-      const int n = A.cols - c0 >= 8 ? 8 : (int)(A.cols - c0);
-      uint32_t wy[Row8<DT>::NW];
-      load8<DT>(wy, A.gy + (t * A.cols + c0) * ES, n);
-#pragma unroll
-      for (int u = 0; u < KB; ++u) {
-        if (j0 + u >= A.k) break;
-        const int64_t r = slot_row(A.rows, t * A.k + j0 + u, A.in_rows);
-        if (r < 0) continue;
-        const int64_t at = (r * A.cols + c0) * ES;
-        if (A.gw) {
-          uint32_t wh[Row8<DT>::NW];
-          load8<DT>(wh, A.h + at, n);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) dot[u] += elem<DT>(wy, j) * elem<DT>(wh, j);
-        }
-        if (A.gh) {
-          const float wt = slot_weight(A.weights, t * A.k + j0 + u);
-          float f[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = wt * elem<DT>(wy, j);
-          uint32_t o[Row8<DT>::NW];
-          pack8<DT>(o, f);
-          store8<DT>(A.gh + at, o, n);
-        }
-      }
-    }
+    for (int u = 0; u < kDots; ++u) dot[u] = 0.0f;
+    for (int64_t c0 = (int64_t)threadIdx.x * 8; c0 < A.cols; c0 += kCombineBwdThreads * 8)
+      combine_bwd_piece<DT, true>(A, t, j0, c0, A.cols - c0 >= 8 ? 8 : (int)(A.cols - c0), dot);
     if (!A.gw) continue;  // the same for the whole launch
 #pragma unroll
-    for (int u = 0; u < KB; ++u) {
+    for (int u = 0; u < kDots; ++u) {
       float s = dot[u];
       for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
       if (lane == 0) part[wave][u] = s;
     }
     __syncthreads();
-    if (threadIdx.x < KB && j0 + (int)threadIdx.x < A.k) {
+    if (threadIdx.x < kDots && j0 + (int)threadIdx.x < A.k) {
       float s = 0.0f;
       for (int w = 0; w < kCombineBwdThreads / 64; ++w) s += part[w][threadIdx.x];
       A.gw[t * A.k + j0 + threadIdx.x] = s;
@@ -355,12 +385,62 @@ __global__ __launch_bounds__(kCombineBwdThreads) void combine_bwd_kernel(Combine
   }
 }
 
-template <int DT, int FMT>
-hipError_t dispatch_one(const DispatchArgs &a, int block, int64_t grid, hipStream_t st) {
-  if (block == 128)
-    hipLaunchKernelGGL((dispatch_kernel<DT, FMT, 16>), dim3((unsigned)grid), dim3(kDispatchThreads), 0, st, a);
+template <int DT>
+__global__ __launch_bounds__(kCombineBwdThreads) void combine_bwd_narrow_kernel(CombineBwdArgs A) {
+  const int tx = threadIdx.x & ((1 << A.tx_log) - 1);
+  const int64_t t = ((int64_t)blockIdx.x * kCombineBwdThreads + threadIdx.x) >> A.tx_log;
+  const int64_t c0 = (int64_t)tx * 8;
+  const int64_t left = t < A.tokens ? A.cols - c0 : 0;
+  const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+  for (int j0 = 0; j0 < A.k; j0 += kDots) {
+    float dot[kDots];
+#pragma unroll
+    for (int u = 0; u < kDots; ++u) dot[u] = 0.0f;
+    if (n > 0) combine_bwd_piece<DT, false>(A, t, j0, c0, n, dot);
+    if (!A.gw) continue;
+#pragma unroll
+    for (int u = 0; u < kDots; ++u) {
+      float s = dot[u];
+      for (int d = 1; d < (1 << A.tx_log); d <<= 1) s += __shfl_xor(s, d);
+      if (tx == 0 && t < A.tokens && j0 + u < A.k) A.gw[t * A.k + j0 + u] = s;
+    }
+  }
+}
+
+template <int DT, int FMT, int G>
+hipError_t dispatch_one(const DispatchArgs &a, int64_t grid, hipStream_t st) {
+  if (a.tx_log == kDispatchLog)
+    hipLaunchKernelGGL((dispatch_kernel<DT, FMT, G, true>), dim3((unsigned)grid), dim3(kDispatchThreads), 0, st, a);
   else
-    hipLaunchKernelGGL((dispatch_kernel<DT, FMT, 4>), dim3((unsigned)grid), dim3(kDispatchThreads), 0, st, a);
+    hipLaunchKernelGGL((dispatch_kernel<DT, FMT, G, false>), dim3((unsigned)grid), dim3(kDispatchThreads), 0, st, a);
+  return hipGetLastError();
+}
+template <int DT, int FMT>
+hipError_t dispatch_g(const DispatchArgs &a, int block, int64_t grid, hipStream_t st) {
+  return block == 128 ? dispatch_one<DT, FMT, 16>(a, grid, st) : dispatch_one<DT, FMT, 4>(a, grid, st);
+}
+
+template <int DT>
+hipError_t combine_one(const CombineArgs &a, int64_t grid, hipStream_t st) {
+  if (a.tx_log == kCombineLog)
+    hipLaunchKernelGGL((combine_kernel<DT, true>), dim3((unsigned)grid), dim3(kCombineThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((combine_kernel<DT, false>), dim3((unsigned)grid), dim3(kCombineThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t combine_bwd_one(CombineBwdArgs &a, hipStream_t st) {
+  constexpr int64_t kNarrow = 512;
+  if (a.cols <= kNarrow) {
+    a.tx_log = lanes_log(a.cols, 0, 6);
+    const int64_t per = kCombineBwdThreads >> a.tx_log, grid = (a.tokens + per - 1) / per;
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((combine_bwd_narrow_kernel<DT>), dim3((unsigned)grid), dim3(kCombineBwdThreads), 0, st, a);
+  } else {
+    if (a.tokens > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((combine_bwd_kernel<DT>), dim3((unsigned)a.tokens), dim3(kCombineBwdThreads), 0, st, a);
+  }
   return hipGetLastError();
 }
 
@@ -402,13 +482,15 @@ hipError_t launch_dispatch(const DispatchLaunch &L, hipStream_t st) {
   a.nb = (L.cols + L.block - 1) / L.block;
   a.out_rows = L.out_rows;
   a.k = L.k;
-  const int64_t chunks = (L.cols + 8 * kDispatchThreads - 1) / (8 * kDispatchThreads);
-  const int64_t grid = chunks * L.tokens;
+  a.tokens = L.tokens;
+  a.tx_log = lanes_log(L.cols, L.block == 128 ? 4 : 2, kDispatchLog);
+  const int64_t chunks = (L.cols + (8 << a.tx_log) - 1) / (8 << a.tx_log);
+  const int64_t per = kDispatchThreads >> a.tx_log, grid = chunks * ((L.tokens + per - 1) / per);
   if (chunks > 0x7FFFFFFF || grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   a.chunks = (int)chunks;
   if (L.dtype == kBF16)
-    return L.fmt == kE4M3 ? dispatch_one<kBF16, kE4M3>(a, L.block, grid, st) : dispatch_one<kBF16, kE5M2>(a, L.block, grid, st);
-  return L.fmt == kE4M3 ? dispatch_one<kF32, kE4M3>(a, L.block, grid, st) : dispatch_one<kF32, kE5M2>(a, L.block, grid, st);
+    return L.fmt == kE4M3 ? dispatch_g<kBF16, kE4M3>(a, L.block, grid, st) : dispatch_g<kBF16, kE5M2>(a, L.block, grid, st);
+  return L.fmt == kE4M3 ? dispatch_g<kF32, kE4M3>(a, L.block, grid, st) : dispatch_g<kF32, kE5M2>(a, L.block, grid, st);
 }
 
 hipError_t launch_combine(const CombineLaunch &L, hipStream_t st) {
@@ -421,13 +503,13 @@ hipError_t launch_combine(const CombineLaunch &L, hipStream_t st) {
   a.cols = L.cols;
   a.in_rows = L.in_rows;
   a.k = L.k;
-  const int64_t chunks = (L.cols + 8 * kCombineThreads - 1) / (8 * kCombineThreads);
-  const int64_t grid = chunks * L.tokens;
+  a.tokens = L.tokens;
+  a.tx_log = lanes_log(L.cols, 0, kCombineLog);
+  const int64_t chunks = (L.cols + (8 << a.tx_log) - 1) / (8 << a.tx_log);
+  const int64_t per = kCombineThreads >> a.tx_log, grid = chunks * ((L.tokens + per - 1) / per);
   if (chunks > 0x7FFFFFFF || grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   a.chunks = (int)chunks;
-  if (L.dtype == kBF16) hipLaunchKernelGGL((combine_kernel<kBF16>), dim3((unsigned)grid), dim3(kCombineThreads), 0, st, a);
-  else hipLaunchKernelGGL((combine_kernel<kF32>), dim3((unsigned)grid), dim3(kCombineThreads), 0, st, a);
-  return hipGetLastError();
+  return L.dtype == kBF16 ? combine_one<kBF16>(a, grid, st) : combine_one<kF32>(a, grid, st);
 }
 
 hipError_t launch_combine_bwd(const CombineBwdLaunch &L, hipStream_t st) {
@@ -441,10 +523,8 @@ hipError_t launch_combine_bwd(const CombineBwdLaunch &L, hipStream_t st) {
   a.cols = L.cols;
   a.in_rows = L.in_rows;
   a.k = L.k;
-  if (L.tokens > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (L.dtype == kBF16) hipLaunchKernelGGL((combine_bwd_kernel<kBF16>), dim3((unsigned)L.tokens), dim3(kCombineBwdThreads), 0, st, a);
-  else hipLaunchKernelGGL((combine_bwd_kernel<kF32>), dim3((unsigned)L.tokens), dim3(kCombineBwdThreads), 0, st, a);
-  return hipGetLastError();
+  a.tokens = L.tokens;
+  return L.dtype == kBF16 ? combine_bwd_one<kBF16>(a, st) : combine_bwd_one<kF32>(a, st);
 }
 
 }  // namespace mxfp4

@@ -27,7 +27,7 @@ import ctypes
 
 import torch
 
-from . import (_FP8, FLOOR, _check, _Desc, _dtype, _group_list, _load, _MxOperand, _need, _operand, _ptr, _stream)
+from . import _FP8, FLOOR, _check, _Desc, _dtype, _group_list, _load, _MxOperand, _need, _operand, _ptr, _stream
 
 __all__ = ["mxfp4_moe_route", "mxfp4_moe_route_bwd", "mxfp4_moe_plan", "mxfp4_moe_plan_workspace",
            "mxfp4_moe_dispatch", "mxfp4_moe_combine", "mxfp4_moe_combine_bwd", "ACTIVATIONS",
@@ -83,21 +83,38 @@ def _lib():
     return lib
 
 
-def _typed_ptr(t, dtype, what):
-    if t is not None and t.dtype != dtype:
-        raise ValueError(f"{what} is a {dtype} tensor, got {t.dtype}")
-    return _ptr(t)
-
-
 def _matrix(t, what):
     if t is None or t.dim() != 2:
         raise ValueError(f"{what} must be a 2-D tensor")
     return t.shape
 
 
-def _same_shape(t, shape, what):
-    if t is not None and tuple(t.shape) != tuple(shape):
+def _arg(t, shape, dtype, what):
+    """Address of a tensor of this shape and type (None stays None)."""
+    if t is None:
+        return None
+    if t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} is a {dtype} tensor, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _on_gpu(*tensors):
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("tensors must live on the GPU (no CPU path)")
+
+
+def _given(t, what):
+    if t is None:
+        raise ValueError(f"{what} is required")
+    return t
+
+
+_F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
 
 
 def _route_desc(logits, k, score, num_groups, topk_groups, renormalize, scale):
@@ -114,29 +131,27 @@ def mxfp4_moe_route(logits, weights, ids, bias=None, score="softmax", num_groups
     """The k experts of every token and their weights: logits [tokens, experts]
     -> weights [tokens, k] float32 and ids [tokens, k] int32, k being ids'
     second dimension; see include/mxfp4.h."""
-    tokens, k = _matrix(ids, "ids")
+    k = _matrix(ids, "ids")[1]
+    shape = tokens, experts = _matrix(logits, "logits")
     d = _route_desc(logits, k, score, num_groups, topk_groups, renormalize, scale)
-    _same_shape(ids, (d.tokens, k), "ids")
-    _same_shape(weights, (d.tokens, k), "weights")
-    _same_shape(bias, (d.experts,), "bias")
-    st = _lib().mxfp4_moe_route(ctypes.byref(d), _ptr(logits), _typed_ptr(bias, torch.float32, "bias"),
-                                _typed_ptr(weights, torch.float32, "weights"), _typed_ptr(ids, torch.int32, "ids"),
-                                _stream())
-    _check(st, "mxfp4_moe_route")
+    args = (ctypes.byref(d), _arg(logits, shape, logits.dtype, "logits"), _arg(bias, (experts,), _F32, "bias"),
+            _arg(_given(weights, "weights"), (tokens, k), _F32, "weights"), _arg(ids, (tokens, k), _I32, "ids"))
+    _on_gpu(logits, weights, ids, bias)
+    _check(_lib().mxfp4_moe_route(*args, _stream()), "mxfp4_moe_route")
 
 
 def mxfp4_moe_route_bwd(grad_weights, logits, ids, grad_logits, score="softmax", renormalize=True, scale=1.0):
     """Gradient of mxfp4_moe_route's weights with respect to the logits (the
     choice is constant; the bias moves the choice only and has none)."""
-    tokens, k = _matrix(ids, "ids")
+    k = _matrix(ids, "ids")[1]
+    shape = _matrix(logits, "logits")
+    chosen = (shape[0], k)
     d = _route_desc(logits, k, score, 1, 1, renormalize, scale)
-    _same_shape(ids, (d.tokens, k), "ids")
-    _same_shape(grad_weights, (d.tokens, k), "grad_weights")
-    _same_shape(grad_logits, logits.shape, "grad_logits")
-    st = _lib().mxfp4_moe_route_bwd(ctypes.byref(d), _typed_ptr(grad_weights, torch.float32, "grad_weights"),
-                                    _ptr(logits), _typed_ptr(ids, torch.int32, "ids"),
-                                    _typed_ptr(grad_logits, logits.dtype, "grad_logits"), _stream())
-    _check(st, "mxfp4_moe_route_bwd")
+    args = (ctypes.byref(d), _arg(_given(grad_weights, "grad_weights"), chosen, _F32, "grad_weights"),
+            _arg(logits, shape, logits.dtype, "logits"), _arg(ids, chosen, _I32, "ids"),
+            _arg(_given(grad_logits, "grad_logits"), shape, logits.dtype, "grad_logits"))
+    _on_gpu(grad_weights, logits, ids, grad_logits)
+    _check(_lib().mxfp4_moe_route_bwd(*args, _stream()), "mxfp4_moe_route_bwd")
 
 
 def mxfp4_moe_plan_workspace(slots: int, experts: int) -> int:
@@ -152,79 +167,69 @@ def mxfp4_moe_plan(ids, group_list, rows, workspace=None):
     grouped calls take) and rows, ids' shape (each slot's row in expert order;
     -1 where ids holds none).  workspace: a uint8 tensor of
     mxfp4_moe_plan_workspace bytes; allocated from torch when None."""
-    _same_shape(rows, ids.shape, "rows")
     if group_list is None or group_list.dim() != 1:
         raise ValueError("group_list must be a 1-D tensor with one count per expert")
-    slots, experts = ids.numel(), group_list.numel()
+    shape, slots, experts = ids.shape, ids.numel(), group_list.numel()
+    if _given(rows, "rows").shape != shape:
+        raise ValueError(f"rows must be {list(shape)}, got {list(rows.shape)}")
     need = mxfp4_moe_plan_workspace(slots, experts)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
+        workspace = torch.empty(need, dtype=_U8, device=ids.device)
     _need(workspace, need, "workspace")
-    st = _lib().mxfp4_moe_plan(slots, experts, _typed_ptr(ids, torch.int32, "ids"), _ptr(group_list, "i64"),
-                               _typed_ptr(rows, torch.int32, "rows"), _ptr(workspace, "u8") if need else None,
-                               need, _stream())
-    _check(st, "mxfp4_moe_plan")
+    args = (slots, experts, _arg(ids, shape, _I32, "ids"), _arg(group_list, (experts,), _I64, "group_list"),
+            _arg(rows, shape, _I32, "rows"), _ptr(workspace, "u8") if need else None, need)
+    _on_gpu(ids, group_list, rows)
+    _check(_lib().mxfp4_moe_plan(*args, _stream()), "mxfp4_moe_plan")
 
 
 def mxfp4_moe_dispatch(x, rows, y=None, q=None, scales=None, fmt="e4m3", block=32):
     """Token rows to their slots' rows: x [tokens, cols] -> y [n, cols] (x's
     type) and / or MXFP8 q [n, cols] with scales [n, ceil(cols / block)]."""
-    tokens, cols = _matrix(x, "x")
+    shape = tokens, cols = _matrix(x, "x")
     k = _matrix(rows, "rows")[1]
-    _same_shape(rows, (tokens, k), "rows")
     if fmt not in _FP8:
         raise ValueError(f"fmt must be 'e4m3' or 'e5m2', got {fmt!r}")
     outs = [t.shape[0] for t in (y, q) if t is not None]
     if not outs or outs[0] != outs[-1]:
         raise ValueError("y and / or q with the same number of rows is required")
     n = outs[0]
-    _same_shape(y, (n, cols), "y")
-    _same_shape(q, (n, cols), "q")
-    _same_shape(scales, (n, -(-cols // int(block))), "scales")
     d = _Desc(_dtype(x), int(block), FLOOR, 0, tokens, cols, 6.0, 0)
-    st = _lib().mxfp4_moe_dispatch(ctypes.byref(d), _FP8[fmt], _ptr(x), _typed_ptr(rows, torch.int32, "rows"), k, n,
-                                   _typed_ptr(y, x.dtype, "y"), _ptr(q, "u8"), _ptr(scales, "u8"), _stream())
-    _check(st, "mxfp4_moe_dispatch")
+    args = (ctypes.byref(d), _FP8[fmt], _arg(x, shape, x.dtype, "x"), _arg(rows, (tokens, k), _I32, "rows"), k, n,
+            _arg(y, (n, cols), x.dtype, "y"), _arg(q, (n, cols), _U8, "q"),
+            _arg(scales, (n, -(-cols // int(block))), _U8, "scales"))
+    _on_gpu(x, rows, y, q, scales)
+    _check(_lib().mxfp4_moe_dispatch(*args, _stream()), "mxfp4_moe_dispatch")
 
 
 def mxfp4_moe_combine(h, rows, y, weights=None, residual=None):
     """Expert rows back to the tokens: y[t] = residual[t] + sum_j weights[t, j]
     * h[rows[t, j]]; y may be the residual."""
-    n, cols = _matrix(h, "h")
+    shape = n, cols = _matrix(h, "h")
     tokens, k = _matrix(rows, "rows")
-    _same_shape(y, (tokens, cols), "y")
-    _same_shape(weights, (tokens, k), "weights")
-    _same_shape(residual, (tokens, cols), "residual")
-    if y is None:
-        raise ValueError("y is required")
-    st = _lib().mxfp4_moe_combine(_dtype(h), tokens, cols, k, n, _ptr(h), _typed_ptr(rows, torch.int32, "rows"),
-                                  _typed_ptr(weights, torch.float32, "weights"),
-                                  _typed_ptr(residual, h.dtype, "residual"), _typed_ptr(y, h.dtype, "y"), _stream())
-    _check(st, "mxfp4_moe_combine")
+    dt, out = h.dtype, (tokens, cols)
+    args = (_dtype(h), tokens, cols, k, n, _arg(h, shape, dt, "h"), _arg(rows, (tokens, k), _I32, "rows"),
+            _arg(weights, (tokens, k), _F32, "weights"), _arg(residual, out, dt, "residual"),
+            _arg(_given(y, "y"), out, dt, "y"))
+    _on_gpu(h, rows, y, weights, residual)
+    _check(_lib().mxfp4_moe_combine(*args, _stream()), "mxfp4_moe_combine")
 
 
 def mxfp4_moe_combine_bwd(grad_y, h, rows, weights=None, grad_h=None, grad_weights=None):
     """Gradients of mxfp4_moe_combine: grad_h [n, cols] and / or grad_weights
     [tokens, k] (which needs h)."""
-    tokens, cols = _matrix(grad_y, "grad_y")
+    shape = tokens, cols = _matrix(grad_y, "grad_y")
     k = _matrix(rows, "rows")[1]
-    _same_shape(rows, (tokens, k), "rows")
     if grad_weights is not None and h is None:
         raise ValueError("grad_weights needs h")
-    sized = [t for t in (h, grad_h) if t is not None]
     if grad_h is None and grad_weights is None:
         raise ValueError("grad_h and / or grad_weights is required")
-    n = sized[0].shape[0]
-    for t, what in ((h, "h"), (grad_h, "grad_h")):
-        _same_shape(t, (n, cols), what)
-    _same_shape(weights, (tokens, k), "weights")
-    _same_shape(grad_weights, (tokens, k), "grad_weights")
-    st = _lib().mxfp4_moe_combine_bwd(_dtype(grad_y), tokens, cols, k, n, _ptr(grad_y),
-                                      _typed_ptr(h, grad_y.dtype, "h"), _typed_ptr(rows, torch.int32, "rows"),
-                                      _typed_ptr(weights, torch.float32, "weights"),
-                                      _typed_ptr(grad_h, grad_y.dtype, "grad_h"),
-                                      _typed_ptr(grad_weights, torch.float32, "grad_weights"), _stream())
-    _check(st, "mxfp4_moe_combine_bwd")
+    n = (grad_h if h is None else h).shape[0]
+    dt, chosen = grad_y.dtype, (tokens, k)
+    args = (_dtype(grad_y), tokens, cols, k, n, _arg(grad_y, shape, dt, "grad_y"), _arg(h, (n, cols), dt, "h"),
+            _arg(rows, chosen, _I32, "rows"), _arg(weights, chosen, _F32, "weights"),
+            _arg(grad_h, (n, cols), dt, "grad_h"), _arg(grad_weights, chosen, _F32, "grad_weights"))
+    _on_gpu(grad_y, h, rows, weights, grad_h, grad_weights)
+    _check(_lib().mxfp4_moe_combine_bwd(*args, _stream()), "mxfp4_moe_combine_bwd")
 
 
 def _act(act):
@@ -259,9 +264,6 @@ def mxfp4_grouped_matmul_act(a, a_scales, b, b_scales, c, group_list=None, act="
     if code & 4 and nb % 2:
         raise ValueError(f"a gated activation needs an even number of rows of b, got {nb}")
     N = nb // 2 if code & 4 else nb
-    _same_shape(c, (M, N), "c")
-    _same_shape(residual, (M, N), "residual")
-    _same_shape(z, (M, nb), "z")
     if bias is not None and tuple(bias.shape) not in ((nb,), (groups, nb)):
         raise ValueError(f"bias must be [{nb}] or [{groups}, {nb}], got {list(bias.shape)}")
     if K is None:
@@ -269,17 +271,14 @@ def mxfp4_grouped_matmul_act(a, a_scales, b, b_scales, c, group_list=None, act="
     oa = _operand(a, a_scales, a_fmt, a_block)
     ob = _operand(b, b_scales, b_fmt, b_block)
     gl = _group_list(group_list, M, group_list_type)
-    ep = _Epilogue(code, 0, _value(_typed_ptr(bias, torch.float32, "bias")),
-                   nb if bias is not None and bias.dim() == 2 else 0,
-                   _value(_typed_ptr(residual, c.dtype, "residual")), N, _value(_typed_ptr(z, c.dtype, "z")), nb)
-    st = _lib().mxfp4_grouped_matmul_act(M, N, int(K), ctypes.byref(oa), ctypes.byref(ob), _ptr(gl, "i64"),
-                                         0 if gl is None else gl.numel(), int(group_list_type), ctypes.byref(ep),
-                                         1 if c.dtype == torch.float32 else 0, _ptr(c), N, _stream())
-    _check(st, "mxfp4_grouped_matmul_act")
-
-
-def _value(p):
-    return None if p is None else p.value
+    dt, out = c.dtype, (M, N)
+    ep = _Epilogue(code, 0, None if bias is None else _arg(bias, bias.shape, _F32, "bias"),
+                   nb if bias is not None and bias.dim() == 2 else 0, _arg(residual, out, dt, "residual"), N,
+                   _arg(z, (M, nb), dt, "z"), nb)
+    args = (M, N, int(K), ctypes.byref(oa), ctypes.byref(ob), _ptr(gl, "i64"), 0 if gl is None else gl.numel(),
+            int(group_list_type), ctypes.byref(ep), 1 if dt == _F32 else 0, _arg(c, out, dt, "c"), N)
+    _on_gpu(c, bias, residual, z)
+    _check(_lib().mxfp4_grouped_matmul_act(*args, _stream()), "mxfp4_grouped_matmul_act")
 
 
 def mxfp4_act_bwd(grad_c, z, grad_z, act="none", grad_bias=None, group_list=None, group_list_type=1, workspace=None):
@@ -288,12 +287,8 @@ def mxfp4_act_bwd(grad_c, z, grad_z, act="none", grad_bias=None, group_list=None
     tensor of mxfp4_act_bwd_workspace bytes for grad_bias; allocated from torch
     when None."""
     code = _act(act)
-    rows, cols = _matrix(grad_c, "grad_c")
-    zc = cols * (2 if code & 4 else 1)
-    _same_shape(z, (rows, zc), "z")
-    _same_shape(grad_z, (rows, zc), "grad_z")
-    if z is None or grad_z is None:
-        raise ValueError("z and grad_z are required")
+    shape = rows, cols = _matrix(grad_c, "grad_c")
+    dt, zc = grad_c.dtype, cols * (2 if code & 4 else 1)
     gl = _group_list(group_list, rows, group_list_type)
     groups = 0 if gl is None else gl.numel()
     need = 0
@@ -304,8 +299,9 @@ def mxfp4_act_bwd(grad_c, z, grad_z, act="none", grad_bias=None, group_list=None
         if workspace is None:
             workspace = torch.empty(max(need, 4), dtype=torch.uint8, device=grad_c.device)
         _need(workspace, need, "workspace")
-    st = _lib().mxfp4_act_bwd(_dtype(grad_c), code, rows, cols, _ptr(grad_c), _typed_ptr(z, grad_c.dtype, "z"),
-                              _typed_ptr(grad_z, grad_c.dtype, "grad_z"),
-                              _typed_ptr(grad_bias, torch.float32, "grad_bias"), _ptr(gl, "i64"), groups,
-                              int(group_list_type), _ptr(workspace, "u8") if need else None, need, _stream())
-    _check(st, "mxfp4_act_bwd")
+    args = (_dtype(grad_c), code, rows, cols, _arg(grad_c, shape, dt, "grad_c"),
+            _arg(_given(z, "z"), (rows, zc), dt, "z"), _arg(_given(grad_z, "grad_z"), (rows, zc), dt, "grad_z"),
+            None if grad_bias is None else _arg(grad_bias, grad_bias.shape, _F32, "grad_bias"), _ptr(gl, "i64"),
+            groups, int(group_list_type), _ptr(workspace, "u8") if need else None, need)
+    _on_gpu(grad_c, z, grad_z, grad_bias)
+    _check(_lib().mxfp4_act_bwd(*args, _stream()), "mxfp4_act_bwd")
