@@ -63,6 +63,28 @@ __device__ __forceinline__ void with_act(int act, F f) {
   }
 }
 
+// The first n < 8 elements of a 16-byte bf16 piece, as one 8-, one 4- and one
+// 2-byte access (element by element the last column tile of an odd row took
+// 15 us longer than the others).
+__device__ __forceinline__ u32x4 load_part(const uint16_t *p, int n) {
+  typedef uint64_t u64_a2 __attribute__((aligned(2)));
+  typedef uint32_t u32_a2 __attribute__((aligned(2)));
+  const uint64_t four = n & 4 ? *reinterpret_cast<const u64_a2 *>(p) : 0;
+  const uint32_t two = n & 2 ? *reinterpret_cast<const u32_a2 *>(p + (n & 4)) : 0;
+  const uint32_t one = n & 1 ? p[n & 6] : 0;
+  const uint64_t rest = n & 2 ? two | ((uint64_t)one << 32) : one;
+  const uint64_t lo = n & 4 ? four : rest, hi = n & 4 ? rest : 0;
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+__device__ __forceinline__ void store_part(uint16_t *p, u32x4 w, int n) {
+  typedef uint64_t u64_a2 __attribute__((aligned(2)));
+  typedef uint32_t u32_a2 __attribute__((aligned(2)));
+  if (n & 4) *reinterpret_cast<u64_a2 *>(p) = (uint64_t)w.x | ((uint64_t)w.y << 32);
+  const uint32_t t = n & 4 ? w.z : w.x, o = n & 4 ? w.w : w.y;
+  if (n & 2) *reinterpret_cast<u32_a2 *>(p + (n & 4)) = t;
+  if (n & 1) p[n & 6] = (uint16_t)(n & 2 ? o : t);
+}
+
 // The accumulators of a tile of mxgemm_tile.h (row 8(v/4) + 4h + v%4, column
 // l32 of each 32 x 32) to the outputs.  bf16 outputs are staged in LDS, the
 // first half of the rows in the A buffers, the second in the B buffers, and
@@ -109,7 +131,7 @@ __device__ __forceinline__ void act_epilogue(void *c, int64_t ldc, int out_f32, 
   auto pieces = [&](auto width, auto f) {
     constexpr int W = decltype(width)::value, CH = W / 8, RPI = NT / CH;
     const int ch = tid % CH;
-#pragma unroll 2  // the accumulators are live
+#pragma unroll 4
     for (int k = 0; k < BM / RPI; ++k) {
       const int row = tid / CH + RPI * k;
       if (row < mlen) f(row, 8 * ch);
@@ -122,7 +144,7 @@ __device__ __forceinline__ void act_epilogue(void *c, int64_t ldc, int out_f32, 
     if (left >= 8) {
       __builtin_nontemporal_store(*reinterpret_cast<const u32x4 *>(src), reinterpret_cast<u32x4_a2 *>(d));
     } else {
-      for (int e = 0; e < left; ++e) d[e] = reinterpret_cast<const uint16_t *>(src)[e];
+      store_part(d, *reinterpret_cast<const u32x4 *>(src), left);
     }
   };
 
@@ -162,18 +184,31 @@ __device__ __forceinline__ void act_epilogue(void *c, int64_t ldc, int out_f32, 
   }
 
   if (E.res && !out_f32) {
+    // 8 pieces in flight a lane (2 were 5 us slower on a 4096 x 4096 product);
+    // pieces past the edge read the tile's first ones and are not used
+    constexpr int CH = BNO / 8, RPI = NT / CH, AHEAD = BM / RPI < 8 ? BM / RPI : 8;
+    const int sc = 8 * (tid % CH), left = (int)(nlen - sc);
+    const uint16_t *src = static_cast<const uint16_t *>(E.res) + m0 * E.ldr + n0;
     __syncthreads();
-    pieces(ActT<BNO>{}, [&](int row, int sc) {
-      const int left = (int)(nlen - sc);
-      if (left <= 0) return;
-      const uint16_t *src = static_cast<const uint16_t *>(E.res) + (m0 + row) * E.ldr + n0 + sc;
-      uint8_t *d = lds_row(row) + 2 * sc;
-      if (left >= 8) {
-        *reinterpret_cast<u32x4 *>(d) = *reinterpret_cast<const u32x4_a2 *>(src);
-      } else {
-        for (int e = 0; e < left; ++e) reinterpret_cast<uint16_t *>(d)[e] = src[e];
+    for (int k = 0; k < BM / RPI; k += AHEAD) {
+      u32x4 w[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int row = tid / CH + RPI * (k + u);
+        const bool in = row < mlen && left > 0;
+        const uint16_t *p = src + (in ? row * E.ldr + sc : 0);
+        if (left >= 8 || !in) {
+          if (nlen >= 8) w[u] = *reinterpret_cast<const u32x4_a2 *>(p);
+        } else {
+          w[u] = load_part(p, left);
+        }
       }
-    });
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int row = tid / CH + RPI * (k + u);
+        if (row < mlen && left > 0) *reinterpret_cast<u32x4 *>(lds_row(row) + 2 * sc) = w[u];
+      }
+    }
   }
   __syncthreads();
   with_act(E.act, [&](auto a) {

@@ -38,12 +38,13 @@ hipError_t gemm_launch(const GemmArgs &a0, hipStream_t st) {
     // half a round), then, for rows of at most 8 N-tiles, the tail's small
     // tiles: 4 per big tile, at most half a round of big tiles (workgroups
     // without a tile return at once)
-    if (a.total > half || a.tiles_n > 8) {
+    a.row_order = a.tiles_n <= 8;
+    if (a.total > half || !a.row_order) {
       const hipError_t e = gemm_launch_one<AF, BF, false>(a, a.total, st);
       if (e != hipSuccess) return e;
     }
     const int64_t small = 4 * (a.total < half ? a.total : half);
-    return small > 0 && a.tiles_n <= 8 ? gemm_launch_one<AF, BF, true>(a, small, st) : hipSuccess;
+    return small > 0 && a.row_order ? gemm_launch_one<AF, BF, true>(a, small, st) : hipSuccess;
   }
   a.tiles_m = (a.M + BM - 1) / BM;
   a.total = a.tiles_m * a.tiles_n * a.G;

@@ -20,58 +20,58 @@ namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
+
+constexpr int kRowsCT = 2;  // 16-row tiles of B a wave takes
 constexpr int kRowsWaves = 4, kRowsThreads = 64 * kRowsWaves;
 
 // 16 bytes at any alignment of the operand's rows (16, by the checks).
 __device__ __forceinline__ u32x4 ld_u4(const uint8_t *p) { return *reinterpret_cast<const u32x4 *>(p); }
 
-// One turn's codes and scales of a 16-row tile: T4 two pieces (E2M1), else four.
+// One turn's codes and scales of a 16-row tile: two pieces of 16 bytes (E2M1)
+// or four; the scale of the lane's K-block in each of the two steps.
 template <int FMT>
 struct Turn {
   static constexpr int N = FMT == kFmtE2M1 ? 2 : 4;
   u32x4 w[N];
-  uint32_t s[2];  // scale bytes of the two steps' four blocks
+  uint32_t s[2];
 };
 
-// The 8 scale bytes of blocks 8 c .. 8 c + 7 of a row (128-element blocks: one
-// byte stands for four), bytes of blocks at or past kb replaced by 2^0.
-template <bool TAIL>
-__device__ __forceinline__ void load_scales(const uint8_t *row, int64_t c, int64_t kb, int sb, uint32_t (&s)[2]) {
+// B32: blocks of 32, a step's four scale bytes in one word (load_turn), of
+// which lane quarter q takes byte q (scale_of).  Otherwise one byte a lane.
+// TAIL: blocks at or past kb are zero codes with scale 2^0, read in bounds.
+template <int FMT, bool B32, bool TAIL>
+__device__ __forceinline__ void load_turn(Turn<FMT> &T, const uint8_t *base, uint32_t at, const uint8_t *scales,
+                                          uint32_t sat, int64_t c, int64_t kb, int sb, int q) {
   typedef uint32_t u32_a1 __attribute__((aligned(1)));
-  if (!TAIL) {
-    if (!sb) {
-      s[0] = *reinterpret_cast<const u32_a1 *>(row + 8 * c);
-      s[1] = *reinterpret_cast<const u32_a1 *>(row + 8 * c + 4);
+  constexpr int TURN = FMT == kFmtE2M1 ? 128 : 256;  // bytes of a turn
+  const uint8_t *p = base + TURN * c;                // the same for the wave
+#pragma unroll
+  for (int i = 0; i < Turn<FMT>::N; ++i) {
+    const int64_t blk = FMT == kFmtE2M1 ? 8 * c + 4 * i + q : 8 * c + 2 * i + (q >> 1);
+    if (!TAIL) {
+      T.w[i] = ld_u4(p + at + 64 * i);
     } else {
-      s[0] = row[2 * c] * 0x01010101u;
-      s[1] = row[2 * c + 1] * 0x01010101u;
+      const bool in = blk < kb;
+      T.w[i] = ld_u4(in ? p + at + 64 * i : base + (at - 16 * q));
+      if (!in) T.w[i] = u32x4{0u, 0u, 0u, 0u};
     }
-    return;
   }
+  if (B32 && !TAIL) {
+    const uint8_t *r = scales + 8 * c + sat;
+    T.s[0] = *reinterpret_cast<const u32_a1 *>(r);
+    T.s[1] = *reinterpret_cast<const u32_a1 *>(r + 4);
+  } else {
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    s[t] = 0;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int64_t blk = 8 * c + 4 * t + b;
-      s[t] |= (blk < kb ? (uint32_t)row[blk >> sb] : 127u) << (8 * b);
+    for (int t = 0; t < 2; ++t) {
+      const int64_t blk = 8 * c + 4 * t + q;
+      const uint32_t v = scales[sat + ((TAIL && blk >= kb ? 0 : blk) >> sb)];
+      T.s[t] = (TAIL && blk >= kb ? 127u : v) << (B32 ? 8 * q : 0);
     }
   }
 }
-
-template <int FMT, bool TAIL>
-__device__ __forceinline__ void load_turn(Turn<FMT> &T, const uint8_t *codes, const uint8_t *scales, int64_t c,
-                                          int64_t kb, int sb, int q) {
-#pragma unroll
-  for (int i = 0; i < Turn<FMT>::N; ++i) {
-    // piece i: its K offset in the turn's 256, and its block
-    const int64_t k = FMT == kFmtE2M1 ? 256 * c + 128 * i + 32 * q : 256 * c + 64 * i + 16 * q;
-    const bool in = !TAIL || (k >> 5) < kb;
-    const int64_t at = FMT == kFmtE2M1 ? k >> 1 : k;
-    T.w[i] = ld_u4(codes + (in ? at : 0));
-    if (TAIL && !in) T.w[i] = u32x4{0u, 0u, 0u, 0u};
-  }
-  load_scales<TAIL>(scales, c, kb, sb, T.s);
+template <int FMT, bool B32>
+__device__ __forceinline__ int scale_of(const Turn<FMT> &T, int step, int q) {
+  return (int)(B32 ? T.s[step] >> (8 * q) : T.s[step]);
 }
 
 template <int FMT>
@@ -84,6 +84,65 @@ __device__ __forceinline__ v8i operand(const Turn<FMT> &T, int step) {
   return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
+// Row tile tm: its first row and rows (0 or less past the last), and its group.
+// One group needs no walk; its count includes the row_skip rows before P.a.
+template <int MLOG>
+__device__ __forceinline__ int row_tile(const GemmArgs &P, int64_t tm, int64_t *m0, int64_t *mlen) {
+  int g = 0;
+  if (P.gl && P.G > 1) {
+    block_row_uniform<false>(P.gl, P.G, P.list_type, P.M, MLOG, tm, m0, mlen, &g);
+  } else {
+    int64_t m = P.gl ? P.gl[0] - P.row_skip : P.M;
+    m = m < P.M ? m : P.M;
+    *m0 = tm << MLOG;
+    *mlen = m - *m0 < (1 << MLOG) ? m - *m0 : 1 << MLOG;
+  }
+  return g;
+}
+
+// One 16 x 16 tile's values (and its up values) to the outputs: rows m0 ..,
+// of which `rows` are there, columns oc0 .., of which `cols` are.
+template <bool GATED>
+__device__ __forceinline__ void put_tile(const GemmArgs &P, const ActArgs &E, int g, int64_t m0, int64_t rows,
+                                         int64_t oc0, int cols, int lane, v4f z, v4f up) {
+  const int l16 = lane & 15, q = lane >> 4;
+  if (l16 >= cols) return;
+  const int64_t oc = oc0 + l16;
+  if (E.bias) {
+    const float *b = E.bias + (int64_t)g * E.bias_gs + oc;
+    z += b[0];
+    if (GATED) up += b[P.N];
+  }
+  float x[4];
+  with_act(E.act, [&](auto a) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] = act_value<decltype(a)::value>(z[v]);
+  });
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (4 * q + v >= rows) break;
+    const int64_t m = m0 + 4 * q + v;
+    if (GATED) x[v] *= up[v];
+    if (P.out_f32) {
+      if (E.z) {
+        float *zr = static_cast<float *>(E.z) + m * E.ldz + oc;
+        zr[0] = z[v];
+        if (GATED) zr[P.N] = up[v];
+      }
+      if (E.res) x[v] += static_cast<const float *>(E.res)[m * E.ldr + oc];
+      static_cast<float *>(P.c)[m * P.ldc + oc] = x[v];
+    } else {
+      if (E.z) {
+        uint16_t *zr = static_cast<uint16_t *>(E.z) + m * E.ldz + oc;
+        zr[0] = f32_to_bf16_rne(z[v]);
+        if (GATED) zr[P.N] = f32_to_bf16_rne(up[v]);
+      }
+      if (E.res) x[v] += bits_f32((uint32_t)static_cast<const uint16_t *>(E.res)[m * E.ldr + oc] << 16);
+      static_cast<uint16_t *>(P.c)[m * P.ldc + oc] = f32_to_bf16_rne(x[v]);
+    }
+  }
+}
+
 template <int AF, int BF, int MT, int CT>
 struct Turns {
   Turn<AF> a[MT];
@@ -92,42 +151,48 @@ struct Turns {
 
 // EPI as in mxgemm_tile.h.  Gated: B tiles 0 .. CT / 2 - 1 are gate rows, the
 // others the up rows of the same columns.
-template <int AF, int BF, int MT, int CT, int EPI>
-__global__ __launch_bounds__(kRowsThreads) void mxgemm_rows_kernel(GemmArgs P, ActArgs E) {
+//
+// Few waves' worth of columns: the four waves of a workgroup share the K of
+// one column run (16 H columns, H tiles of output columns), in turns of 256.
+template <int AF, int BF, bool B32, int MT, int CT, int EPI>
+__global__ __launch_bounds__(kRowsThreads, (MT == 1 ? 4 : 2)) void mxgemm_rows_split_kernel(GemmArgs P, ActArgs E) {
   constexpr bool GATED = EPI == 2;
-  constexpr int H = GATED ? CT / 2 : CT;  // tiles of output columns
+  constexpr int H = GATED ? CT / 2 : CT;
   constexpr int MLOG = MT == 1 ? 4 : MT == 2 ? 5 : 6;
+  constexpr int KS = kRowsWaves;
   __shared__ v4f red[kRowsWaves][MT][CT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int l16 = lane & 15, q = lane >> 4;
 
   const int64_t tm = blockIdx.x % P.tiles_m, tn = blockIdx.x / P.tiles_m;
   int64_t m0, mlen;
-  int g = 0;
-  if (P.gl) {
-    block_row_uniform<false>(P.gl, P.G, P.list_type, P.M, MLOG, tm, &m0, &mlen, &g);
-  } else {
-    m0 = tm << MLOG;
-    mlen = P.M - m0 < 16 * MT ? P.M - m0 : 16 * MT;
-  }
+  const int g = row_tile<MLOG>(P, tm, &m0, &mlen);
   if (mlen <= 0) return;  // the same for the workgroup
   const int64_t n0 = tn * 16 * H;
   const int nlen = (int)(P.N - n0 < 16 * H ? P.N - n0 : 16 * H);
   const int64_t kb = P.K >> 5;
 
-  const uint8_t *ac[MT], *as[MT], *bc[CT], *bs[CT];
+  // wave-uniform bases and 32-bit lane offsets
+  const uint8_t *ab = P.a + m0 * P.lda, *asb = P.as + m0 * P.ldas;
+  uint32_t ao[MT], aso[MT], bo[CT], bso[CT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int r = 16 * i + l16 < (int)mlen ? 16 * i + l16 : (int)mlen - 1;
-    ac[i] = P.a + (m0 + r) * P.lda;
-    as[i] = P.as + (m0 + r) * P.ldas;
+    ao[i] = (uint32_t)r * (uint32_t)P.lda + 16 * q;
+    aso[i] = (uint32_t)r * (uint32_t)P.ldas;
+  }
+  const uint8_t *bb[GATED ? 2 : 1], *bsb[GATED ? 2 : 1];
+#pragma unroll
+  for (int p = 0; p < (GATED ? 2 : 1); ++p) {
+    bb[p] = P.b + (int64_t)g * P.b_gs + (n0 + p * P.N) * P.ldb;
+    bsb[p] = P.bs + (int64_t)g * P.b_gss + (n0 + p * P.N) * P.ldbs;
   }
 #pragma unroll
   for (int j = 0; j < CT; ++j) {
-    const int col = 16 * (j % H) + l16 < nlen ? 16 * (j % H) + l16 : nlen - 1;
-    const int64_t r = n0 + col + (j >= H ? P.N : 0);
-    bc[j] = P.b + (int64_t)g * P.b_gs + r * P.ldb;
-    bs[j] = P.bs + (int64_t)g * P.b_gss + r * P.ldbs;
+    int col = 16 * (j % H) + l16;
+    col = col < nlen ? col : nlen - 1;
+    bo[j] = (uint32_t)col * (uint32_t)P.ldb + 16 * q;
+    bso[j] = (uint32_t)col * (uint32_t)P.ldbs;
   }
 
   v4f acc[MT][CT];
@@ -140,35 +205,46 @@ __global__ __launch_bounds__(kRowsThreads) void mxgemm_rows_kernel(GemmArgs P, A
   auto load = [&](T &t, int64_t c, auto tail) {
     constexpr bool TAIL = decltype(tail)::value;
 #pragma unroll
-    for (int j = 0; j < CT; ++j) load_turn<BF, TAIL>(t.b[j], bc[j], bs[j], c, kb, P.b_sb, q);
+    for (int j = 0; j < CT; ++j)
+      load_turn<BF, B32, TAIL>(t.b[j], bb[j / H], bo[j], bsb[j / H], bso[j], c, kb, P.b_sb, q);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) load_turn<AF, TAIL>(t.a[i], ac[i], as[i], c, kb, P.a_sb, q);
+    for (int i = 0; i < MT; ++i) load_turn<AF, B32, TAIL>(t.a[i], ab, ao[i], asb, aso[i], c, kb, P.a_sb, q);
   };
   auto multiply = [&](const T &t) {
+    __builtin_amdgcn_sched_barrier(0);  // the next turn's loads stay before, the one after's behind
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int j = 0; j < CT; ++j) {
         const v8i b = operand<BF>(t.b[j], s);
-        const int sb = (int)(t.b[j].s[s] >> (8 * q));
+        const int sb = scale_of<BF, B32>(t.b[j], s, q);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              operand<AF>(t.a[i], s), b, acc[i][j], AF, BF, 0, (int)(t.a[i].s[s] >> (8 * q)), 0, sb);
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand<AF>(t.a[i], s), b, acc[i][j], AF, BF, 0,
+                                                                       scale_of<AF, B32>(t.a[i], s, q), 0, sb);
       }
+    __builtin_amdgcn_sched_barrier(0);
   };
-  const int64_t full = kb >> 3;  // whole turns
-  T cur, next;
-  int64_t c = wave;
-  if (c < full) load(cur, c, std::false_type{});
-  for (; c < full; c += kRowsWaves) {
-    if (c + kRowsWaves < full) load(next, c + kRowsWaves, std::false_type{});
-    multiply(cur);
-    cur = next;
+  // turns wave, wave + KS, ...: two sets of registers, each loaded while the
+  // other multiplies (past the last turn the last one is loaded again, unused)
+  const int full = (int)(kb >> 3);  // whole turns
+  const int mine = (full - wave + KS - 1) / KS;
+  T t0, t1;
+  if (mine > 0) {
+    auto turn = [&](int i) { return (int64_t)(wave + KS * (i < mine ? i : mine - 1)); };
+    load(t0, turn(0), std::false_type{});
+    int i = 0;
+    for (; i + 1 < mine; i += 2) {
+      load(t1, turn(i + 1), std::false_type{});
+      multiply(t0);
+      load(t0, turn(i + 2), std::false_type{});
+      multiply(t1);
+    }
+    if (i < mine) multiply(t0);
   }
-  if ((kb & 7) && full % kRowsWaves == wave) {
-    load(cur, full, std::true_type{});
-    multiply(cur);
+  if ((kb & 7) && full % KS == wave) {
+    load(t0, full, std::true_type{});
+    multiply(t0);
   }
 
 #pragma unroll
@@ -177,82 +253,234 @@ __global__ __launch_bounds__(kRowsThreads) void mxgemm_rows_kernel(GemmArgs P, A
     for (int j = 0; j < CT; ++j) red[wave][i][j][lane] = acc[i][j];
   __syncthreads();
 
-  // Wave w takes the (row tile, column tile) pairs w, w + 4, ...
-  auto total = [&](int i, int j) {
-    v4f s = red[0][i][j][lane];
-#pragma unroll
-    for (int w = 1; w < kRowsWaves; ++w) s += red[w][i][j][lane];
-    return s;
-  };
+  // the waves take the run's (row tile, column tile) pairs in turn
   for (int u = wave; u < MT * H; u += kRowsWaves) {
     const int i = u / H, j = u % H;
-    const int col = 16 * j + l16;
-    if (col >= nlen) continue;
-    const int64_t oc = n0 + col;
-    v4f z = total(i, j), up = GATED ? total(i, (j + H) % CT) : v4f{};
-    if (E.bias) {
-      const float *b = E.bias + (int64_t)g * E.bias_gs + oc;
-      z += b[0];
-      if (GATED) up += b[P.N];
-    }
+    auto total = [&](int jj) {
+      v4f s = red[0][i][jj][lane];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int row = 16 * i + 4 * q + v;
-      if (row >= mlen) break;
-      const int64_t m = m0 + row;
-      if (E.z) {
-        if (P.out_f32) {
-          float *zr = static_cast<float *>(E.z) + m * E.ldz + oc;
-          zr[0] = z[v];
-          if (GATED) zr[P.N] = up[v];
-        } else {
-          uint16_t *zr = static_cast<uint16_t *>(E.z) + m * E.ldz + oc;
-          zr[0] = f32_to_bf16_rne(z[v]);
-          if (GATED) zr[P.N] = f32_to_bf16_rne(up[v]);
-        }
-      }
-      float x = 0.0f;
-      with_act(E.act, [&](auto a) { x = act_value<decltype(a)::value>(z[v]); });
-      if (GATED) x *= up[v];
-      if (P.out_f32) {
-        if (E.res) x += static_cast<const float *>(E.res)[m * E.ldr + oc];
-        static_cast<float *>(P.c)[m * P.ldc + oc] = x;
-      } else {
-        if (E.res) x += bits_f32((uint32_t)static_cast<const uint16_t *>(E.res)[m * E.ldr + oc] << 16);
-        static_cast<uint16_t *>(P.c)[m * P.ldc + oc] = f32_to_bf16_rne(x);
-      }
-    }
+      for (int w = 1; w < kRowsWaves; ++w) s += red[w][i][jj][lane];
+      return s;
+    };
+    put_tile<GATED>(P, E, g, m0 + 16 * i, mlen - 16 * i, n0 + 16 * j, nlen - 16 * j, lane, total(j),
+                    GATED ? total((j + H) % CT) : v4f{});
   }
 }
 
-template <int AF, int BF, int MT, int EPI>
-hipError_t rows_one(const GemmArgs &a0, const ActArgs &e, hipStream_t st) {
-  constexpr int CT = 2, H = EPI == 2 ? CT / 2 : CT;
-  GemmArgs a = a0;
+// More columns: every wave takes the whole K of a column run of its own, and
+// the A rows, which the four runs share, pass through LDS in slabs of SL turns
+// (double-buffered; a lane's fragment is two 16-byte reads), so that the
+// memory pipeline of a CU carries B almost alone.
+template <int AF, int BF, bool B32, int MT, int CT, int SL, int EPI>
+__global__ __launch_bounds__(kRowsThreads, (MT == 4 ? 2 : 4)) void mxgemm_rows_kernel(GemmArgs P, ActArgs E) {
+  constexpr bool GATED = EPI == 2;
+  constexpr int H = GATED ? CT / 2 : CT;
+  constexpr int MLOG = MT == 1 ? 4 : MT == 2 ? 5 : 6;
+  constexpr int ROWS = 16 * MT, RSTR = 256 * SL + 16;  // bytes of a slab's row in LDS: 16 rows' pieces on all banks
+  constexpr int LD = ROWS * 16 * SL / kRowsThreads;     // 16-byte pieces a thread stages
+  static_assert(ROWS * 16 * SL % kRowsThreads == 0 && SL % 2 == 0, "slab");
+  __shared__ __align__(16) uint8_t sa[2][ROWS * RSTR];
+  __shared__ __align__(16) uint8_t ss[2][ROWS * 8 * SL];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, q = lane >> 4;
+
+  const int64_t tm = blockIdx.x % P.tiles_m, tn = blockIdx.x / P.tiles_m;
+  int64_t m0, mlen64;
+  const int g = row_tile<MLOG>(P, tm, &m0, &mlen64);
+  const int mlen = (int)mlen64;
+  if (mlen <= 0) return;  // the same for the workgroup
+  const int64_t n0 = (tn * kRowsWaves + wave) * 16 * H;
+  const int nlen = (int)(P.N - n0 < 16 * H ? P.N - n0 : 16 * H);  // 0 or less: the wave only helps to stage
+  const int64_t kb = P.K >> 5;
+
+  const int64_t nb0 = nlen > 0 ? n0 : 0;
+  const uint8_t *bb[GATED ? 2 : 1], *bsb[GATED ? 2 : 1];
+  uint32_t bo[CT], bso[CT];
+#pragma unroll
+  for (int p = 0; p < (GATED ? 2 : 1); ++p) {
+    bb[p] = P.b + (int64_t)g * P.b_gs + (nb0 + p * P.N) * P.ldb;
+    bsb[p] = P.bs + (int64_t)g * P.b_gss + (nb0 + p * P.N) * P.ldbs;
+  }
+#pragma unroll
+  for (int j = 0; j < CT; ++j) {
+    int col = 16 * (j % H) + l16;
+    col = col < nlen ? col : (nlen > 0 ? nlen - 1 : 0);
+    bo[j] = (uint32_t)col * (uint32_t)P.ldb + 16 * q;
+    bso[j] = (uint32_t)col * (uint32_t)P.ldbs;
+  }
+  struct BTurn {
+    Turn<BF> b[CT];
+  };
+  auto load_b = [&](BTurn &t, int64_t c, auto tail) {
+    constexpr bool TAIL = decltype(tail)::value;
+#pragma unroll
+    for (int j = 0; j < CT; ++j)
+      load_turn<BF, B32, TAIL>(t.b[j], bb[j / H], bo[j], bsb[j / H], bso[j], c, kb, P.b_sb, q);
+  };
+
+  // A slab s (turns SL s ..): thread's pieces into registers, then into LDS.
+  // Pieces past K are zero codes, blocks past K have scale 2^0; rows past the
+  // tile's stay as they are (they reach only outputs that are not stored).
+  u32x4 ra[LD];
+  uint32_t rs[(ROWS * 2 * SL + kRowsThreads - 1) / kRowsThreads];
+  constexpr int SW = ROWS * 2 * SL;  // scale words of a slab: two a row and turn
+  const uint8_t *arow = P.a + m0 * P.lda, *asrow = P.as + m0 * P.ldas;
+  auto fetch = [&](int64_t s) {
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const int idx = tid + kRowsThreads * i, row = idx / (16 * SL), piece = idx % (16 * SL);
+      const int64_t k = 256 * SL * s + 16 * piece;
+      const bool in = row < mlen && k < P.K;
+      ra[i] = ld_u4(arow + (in ? (int64_t)row * P.lda + k : 0));
+      if (!in) ra[i] = u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int i = 0; i < (SW + kRowsThreads - 1) / kRowsThreads; ++i) {
+      const int idx = tid + kRowsThreads * i, row = idx / (2 * SL), word = idx % (2 * SL);
+      const int64_t blk = 8 * SL * s + 4 * word;
+      rs[i] = 0x7F7F7F7Fu;
+      if (idx < SW && row < mlen && blk < kb) {
+        const uint8_t *r = asrow + (int64_t)row * P.ldas;
+        typedef uint32_t u32_a1 __attribute__((aligned(1)));
+        if (B32 && blk + 4 <= kb) {
+          rs[i] = *reinterpret_cast<const u32_a1 *>(r + blk);
+        } else {
+          uint32_t v = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v |= (blk + e < kb ? (uint32_t)r[(blk + e) >> P.a_sb] : 127u) << (8 * e);
+          rs[i] = v;
+        }
+      }
+    }
+  };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const int idx = tid + kRowsThreads * i, row = idx / (16 * SL), piece = idx % (16 * SL);
+      *reinterpret_cast<u32x4 *>(&sa[buf][row * RSTR + 16 * piece]) = ra[i];
+    }
+#pragma unroll
+    for (int i = 0; i < (SW + kRowsThreads - 1) / kRowsThreads; ++i) {
+      const int idx = tid + kRowsThreads * i;
+      if (idx < SW) *reinterpret_cast<uint32_t *>(&ss[buf][4 * idx]) = rs[i];
+    }
+  };
+
+  v4f acc[MT][CT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < CT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](const BTurn &t, int buf, int u) {  // turn u of the slab in buf
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      v8i a[MT];
+      int sca[MT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const uint8_t *r = &sa[buf][(16 * i + l16) * RSTR + 256 * u + 128 * s + 16 * q];
+        const u32x4 lo = *reinterpret_cast<const u32x4 *>(r), hi = *reinterpret_cast<const u32x4 *>(r + 64);
+        a[i] = v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+        sca[i] = (int)ss[buf][(16 * i + l16) * 8 * SL + 8 * u + 4 * s + q];
+      }
+#pragma unroll
+      for (int j = 0; j < CT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[i], operand<BF>(t.b[j], s), acc[i][j], AF, BF, 0,
+                                                                       sca[i], 0, scale_of<BF, B32>(t.b[j], s, q));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  const int full = (int)(kb >> 3), turns = (int)((kb + 7) >> 3);
+  const int slabs = (turns + SL - 1) / SL;
+  BTurn t0, t1;
+  auto upto = [&](int c) { return (int64_t)(c < full ? c : full - 1); };
+  fetch(0);
+  if (full > 0) load_b(t0, 0, std::false_type{});
+  stage(0);
+  __syncthreads();
+  for (int s = 0; s < slabs; ++s) {
+    const int buf = s & 1;
+    if (s + 1 < slabs) fetch(s + 1);
+#pragma unroll
+    for (int u = 0; u < SL; u += 2) {
+      const int c = SL * s + u;
+      if (c < full) {
+        load_b(t1, upto(c + 1), std::false_type{});
+        multiply(t0, buf, u);
+        if (c + 1 < full) {
+          load_b(t0, upto(c + 2), std::false_type{});
+          multiply(t1, buf, u + 1);
+        }
+      }
+    }
+    if (s + 1 < slabs) {
+      stage(buf ^ 1);  // read last before the previous barrier
+      __syncthreads();
+    }
+  }
+  if (turns > full) {  // the partial last turn, in the last slab
+    load_b(t0, full, std::true_type{});
+    const int u = full - SL * (slabs - 1);
+    multiply(t0, (slabs - 1) & 1, u);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < H; ++j)
+      put_tile<GATED>(P, E, g, m0 + 16 * i, mlen - 16 * i, n0 + 16 * j, nlen - 16 * j, lane, acc[i][j],
+                      acc[i][(j + H) % CT]);
+}
+
+template <int AF, int BF, bool B32, int MT, int EPI>
+hipError_t rows_one(GemmArgs a, const ActArgs &e, hipStream_t st) {
+  constexpr int CT = kRowsCT, H = EPI == 2 ? CT / 2 : CT, COLS = 16 * H, SL = MT == 1 ? 4 : 2;
   // upper bound of the row tiles: every group adds at most one partial tile,
   // and no tile is empty
   const int64_t whole = a.M / (16 * MT) + (a.gl ? a.G : (a.M % (16 * MT) ? 1 : 0));
   a.tiles_m = whole < a.M ? whole : a.M;
-  a.tiles_n = (a.N + 16 * H - 1) / (16 * H);
+  const int64_t runs = (a.N + COLS - 1) / COLS;
+  // Shared K below 4096 runs (4 waves a SIMD): 8 experts of one row, 7168 ->
+  // 2 x 2048 (1024 runs), 26 us against 29; 32 groups, 2048 -> 7168 (about
+  // 7600 runs), 127 us against 71.
+  const bool split = a.tiles_m * runs < 4096;
+  a.tiles_n = split ? runs : (runs + kRowsWaves - 1) / kRowsWaves;
   a.total = a.tiles_m * a.tiles_n;
   if (a.total > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((mxgemm_rows_kernel<AF, BF, MT, CT, EPI>), dim3((unsigned)a.total), dim3(kRowsThreads), 0, st, a, e);
+  const dim3 grid((unsigned)a.total), block(kRowsThreads);
+  if (split)
+    hipLaunchKernelGGL((mxgemm_rows_split_kernel<AF, BF, B32, MT, CT, EPI>), grid, block, 0, st, a, e);
+  else
+    hipLaunchKernelGGL((mxgemm_rows_kernel<AF, BF, B32, MT, CT, SL, EPI>), grid, block, 0, st, a, e);
   return hipGetLastError();
 }
 
-template <int AF, int BF, int EPI>
+template <int AF, int BF, bool B32, int EPI>
 hipError_t rows_mt(const GemmArgs &a, const ActArgs &e, int mt, hipStream_t st) {
-  if (mt == 1) return rows_one<AF, BF, 1, EPI>(a, e, st);
-  if (mt == 2) return rows_one<AF, BF, 2, EPI>(a, e, st);
-  return rows_one<AF, BF, 4, EPI>(a, e, st);
+  if (mt == 1) return rows_one<AF, BF, B32, 1, EPI>(a, e, st);
+  if (mt == 2) return rows_one<AF, BF, B32, 2, EPI>(a, e, st);
+  return rows_one<AF, BF, B32, 4, EPI>(a, e, st);
+}
+template <int AF, int BF, int EPI>
+hipError_t rows_b32(const GemmArgs &a, const ActArgs &e, int mt, hipStream_t st) {
+  return a.a_sb || a.b_sb ? rows_mt<AF, BF, false, EPI>(a, e, mt, st) : rows_mt<AF, BF, true, EPI>(a, e, mt, st);
 }
 
 template <int EPI>
-hipError_t rows_any(const GemmLaunch &L, const ActArgs &e, int mt, hipStream_t st) {
-  const GemmArgs a = gemm_args(L);
+hipError_t rows_any(const GemmLaunch &L, const ActArgs &e, int mt, int64_t skip, hipStream_t st) {
+  GemmArgs a = gemm_args(L);
+  a.row_skip = skip;
   if (L.a_fmt == kFmtE4M3)
-    return L.b_fmt == kFmtE2M1 ? rows_mt<kFmtE4M3, kFmtE2M1, EPI>(a, e, mt, st) : rows_mt<kFmtE4M3, kFmtE4M3, EPI>(a, e, mt, st);
-  return L.b_fmt == kFmtE2M1 ? rows_mt<kFmtE5M2, kFmtE2M1, EPI>(a, e, mt, st) : rows_mt<kFmtE5M2, kFmtE4M3, EPI>(a, e, mt, st);
+    return L.b_fmt == kFmtE2M1 ? rows_b32<kFmtE4M3, kFmtE2M1, EPI>(a, e, mt, st) : rows_b32<kFmtE4M3, kFmtE4M3, EPI>(a, e, mt, st);
+  return L.b_fmt == kFmtE2M1 ? rows_b32<kFmtE5M2, kFmtE2M1, EPI>(a, e, mt, st) : rows_b32<kFmtE5M2, kFmtE4M3, EPI>(a, e, mt, st);
+}
+
+// mt: 16-row tiles a workgroup takes; skip: rows of the (one) group before L's first.
+hipError_t rows_act(const GemmLaunch &L, const ActArgs &e, bool gated, int mt, int64_t skip, hipStream_t st) {
+  return gated ? rows_any<2>(L, e, mt, skip, st) : rows_any<1>(L, e, mt, skip, st);
 }
 
 }  // namespace
@@ -261,9 +489,32 @@ hipError_t launch_gemm_act(const GemmLaunch &L, const ActArgs &e, bool gated, hi
   // rows an average group has, of the groups that can have any
   const int64_t groups = L.num_groups < L.M ? L.num_groups : L.M;
   const int64_t avg = (L.M + groups - 1) / groups;
-  if (avg > 64) return gated ? launch_gated_tiles(L, e, st) : launch_act_tiles(L, e, st);
-  const int mt = avg <= 8 ? 1 : avg <= 24 ? 2 : 4;
-  return gated ? rows_any<2>(L, e, mt, st) : rows_any<1>(L, e, mt, st);
+  // The few-rows form up to 64: 32 groups, 2048 -> 7168, it took 71 us with 6
+  // rows a group on average, 108 with 25, 157 with 50 and 257 with 100, the
+  // tiles 198 - 210 at each; one group of 64 / 128 / 256 rows 15 / 23 / 44 us
+  // against 22 / 25 / 26.  Row tiles by the same runs (16 / 32 / 64 rows a
+  // workgroup): 71 / 81 / 95 us at 6 rows, 119 / 108 / 121 at 25; gated, 7168
+  // -> 2048, 351 / 271 / 193 at 50.
+  if (avg <= 64) return rows_act(L, e, gated, avg <= 8 ? 1 : avg <= 24 ? 2 : 4, 0, st);
+  // One group whose last row tile has few rows: a launch of its own for them,
+  // where that tile would cost a share of a round (4099 x 4095 x 4096: 133 us
+  // as 17 row tiles, the last 16 of them in the tail launch).
+  const int64_t rest = L.M % 256, whole = L.M - rest;
+  if (L.num_groups != 1 || rest == 0 || rest > 64 || whole == 0 || whole / 256 * ((L.N + 255) / 256) > 1024)
+    return gated ? launch_gated_tiles(L, e, st) : launch_act_tiles(L, e, st);
+  GemmLaunch T = L;
+  T.M = whole;
+  const hipError_t r = gated ? launch_gated_tiles(T, e, st) : launch_act_tiles(T, e, st);
+  if (r != hipSuccess) return r;
+  const int64_t es = L.out_f32 ? 4 : 2;
+  T.M = rest;
+  T.a += whole * L.lda;
+  T.as += whole * L.ldas;
+  T.c = static_cast<uint8_t *>(L.c) + whole * L.ldc * es;
+  ActArgs t = e;
+  if (e.res) t.res = static_cast<const uint8_t *>(e.res) + whole * e.ldr * es;
+  if (e.z) t.z = static_cast<uint8_t *>(e.z) + whole * e.ldz * es;
+  return rows_act(T, t, gated, rest <= 16 ? 1 : rest <= 32 ? 2 : 4, whole, st);
 }
 
 }  // namespace mxfp4

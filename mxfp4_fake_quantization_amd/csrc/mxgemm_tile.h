@@ -97,7 +97,9 @@ struct GemmArgs {
   int s4;                // both scale arrays have dword-aligned rows: dword slice loads
   int c16;               // bf16 output with 16-byte aligned rows: whole tiles stored through LDS
   int ncu;               // compute units of the device (row-split tail decision)
+  int row_order;         // row-split tiles in row order with a tail launch, else in bands
   int64_t tiles_m, tiles_n, total;
+  int64_t row_skip;      // few-rows form, one group: its rows before a
 };
 
 typedef const uint8_t __attribute__((address_space(1))) *gp8;
@@ -191,7 +193,7 @@ __device__ __forceinline__ void mxgemm_tile(const GemmArgs &P, const ActArgs &E)
     // time unchanged), dealt by xcd_tile, with no tail launch: the tail
     // split measured 2 % slower there (NT on the MoE layer 526 -> 537 us).
     int64_t v, sub = 0, tm, tn;
-    if (P.tiles_n <= 8) {
+    if (P.row_order) {
       int64_t rm;
       if (P.gl) {
         int64_t before, last;
@@ -318,15 +320,18 @@ __device__ __forceinline__ void mxgemm_tile(const GemmArgs &P, const ActArgs &E)
                            (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)sbp));
   const uint32_t s_ld = (uint32_t)__builtin_amdgcn_readfirstlane((int)(sl_b ? P.ldbs : P.ldas));
   const int s_rows = __builtin_amdgcn_readfirstlane((int)(sl_b ? nlen : mlen));
+  const int s_gated = GATED ? __builtin_amdgcn_readfirstlane(sl_b ? 1 : 0) : 0;
+  const uint64_t s_up = GATED ? (uint64_t)P.N * (uint64_t)P.ldbs : 0;
   // A slice is loaded one step before it is stored (pv: loaded during the
   // previous step, pc: its bytes as one dword, being stored), so that the
   // step's last wait for its loads does not wait for the scattered scale rows.
   uint32_t pv[S4 ? 1 : 4], pc;
   auto load_slice = [&](int64_t chunk, int piece) {
-    const int rw = piece * (NT / 8) + sr;
-    const int row = GATED && sl_b ? (int)gated_row(piece, sr) : (rw < s_rows ? rw : s_rows - 1);
+    // gated B: pieces alternate between the gate and the up rows, a scalar apart
+    const int rw = (GATED ? piece >> s_gated : piece) * (NT / 8) + sr;
+    const int row = rw < s_rows ? rw : s_rows - 1;
     const int pbyte = (int)((kb0 + 16 * chunk) >> sb_log) + (sb_log ? 0 : 4 * sd);
-    const gp8 rp = s_base + (uint32_t)row * s_ld;
+    const gp8 rp = (GATED ? s_base + (piece & s_gated) * s_up : s_base) + (uint32_t)row * s_ld;
     const int at = pbyte < s_hi ? pbyte : s_hi - 1;  // in bounds (s_hi <= row length)
     if (S4) {
       pv[0] = *(gp32)(rp + (at & ~3));

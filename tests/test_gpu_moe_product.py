@@ -174,6 +174,16 @@ def test_many_rows_exact(n, dtype):
          dtype=dtype)
 
 
+# one group whose last rows have a launch of their own, and a list that ends
+# before, inside and after them
+@pytest.mark.parametrize("rows,counts,list_type", [
+    (257, [257], 1), (300, [300], 0), (300, [299], 1), (320, [256], 1), (320, [250], 0), (272, [260], 1), (290, [0], 1),
+    (528, [513], 0)])
+@pytest.mark.parametrize("act", ["none", "geglu"])
+def test_one_group_with_few_last_rows(rows, counts, list_type, act):
+    case(rows, counts, rows, 320, 67, act, bias="groups", res=True, keep_z=True, dtype="bf16", list_type=list_type)
+
+
 @pytest.mark.parametrize("rows,counts", [(6, [2, 0, 4]), (70, [30, 40]), (330, [200, 130])])
 @pytest.mark.parametrize("a_fmt,b_fmt,a_block,b_block", [
     ("e5m2", "e2m1", 32, 32), ("e4m3", "e4m3", 32, 32), ("e4m3", "e2m1", 128, 128), ("e5m2", "e4m3", 128, 32),
