@@ -5,11 +5,12 @@
 //   dup = dc act(gate);   dbias_g = the sum of group g's rows of dz in fp32.
 //   silu' = s (1 + x (1 - s)), s = 1 / (1 + exp(-x));  gelu' = Phi(x) + x phi(x)
 //
-// A workgroup takes a run of consecutive rows (of one group: the runs
-// restart at every group start, as the grouped quantizers' blocks do) and up to 2048 columns, 8 a lane; narrower rows go
-// side by side.  Each lane keeps its columns' sums, the lanes of a column meet
-// in LDS, and a second launch adds the runs' sums in order: no atomics, the
-// same bits every time.  Bound by the bytes of z, dc and dz.
+// A workgroup takes a run of consecutive rows (of one group: the runs restart
+// at every group start, as the grouped quantizers' blocks do) and 256 columns,
+// 8 a lane, its rows eight at a time.  Each lane keeps its columns' sums, the
+// lanes of a column meet in LDS, and a second launch adds the runs' sums in
+// order: no atomics, the same bits every time.  Bound by the bytes of z, dc and
+// dz.
 #include "moe_kernels.h"
 #include "mxfp4_groups.h"
 #include "mxgemm_act.h"
@@ -18,7 +19,11 @@ namespace mxfp4 {
 namespace {
 
 constexpr int kActBwdThreads = 256;
-constexpr int kRunLog = 6;  // rows of a run
+// Rows of a run and lanes side by side (8 columns each), logarithms.  Small
+// pieces spread evenly over the CUs: swiglu with bias on 32768 x 2 x 2048 takes
+// 138 us (4.9 TB/s); 64-row runs 146, 64 lanes 151, 256 lanes of 64-row runs
+// (two workgroups a CU and a few more) 176.
+constexpr int kRunLog = 5, kColsLog = 5;
 
 struct ActBwdArgs {
   const uint8_t *dc, *z;
@@ -174,7 +179,7 @@ hipError_t launch_act_bwd(const ActBwdLaunch &L, hipStream_t st) {
   a.G = L.num_groups;
   a.list_type = L.list_type;
   a.act = L.act & 3;
-  while (a.tx_log < 8 && (int64_t)(8 << a.tx_log) < L.cols) ++a.tx_log;
+  while (a.tx_log < kColsLog && (int64_t)(8 << a.tx_log) < L.cols) ++a.tx_log;
   a.ctiles = (L.cols + (8 << a.tx_log) - 1) / (8 << a.tx_log);
   const int64_t runs = a.gl ? runs_of(L.rows, L.num_groups) : (L.rows + (1 << kRunLog) - 1) >> kRunLog;
   const int64_t grid = runs * a.ctiles;

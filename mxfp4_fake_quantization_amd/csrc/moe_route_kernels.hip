@@ -459,8 +459,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(RouteBwdArgs A
       words w;
 #pragma unroll
       for (int j = 0; j < P::PW; ++j)
-        w[j] = DT == kBF16 ? f32_to_bf16_rne(o[(q * P::PE + 2 * j) % V]) |
-                                ((uint32_t)f32_to_bf16_rne(o[(q * P::PE + 2 * j + 1) % V]) << 16)
+        w[j] = DT == kBF16 ? pack_bf16(o[(q * P::PE + 2 * j) % V], o[(q * P::PE + 2 * j + 1) % V])
                            : fbits(o[(q * P::PE + j) % V]);
       *reinterpret_cast<words *>(A.gl + (row + e0 + q * P::PE) * P::ES) = w;
     }
@@ -468,7 +467,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(RouteBwdArgs A
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (j >= cnt) break;
-      if (DT == kBF16) reinterpret_cast<uint16_t *>(A.gl)[row + e0 + j] = f32_to_bf16_rne(o[j]);
+      if (DT == kBF16) reinterpret_cast<uint16_t *>(A.gl)[row + e0 + j] = (uint16_t)pack_bf16(o[j], 0.0f);
       else reinterpret_cast<float *>(A.gl)[row + e0 + j] = o[j];
     }
   }

@@ -13,6 +13,14 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   return (uint16_t)(u >> 16);
 }
 
+// Two values rounded to bf16 (nearest even) by the hardware conversion, a in
+// the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
 // Rows of any length start at any element: 16-byte accesses with the
 // element's alignment (the hardware takes unaligned global accesses).
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
@@ -72,7 +80,7 @@ template <int DT>
 __device__ __forceinline__ void pack8(uint32_t (&w)[Row8<DT>::NW], const float (&f)[8]) {
 #pragma unroll
   for (int j = 0; j < Row8<DT>::NW; ++j)
-    w[j] = DT == kBF16 ? f32_to_bf16_rne(f[(2 * j) % 8]) | ((uint32_t)f32_to_bf16_rne(f[(2 * j + 1) % 8]) << 16)
+    w[j] = DT == kBF16 ? pack_bf16(f[(2 * j) % 8], f[(2 * j + 1) % 8])
                        : __builtin_bit_cast(uint32_t, f[j % 8]);
 }
 

@@ -157,7 +157,7 @@ __device__ __forceinline__ void act_epilogue(void *c, int64_t ldc, int out_f32, 
         for (int j = 0; j < WN; ++j)
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
-            *reinterpret_cast<uint16_t *>(mine + 2 * wc0 + tile_row(i, v) * OS + 64 * j) = f32_to_bf16_rne(acc[i][j][v]);
+            *reinterpret_cast<uint16_t *>(mine + 2 * wc0 + tile_row(i, v) * OS + 64 * j) = (uint16_t)pack_bf16(acc[i][j][v], 0.0f);
             if ((v & 3) == 3) __builtin_amdgcn_sched_barrier(0);
           }
       __syncthreads();
@@ -226,7 +226,7 @@ __device__ __forceinline__ void act_epilogue(void *c, int64_t ldc, int out_f32, 
             uint16_t *at = reinterpret_cast<uint16_t *>(mine + 2 * oc0 + tile_row(i, v) * OS + 64 * j);
             // places past the tile's edge hold what was there before, and are not stored
             if (E.res) x += bits_f32((uint32_t)*at << 16);
-            *at = f32_to_bf16_rne(x);
+            *at = (uint16_t)pack_bf16(x, 0.0f);
           } else {
             const int row = row0 + tile_row(i, v);
             if (row < mlen && col < nlen) {

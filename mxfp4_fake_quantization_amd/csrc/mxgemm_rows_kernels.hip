@@ -134,11 +134,11 @@ __device__ __forceinline__ void put_tile(const GemmArgs &P, const ActArgs &E, in
     } else {
       if (E.z) {
         uint16_t *zr = static_cast<uint16_t *>(E.z) + m * E.ldz + oc;
-        zr[0] = f32_to_bf16_rne(z[v]);
-        if (GATED) zr[P.N] = f32_to_bf16_rne(up[v]);
+        zr[0] = (uint16_t)pack_bf16(z[v], 0.0f);
+        if (GATED) zr[P.N] = (uint16_t)pack_bf16(up[v], 0.0f);
       }
       if (E.res) x[v] += bits_f32((uint32_t)static_cast<const uint16_t *>(E.res)[m * E.ldr + oc] << 16);
-      static_cast<uint16_t *>(P.c)[m * P.ldc + oc] = f32_to_bf16_rne(x[v]);
+      static_cast<uint16_t *>(P.c)[m * P.ldc + oc] = (uint16_t)pack_bf16(x[v], 0.0f);
     }
   }
 }

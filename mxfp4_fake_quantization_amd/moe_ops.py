@@ -27,7 +27,7 @@ import ctypes
 
 import torch
 
-from . import _FP8, FLOOR, _check, _Desc, _dtype, _group_list, _load, _MxOperand, _need, _operand, _ptr, _stream
+from . import (_FP8, FLOOR, MX_FORMATS, _check, _Desc, _dtype, _group_list, _load, _MxOperand, _need, _ptr, _stream)
 
 __all__ = ["mxfp4_moe_route", "mxfp4_moe_route_bwd", "mxfp4_moe_plan", "mxfp4_moe_plan_workspace",
            "mxfp4_moe_dispatch", "mxfp4_moe_combine", "mxfp4_moe_combine_bwd", "ACTIVATIONS",
@@ -106,6 +106,10 @@ def _on_gpu(*tensors):
     for t in tensors:
         if t is not None and not t.is_cuda:
             raise ValueError("tensors must live on the GPU (no CPU path)")
+
+
+def _list(gl):
+    return None if gl is None else _arg(gl, gl.shape, _I64, "group_list")
 
 
 def _given(t, what):
@@ -232,6 +236,19 @@ def mxfp4_moe_combine_bwd(grad_y, h, rows, weights=None, grad_h=None, grad_weigh
     _check(_lib().mxfp4_moe_combine_bwd(*args, _stream()), "mxfp4_moe_combine_bwd")
 
 
+def _mx(data, scales, fmt, block):
+    """mxfp4_mx_operand_t of codes [rows, ld] or [G, rows, ld] and their scales."""
+    if fmt not in MX_FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(MX_FORMATS)}, got {fmt!r}")
+    shape, sshape = data.shape, scales.shape
+    if len(shape) != len(sshape):
+        raise ValueError("operand data and scales must have the same rank")
+    three = len(shape) == 3
+    return _MxOperand(_arg(data, shape, _U8, "operand data"), _arg(scales, sshape, _U8, "operand scales"),
+                      MX_FORMATS[fmt], block, shape[-1], sshape[-1], shape[1] * shape[2] if three else 0,
+                      sshape[1] * sshape[2] if three else 0)
+
+
 def _act(act):
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
@@ -266,18 +283,16 @@ def mxfp4_grouped_matmul_act(a, a_scales, b, b_scales, c, group_list=None, act="
     N = nb // 2 if code & 4 else nb
     if bias is not None and tuple(bias.shape) not in ((nb,), (groups, nb)):
         raise ValueError(f"bias must be [{nb}] or [{groups}, {nb}], got {list(bias.shape)}")
-    if K is None:
-        K = a.shape[1]
-    oa = _operand(a, a_scales, a_fmt, a_block)
-    ob = _operand(b, b_scales, b_fmt, b_block)
+    K = a.shape[1] if K is None else int(K)
+    oa, ob = _mx(a, a_scales, a_fmt, a_block), _mx(b, b_scales, b_fmt, b_block)
     gl = _group_list(group_list, M, group_list_type)
     dt, out = c.dtype, (M, N)
     ep = _Epilogue(code, 0, None if bias is None else _arg(bias, bias.shape, _F32, "bias"),
                    nb if bias is not None and bias.dim() == 2 else 0, _arg(residual, out, dt, "residual"), N,
                    _arg(z, (M, nb), dt, "z"), nb)
-    args = (M, N, int(K), ctypes.byref(oa), ctypes.byref(ob), _ptr(gl, "i64"), 0 if gl is None else gl.numel(),
+    args = (M, N, K, ctypes.byref(oa), ctypes.byref(ob), _list(gl), 0 if gl is None else gl.numel(),
             int(group_list_type), ctypes.byref(ep), 1 if dt == _F32 else 0, _arg(c, out, dt, "c"), N)
-    _on_gpu(c, bias, residual, z)
+    _on_gpu(a, a_scales, b, b_scales, c, bias, residual, z, gl)
     _check(_lib().mxfp4_grouped_matmul_act(*args, _stream()), "mxfp4_grouped_matmul_act")
 
 
@@ -301,7 +316,7 @@ def mxfp4_act_bwd(grad_c, z, grad_z, act="none", grad_bias=None, group_list=None
         _need(workspace, need, "workspace")
     args = (_dtype(grad_c), code, rows, cols, _arg(grad_c, shape, dt, "grad_c"),
             _arg(_given(z, "z"), (rows, zc), dt, "z"), _arg(_given(grad_z, "grad_z"), (rows, zc), dt, "grad_z"),
-            None if grad_bias is None else _arg(grad_bias, grad_bias.shape, _F32, "grad_bias"), _ptr(gl, "i64"),
+            None if grad_bias is None else _arg(grad_bias, grad_bias.shape, _F32, "grad_bias"), _list(gl),
             groups, int(group_list_type), _ptr(workspace, "u8") if need else None, need)
-    _on_gpu(grad_c, z, grad_z, grad_bias)
+    _on_gpu(grad_c, z, grad_z, grad_bias, gl)
     _check(_lib().mxfp4_act_bwd(*args, _stream()), "mxfp4_act_bwd")
