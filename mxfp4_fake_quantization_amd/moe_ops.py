@@ -108,6 +108,12 @@ def _on_gpu(*tensors):
             raise ValueError("tensors must live on the GPU (no CPU path)")
 
 
+def _groups(group_list):
+    if group_list is None:
+        return 0
+    return group_list.numel() if isinstance(group_list, torch.Tensor) else len(group_list)
+
+
 def _list(gl):
     return None if gl is None else _arg(gl, gl.shape, _I64, "group_list")
 
@@ -268,8 +274,7 @@ def mxfp4_grouped_matmul_act(a, a_scales, b, b_scales, c, group_list=None, act="
     if c is None or c.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("c must be a bfloat16 or float32 tensor")
     M = _matrix(a, "a")[0]
-    n_list = 0 if group_list is None else (group_list.numel() if isinstance(group_list, torch.Tensor)
-                                           else len(group_list))
+    n_list = _groups(group_list)
     if a_scales is None or a_scales.dim() != 2 or a_scales.shape[0] < M:
         raise ValueError(f"a_scales must have M={M} rows")
     if b is None or b_scales is None or b.dim() < 2 or b_scales.dim() < 2 or b_scales.shape[-2] != b.shape[-2]:
@@ -285,15 +290,16 @@ def mxfp4_grouped_matmul_act(a, a_scales, b, b_scales, c, group_list=None, act="
         raise ValueError(f"bias must be [{nb}] or [{groups}, {nb}], got {list(bias.shape)}")
     K = a.shape[1] if K is None else int(K)
     oa, ob = _mx(a, a_scales, a_fmt, a_block), _mx(b, b_scales, b_fmt, b_block)
-    gl = _group_list(group_list, M, group_list_type)
     dt, out = c.dtype, (M, N)
     ep = _Epilogue(code, 0, None if bias is None else _arg(bias, bias.shape, _F32, "bias"),
                    nb if bias is not None and bias.dim() == 2 else 0, _arg(residual, out, dt, "residual"), N,
                    _arg(z, (M, nb), dt, "z"), nb)
-    args = (M, N, K, ctypes.byref(oa), ctypes.byref(ob), _list(gl), 0 if gl is None else gl.numel(),
-            int(group_list_type), ctypes.byref(ep), 1 if dt == _F32 else 0, _arg(c, out, dt, "c"), N)
-    _on_gpu(a, a_scales, b, b_scales, c, bias, residual, z, gl)
-    _check(_lib().mxfp4_grouped_matmul_act(*args, _stream()), "mxfp4_grouped_matmul_act")
+    cp = _arg(c, out, dt, "c")
+    _on_gpu(a, a_scales, b, b_scales, c, bias, residual, z)
+    gl = _group_list(group_list, M, group_list_type)
+    _check(_lib().mxfp4_grouped_matmul_act(M, N, K, ctypes.byref(oa), ctypes.byref(ob), _list(gl), n_list,
+                                           int(group_list_type), ctypes.byref(ep), 1 if dt == _F32 else 0, cp, N,
+                                           _stream()), "mxfp4_grouped_matmul_act")
 
 
 def mxfp4_act_bwd(grad_c, z, grad_z, act="none", grad_bias=None, group_list=None, group_list_type=1, workspace=None):
@@ -304,9 +310,7 @@ def mxfp4_act_bwd(grad_c, z, grad_z, act="none", grad_bias=None, group_list=None
     code = _act(act)
     shape = rows, cols = _matrix(grad_c, "grad_c")
     dt, zc = grad_c.dtype, cols * (2 if code & 4 else 1)
-    gl = _group_list(group_list, rows, group_list_type)
-    groups = 0 if gl is None else gl.numel()
-    need = 0
+    groups, need = _groups(group_list), 0
     if grad_bias is not None:
         if tuple(grad_bias.shape) not in ((max(groups, 1), zc),) + (((zc,),) if groups <= 1 else ()):
             raise ValueError(f"grad_bias must be [{groups or 1}, {zc}], got {list(grad_bias.shape)}")
@@ -316,7 +320,9 @@ def mxfp4_act_bwd(grad_c, z, grad_z, act="none", grad_bias=None, group_list=None
         _need(workspace, need, "workspace")
     args = (_dtype(grad_c), code, rows, cols, _arg(grad_c, shape, dt, "grad_c"),
             _arg(_given(z, "z"), (rows, zc), dt, "z"), _arg(_given(grad_z, "grad_z"), (rows, zc), dt, "grad_z"),
-            None if grad_bias is None else _arg(grad_bias, grad_bias.shape, _F32, "grad_bias"), _list(gl),
-            groups, int(group_list_type), _ptr(workspace, "u8") if need else None, need)
-    _on_gpu(grad_c, z, grad_z, grad_bias, gl)
-    _check(_lib().mxfp4_act_bwd(*args, _stream()), "mxfp4_act_bwd")
+            None if grad_bias is None else _arg(grad_bias, grad_bias.shape, _F32, "grad_bias"))
+    _on_gpu(grad_c, z, grad_z, grad_bias)
+    gl = _group_list(group_list, rows, group_list_type)
+    st = _lib().mxfp4_act_bwd(*args, _list(gl), groups, int(group_list_type), _ptr(workspace, "u8") if need else None,
+                              need, _stream())
+    _check(st, "mxfp4_act_bwd")

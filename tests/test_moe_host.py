@@ -161,3 +161,100 @@ def test_abi_dispatch_and_combine(lib):
     assert bwd(gy=None) == EINVAL and bwd(h=None) == EINVAL and bwd(r=None) == EINVAL
     assert bwd(gh=A[0]) == EINVAL and bwd(gh=A[1]) == EINVAL and bwd(gw=A[3]) == EINVAL
     assert bwd(tokens=0) == OK and bwd(cols=0, gw=None) == OK
+
+
+# ---- the product with its epilogue, and its backward ------------------------------
+
+def test_binding_product():
+    a, asc = t(64, 128, dtype=u8), t(64, 4, dtype=u8)
+    b, bsc = t(2, 48, 64, dtype=u8), t(2, 48, 4, dtype=u8)            # 2 experts, 48 rows, K = 128 (fp4)
+    c, gl = t(64, 48, dtype=bf16), [30, 34]
+    f = M.mxfp4_grouped_matmul_act
+    refused("act", f, a, asc, b, bsc, c, group_list=gl, act="tanh")
+    refused("c must be", f, a, asc, b, bsc, t(64, 24, dtype=bf16), group_list=gl)
+    refused("c must be", f, a, asc, b, bsc, c, group_list=gl, act="swiglu")        # gated: half as many columns
+    refused("bfloat16 or float32", f, a, asc, b, bsc, t(64, 48, dtype=torch.float16), group_list=gl)
+    refused("even number", f, a, asc, t(2, 47, 64, dtype=u8), t(2, 47, 4, dtype=u8), c, group_list=gl, act="geglu")
+    refused("bias", f, a, asc, b, bsc, c, group_list=gl, bias=t(47))
+    refused("bias", f, a, asc, b, bsc, c, group_list=gl, bias=t(3, 48))
+    refused("residual", f, a, asc, b, bsc, c, group_list=gl, residual=t(64, 47, dtype=bf16))
+    refused("residual", f, a, asc, b, bsc, c, group_list=gl, residual=t(64, 48))   # another type
+    refused("z must be", f, a, asc, b, bsc, t(64, 24, dtype=bf16), group_list=gl, act="swiglu", z=t(64, 24, dtype=bf16))
+    refused("one matrix per group", f, a, asc, b, bsc, c, group_list=[10, 20, 34])
+    refused("a_scales", f, a, t(63, 4, dtype=u8), b, bsc, c, group_list=gl)
+    refused("b_scales", f, a, asc, b, t(2, 47, 4, dtype=u8), c, group_list=gl)
+    refused("same rank", f, a, asc, b, t(48, 4, dtype=u8), c)
+    refused("fmt", f, a, asc, b, bsc, c, a_fmt="e3m2")
+    z, dc = t(9, 32), t(9, 16)
+    g = M.mxfp4_act_bwd
+    refused("z must be", g, dc, t(9, 16), z, act="swiglu")
+    refused("grad_z", g, dc, z, t(9, 16), act="swiglu")
+    refused("grad_bias", g, dc, z, z, act="swiglu", grad_bias=t(2, 32))
+    refused("workspace", g, dc, z, z, act="swiglu", grad_bias=t(1, 32), workspace=t(8, dtype=u8))
+    refused("act", g, dc, z, z, act="none2")
+
+
+def operand(data, scales, fmt, block=32, ld=128, lds=4, gs=0, gss=0):
+    return M._MxOperand(data, scales, fmt, block, ld, lds, gs, gss)
+
+
+def test_abi_product(lib):
+    from mxfp4_fake_quantization_amd.moe_ops import _Epilogue
+
+    def ep(act=0, reserved=0, bias=None, bs=0, res=None, ldr=48, z=None, ldz=48):
+        return _Epilogue(act, reserved, bias, bs, res, ldr, z, ldz)
+
+    def call(m=64, n=48, k=128, a=None, b=None, gl=None, ng=1, lt=1, e=None, out=0, c=A[4], ldc=48):
+        a = a or operand(A[0], A[1], 0)
+        b = b or operand(A[2], A[3], 4, ld=64)
+        e = ep() if e is None else e
+        return lib.mxfp4_grouped_matmul_act(m, n, k, ctypes.byref(a), ctypes.byref(b), P(gl), ng, lt,
+                                            ctypes.byref(e) if e else None, out, P(c), ldc, None)
+    assert call(m=-1) == EINVAL and call(k=40) == EINVAL and call(k=0) == EUNSUP
+    assert call(e=False) == EINVAL
+    for act in (-1, 4, 5, 8):
+        assert call(e=ep(act)) == EUNSUP
+    assert call(e=ep(reserved=1)) == EINVAL
+    assert call(out=2) == EUNSUP
+    assert call(gl=A[5], ng=0) == EINVAL and call(gl=A[5], lt=2) == EINVAL and call(gl=A[5] + 4) == EINVAL
+    assert call(a=operand(A[0], A[1], 4)) == EUNSUP                         # A is fp8
+    assert call(b=operand(A[2], A[3], 1)) == EUNSUP                         # B is E2M1 or E4M3
+    assert call(a=operand(A[0], A[1], 0, block=64)) == EUNSUP
+    assert call(a=operand(A[0], A[1], 0, ld=112)) == EINVAL and call(a=operand(A[0], A[1], 0, lds=3)) == EINVAL
+    assert call(b=operand(A[2] + 8, A[3], 4, ld=64)) == EINVAL
+    assert call(c=None) == EINVAL and call(c=A[4] + 1) == EINVAL and call(ldc=47) == EINVAL
+    assert call(e=ep(bias=A[6] + 2)) == EINVAL and call(e=ep(bias=A[6], bs=-1)) == EINVAL
+    assert call(e=ep(res=A[6], ldr=47)) == EINVAL and call(e=ep(res=A[4], ldr=56)) == EINVAL
+    assert call(e=ep(z=A[6], ldz=47)) == EINVAL and call(e=ep(6, z=A[6], ldz=95)) == EINVAL
+    assert call(e=ep(z=A[4])) == EINVAL and call(c=A[0]) == EINVAL          # outputs over inputs
+    assert call(n=1 << 20, ldc=1 << 20, e=ep(6), b=operand(A[2], A[3], 4, ld=1 << 13)) == EUNSUP   # 2^33 bytes of gate
+    assert call(m=0) == OK and call(n=0) == OK
+
+
+def test_abi_act_bwd(lib):
+    def call(dt=F32, act=2, rows=9, cols=16, dc=A[0], z=A[1], dz=A[2], db=None, gl=None, ng=0, lt=1, ws=None, n=0):
+        return lib.mxfp4_act_bwd(dt, act, rows, cols, P(dc), P(z), P(dz), P(db), P(gl), ng, lt, P(ws), n, None)
+    assert call(dt=4) == EUNSUP and call(act=5) == EUNSUP and call(rows=-1) == EINVAL
+    assert call(rows=1 << 40, cols=1 << 40) == EINVAL
+    assert call(dc=None) == EINVAL and call(z=None) == EINVAL and call(dz=None) == EINVAL
+    assert call(dz=A[2] + 2) == EINVAL
+    assert call(gl=A[3], ng=0) == EINVAL and call(gl=A[3], ng=2, lt=3) == EINVAL
+    need = lib.mxfp4_act_bwd_workspace(2, 9, 16, 0)
+    assert need > 0 and lib.mxfp4_act_bwd_workspace(5, 9, 16, 0) == -1 and lib.mxfp4_act_bwd_workspace(2, -1, 16, 0) == -1
+    assert call(db=A[4]) == EINVAL and call(db=A[4], ws=A[5], n=need - 1) == EINVAL
+    assert call(db=A[0], ws=A[5], n=need) == EINVAL                          # the sums over grad_c
+    assert call(act=6, dz=A[0]) == EINVAL and call(act=6, dz=A[1]) == EINVAL  # gated: not in place
+    assert call(rows=0, dc=None, z=None, dz=None) == OK and call(cols=0, dc=None) == OK
+
+
+def test_layer_refusals():
+    from mxfp4_fake_quantization_amd import moe
+    with pytest.raises(ValueError, match="act"):
+        moe.MoESpec(act="tanh")
+    x, l, w1, w2 = t(4, 64, dtype=bf16), t(4, 3), t(3, 64, 64, dtype=bf16), t(3, 64, 32, dtype=bf16)
+    s = moe.MoESpec()
+    refused("bfloat16", moe._check_shapes, t(4, 64), l, w1, w2, s)
+    refused("multiples of 32", moe._check_shapes, x, l, t(3, 62, 64, dtype=bf16), w2, s)
+    refused("w2 must be", moe._check_shapes, x, l, w1, t(3, 64, 64, dtype=bf16), s)
+    refused("logits", moe._check_shapes, x, t(4, 2), w1, w2, s)
+    moe._check_shapes(x, l, w1, w2, s)
