@@ -118,23 +118,33 @@ __global__ __launch_bounds__(kActBwdThreads) void act_bwd_kernel(ActBwdArgs A) {
   }
 }
 
-// dbias[g, c]: the sums of the group's runs, in order.
+// dbias[g, c]: the sums of the group's runs.  64 columns a workgroup, a quarter
+// of the runs each wave, in order, then the quarters in order (one thread a
+// column for all runs took 20 us for 129 runs of 4096 columns, ahead of its
+// loads' latency only).
 __global__ __launch_bounds__(kActBwdThreads) void bias_sum_kernel(const float *part, const int64_t *gl, int G,
                                                                   int list_type, int64_t rows, int64_t zcols,
                                                                   int64_t ctiles, float *out) {
+  __shared__ float quarter[kActBwdThreads / 64][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = (int)(blockIdx.x / ctiles);
-  const int64_t c = (blockIdx.x % ctiles) * kActBwdThreads + threadIdx.x;
+  const int64_t c = (blockIdx.x % ctiles) * 64 + lane;
   int64_t first = 0, n = (rows + (1 << kRunLog) - 1) >> kRunLog;
   if (gl) group_block_span(gl, G, list_type, rows, kRunLog, g, &first, &n);
-  if (c >= zcols) return;
-  const float *p = part + first * zcols + c;
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  int64_t i = 0;
-  for (; i + 4 <= n; i += 4)
+  const int64_t per = (n + 3) >> 2, lo = wave * per, hi = lo + per < n ? lo + per : n;
+  float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < zcols) {
+    const float *p = part + first * zcols + c;
+    int64_t i = lo;
+    for (; i + 8 <= hi; i += 8)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) s[u] += p[(i + u) * zcols];
-  for (; i < n; ++i) s[0] += p[i * zcols];
-  out[(int64_t)g * zcols + c] = (s[0] + s[1]) + (s[2] + s[3]);
+      for (int u = 0; u < 8; ++u) s[u] += p[(i + u) * zcols];
+    for (; i < hi; ++i) s[0] += p[i * zcols];
+  }
+  quarter[wave][lane] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+  __syncthreads();
+  if (wave == 0 && c < zcols)
+    out[(int64_t)g * zcols + c] = (quarter[0][lane] + quarter[1][lane]) + (quarter[2][lane] + quarter[3][lane]);
 }
 
 int64_t runs_of(int64_t rows, int groups) {  // at most: every group adds one partial run
@@ -190,7 +200,7 @@ hipError_t launch_act_bwd(const ActBwdLaunch &L, hipStream_t st) {
     if (r != hipSuccess) return r;
   }
   if (!L.grad_bias) return hipSuccess;
-  const int64_t bt = (a.zcols + kActBwdThreads - 1) / kActBwdThreads;
+  const int64_t bt = (a.zcols + 63) / 64;
   const int64_t groups = L.group_list ? L.num_groups : 1;
   if (bt * groups > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL(bias_sum_kernel, dim3((unsigned)(bt * groups)), dim3(kActBwdThreads), 0, st, a.part, L.group_list,
