@@ -31,7 +31,10 @@ constexpr int64_t kPlanOne = 8192;
 constexpr int kPlanMaxChunks = 256;
 
 int64_t plan_chunk(int64_t slots) {
-  if (slots <= kPlanOne) return kPlanOne;
+  if (slots <= kPlanOne) {  // as few steps a wave as there are
+    const int64_t c = (slots + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
+    return c < kPlanThreads ? kPlanThreads : c;
+  }
   const int64_t per = (slots + kPlanMaxChunks - 1) / kPlanMaxChunks;
   const int64_t c = (per + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
   return c < 2048 ? 2048 : c;

@@ -39,7 +39,8 @@ struct Turn {
 // B32: blocks of 32, a step's four scale bytes in one word (load_turn), of
 // which lane quarter q takes byte q (scale_of).  Otherwise one byte a lane.
 // TAIL: blocks at or past kb are zero codes with scale 2^0, read in bounds.
-template <int FMT, bool B32, bool TAIL>
+// SCALES false: the codes alone.
+template <int FMT, bool B32, bool TAIL, bool SCALES = true>
 __device__ __forceinline__ void load_turn(Turn<FMT> &T, const uint8_t *base, uint32_t at, const uint8_t *scales,
                                           uint32_t sat, int64_t c, int64_t kb, int sb, int q) {
   typedef uint32_t u32_a1 __attribute__((aligned(1)));
@@ -56,6 +57,7 @@ __device__ __forceinline__ void load_turn(Turn<FMT> &T, const uint8_t *base, uin
       if (!in) T.w[i] = u32x4{0u, 0u, 0u, 0u};
     }
   }
+  if (!SCALES) return;
   if (B32 && !TAIL) {
     const uint8_t *r = scales + 8 * c + sat;
     T.s[0] = *reinterpret_cast<const u32_a1 *>(r);
@@ -270,7 +272,11 @@ __global__ __launch_bounds__(kRowsThreads, (MT == 1 ? 4 : 2)) void mxgemm_rows_s
 // More columns: every wave takes the whole K of a column run of its own, and
 // the A rows, which the four runs share, pass through LDS in slabs of SL turns
 // (double-buffered; a lane's fragment is two 16-byte reads), so that the
-// memory pipeline of a CU carries B almost alone.
+// memory pipeline of a CU carries B almost alone.  B's scales (blocks of 32)
+// pass through LDS by the same slabs, each
+// wave's its own, 16 bytes a lane (a turn's 8 bytes a row, loaded for every
+// turn, read half as many lines from L2 again as the codes: 32 groups of 6
+// rows, 2048 -> 7168, 70.5 us against 64.2).
 template <int AF, int BF, bool B32, int MT, int CT, int SL, int EPI>
 __global__ __launch_bounds__(kRowsThreads, (MT == 4 ? 2 : 4)) void mxgemm_rows_kernel(GemmArgs P, ActArgs E) {
   constexpr bool GATED = EPI == 2;
@@ -281,6 +287,9 @@ __global__ __launch_bounds__(kRowsThreads, (MT == 4 ? 2 : 4)) void mxgemm_rows_k
   static_assert(ROWS * 16 * SL % kRowsThreads == 0 && SL % 2 == 0, "slab");
   __shared__ __align__(16) uint8_t sa[2][ROWS * RSTR];
   __shared__ __align__(16) uint8_t ss[2][ROWS * 8 * SL];
+  constexpr int BSL = 8 * SL, BSTR = BSL + 8;  // blocks of a slab; bytes of a B row's scales in LDS, 16 rows on all banks
+  __shared__ __align__(16) uint8_t sbs[kRowsWaves][B32 ? 16 * CT * BSTR : 8];
+  static_assert(CT == 2, "two lanes a B row");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4;
 
@@ -315,7 +324,32 @@ __global__ __launch_bounds__(kRowsThreads, (MT == 4 ? 2 : 4)) void mxgemm_rows_k
     constexpr bool TAIL = decltype(tail)::value;
 #pragma unroll
     for (int j = 0; j < CT; ++j)
-      load_turn<BF, B32, TAIL>(t.b[j], bb[j / H], bo[j], bsb[j / H], bso[j], c, kb, P.b_sb, q);
+      load_turn<BF, B32, TAIL, !B32>(t.b[j], bb[j / H], bo[j], bsb[j / H], bso[j], c, kb, P.b_sb, q);
+  };
+  // A slab's B scales: lane l holds half of row l / 2's (4 SL bytes); 2^0 past K.
+  typedef uint32_t half_t __attribute__((ext_vector_type(SL)));
+  typedef half_t half_a1 __attribute__((aligned(1)));
+  half_t rb;
+  const int brow = lane >> 1, btile = brow >> 4;
+  const uint8_t *bsrow;
+  {
+    int col = 16 * (btile % H) + (brow & 15);
+    col = col < nlen ? col : (nlen > 0 ? nlen - 1 : 0);
+    bsrow = bsb[0] + (GATED && btile ? P.N * P.ldbs : 0) + (uint32_t)col * (uint32_t)P.ldbs;
+  }
+  auto fetch_bs = [&](int64_t s) {
+    const int64_t blk = BSL * s + 4 * SL * (lane & 1);
+    if (blk + 4 * SL <= kb) {
+      rb = *reinterpret_cast<const half_a1 *>(bsrow + blk);
+    } else {
+#pragma unroll
+      for (int w = 0; w < SL; ++w) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v |= (blk + 4 * w + e < kb ? (uint32_t)bsrow[blk + 4 * w + e] : 127u) << (8 * e);
+        rb[w] = v;
+      }
+    }
   };
 
   // A slab s (turns SL s ..): thread's pieces into registers, then into LDS.
@@ -354,6 +388,11 @@ __global__ __launch_bounds__(kRowsThreads, (MT == 4 ? 2 : 4)) void mxgemm_rows_k
     }
   };
   auto stage = [&](int buf) {
+    if (B32) {  // this wave read its scales before, in order
+      uint32_t *r = reinterpret_cast<uint32_t *>(&sbs[wave][brow * BSTR + 4 * SL * (lane & 1)]);
+#pragma unroll
+      for (int w = 0; w < SL; ++w) r[w] = rb[w];
+    }
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
       const int idx = tid + kRowsThreads * i, row = idx / (16 * SL), piece = idx % (16 * SL);
@@ -373,6 +412,11 @@ __global__ __launch_bounds__(kRowsThreads, (MT == 4 ? 2 : 4)) void mxgemm_rows_k
     for (int j = 0; j < CT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   auto multiply = [&](const BTurn &t, int buf, int u) {  // turn u of the slab in buf
     __builtin_amdgcn_sched_barrier(0);
+    u32x2 sw[CT];
+    if (B32) {
+#pragma unroll
+      for (int j = 0; j < CT; ++j) sw[j] = *reinterpret_cast<const u32x2 *>(&sbs[wave][(16 * j + l16) * BSTR + 8 * u]);
+    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       v8i a[MT];
@@ -389,7 +433,7 @@ __global__ __launch_bounds__(kRowsThreads, (MT == 4 ? 2 : 4)) void mxgemm_rows_k
 #pragma unroll
         for (int i = 0; i < MT; ++i)
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[i], operand<BF>(t.b[j], s), acc[i][j], AF, BF, 0,
-                                                                       sca[i], 0, scale_of<BF, B32>(t.b[j], s, q));
+                                                                       sca[i], 0, B32 ? (int)(sw[j][s] >> (8 * q)) : (int)t.b[j].s[s]);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -399,12 +443,16 @@ __global__ __launch_bounds__(kRowsThreads, (MT == 4 ? 2 : 4)) void mxgemm_rows_k
   BTurn t0, t1;
   auto upto = [&](int c) { return (int64_t)(c < full ? c : full - 1); };
   fetch(0);
+  if (B32) fetch_bs(0);
   if (full > 0) load_b(t0, 0, std::false_type{});
   stage(0);
   __syncthreads();
   for (int s = 0; s < slabs; ++s) {
     const int buf = s & 1;
-    if (s + 1 < slabs) fetch(s + 1);
+    if (s + 1 < slabs) {
+      fetch(s + 1);
+      if (B32) fetch_bs(s + 1);
+    }
 #pragma unroll
     for (int u = 0; u < SL; u += 2) {
       const int c = SL * s + u;
