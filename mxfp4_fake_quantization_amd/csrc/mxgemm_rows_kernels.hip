@@ -20,7 +20,6 @@ namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-
 constexpr int kRowsCT = 2;  // 16-row tiles of B a wave takes
 constexpr int kRowsWaves = 4, kRowsThreads = 64 * kRowsWaves;
 
@@ -278,7 +277,7 @@ __global__ __launch_bounds__(kRowsThreads, (MT == 1 ? 4 : 2)) void mxgemm_rows_s
 // turn, read half as many lines from L2 again as the codes: 32 groups of 6
 // rows, 2048 -> 7168, 70.5 us against 64.2).
 template <int AF, int BF, bool B32, int MT, int CT, int SL, int EPI>
-__global__ __launch_bounds__(kRowsThreads, (MT == 4 ? 2 : 4)) void mxgemm_rows_kernel(GemmArgs P, ActArgs E) {
+__global__ __launch_bounds__(kRowsThreads, (MT == 4 ? 2 : MT == 2 ? 3 : 4)) void mxgemm_rows_kernel(GemmArgs P, ActArgs E) {
   constexpr bool GATED = EPI == 2;
   constexpr int H = GATED ? CT / 2 : CT;
   constexpr int MLOG = MT == 1 ? 4 : MT == 2 ? 5 : 6;
@@ -493,7 +492,7 @@ hipError_t rows_one(GemmArgs a, const ActArgs &e, hipStream_t st) {
   const int64_t runs = (a.N + COLS - 1) / COLS;
   // Shared K below 4096 runs (4 waves a SIMD): 8 experts of one row, 7168 ->
   // 2 x 2048 (1024 runs), 26 us against 29; 32 groups, 2048 -> 7168 (about
-  // 7600 runs), 127 us against 71.
+  // 7600 runs), 127 us against 64.
   const bool split = a.tiles_m * runs < 4096;
   a.tiles_n = split ? runs : (runs + kRowsWaves - 1) / kRowsWaves;
   a.total = a.tiles_m * a.tiles_n;
@@ -537,13 +536,20 @@ hipError_t launch_gemm_act(const GemmLaunch &L, const ActArgs &e, bool gated, hi
   // rows an average group has, of the groups that can have any
   const int64_t groups = L.num_groups < L.M ? L.num_groups : L.M;
   const int64_t avg = (L.M + groups - 1) / groups;
-  // The few-rows form up to 64: 32 groups, 2048 -> 7168, it took 71 us with 6
-  // rows a group on average, 108 with 25, 157 with 50 and 257 with 100, the
-  // tiles 198 - 210 at each; one group of 64 / 128 / 256 rows 15 / 23 / 44 us
-  // against 22 / 25 / 26.  Row tiles by the same runs (16 / 32 / 64 rows a
-  // workgroup): 71 / 81 / 95 us at 6 rows, 119 / 108 / 121 at 25; gated, 7168
-  // -> 2048, 351 / 271 / 193 at 50.
-  if (avg <= 64) return rows_act(L, e, gated, avg <= 8 ? 1 : avg <= 24 ? 2 : 4, 0, st);
+  // The few-rows form up to 64: 32 groups, 2048 -> 7168, it takes 64 us with 6
+  // rows a group on average, 100 with 25 and 150 with 50, the tiles 198 - 210
+  // at each and 185 with 100 (this form 257); one group of 64 / 128 / 256 rows
+  // 15 / 23 / 44 us against 22 / 25 / 26.  Rows a workgroup (16 / 32 / 64), us:
+  //                      6 rows on average     12            25            50
+  //   K = 2048 -> 7168     64 /  81 /  90   77 /  82 /  96  107 / 100 / 113  171 / 150 / 154
+  //   K = 7168 -> 4096    103 / 128 / 120  138 / 145 / 130  201 / 165 / 150  340 / 251 / 209
+  // (gated, 7168 -> 2 x 2048: 109 / 118 / 115 at 8, 130 / 122 / 118 at 12.)  A
+  // longer K pays the larger workgroup's start and end off.
+  if (avg <= 64) {
+    const bool long_k = L.K >= 4096;
+    const int mt = avg <= (long_k ? 10 : 18) ? 1 : (long_k || avg > 48 ? 4 : 2);
+    return rows_act(L, e, gated, mt, 0, st);
+  }
   // One group whose last row tile has few rows: a launch of its own for them,
   // where that tile would cost a share of a round (4099 x 4095 x 4096: 133 us
   // as 17 row tiles, the last 16 of them in the tail launch).
