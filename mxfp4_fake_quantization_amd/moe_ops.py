@@ -24,6 +24,7 @@ their gradients float32; ids and rows int32 [tokens, k]; group_list int64
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -53,6 +54,15 @@ class _Epilogue(ctypes.Structure):
                 ("z", ctypes.c_void_p), ("ld_z", ctypes.c_int64)]
 
 
+# The same structs as bytes: filling a ctypes structure and pointing at it takes
+# about three times as long, which a small call's time shows.
+_ROUTE = struct.Struct("@iiiiqiiifi4x")
+_EPILOGUE = struct.Struct("@iiPqPqPq")
+_DESC = struct.Struct("@iiiiqqfi")
+_OPERAND = struct.Struct("@PPiiqqqq")
+assert [f.size for f in (_ROUTE, _EPILOGUE, _DESC, _OPERAND)] == [
+    ctypes.sizeof(c) for c in (_Route, _Epilogue, _Desc, _MxOperand)]
+
 _typed = False
 
 
@@ -61,7 +71,7 @@ def _lib():
     lib = _load()
     if not _typed:
         vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
-        rp, dp = ctypes.POINTER(_Route), ctypes.POINTER(_Desc)
+        rp = dp = op = vp  # a struct's bytes, or ctypes.byref of one
         lib.mxfp4_moe_route.argtypes = [rp, vp, vp, vp, vp, vp]
         lib.mxfp4_moe_route_bwd.argtypes = [rp, vp, vp, vp, vp, vp]
         lib.mxfp4_moe_plan_workspace.argtypes = [i64, i32]
@@ -70,8 +80,7 @@ def _lib():
         lib.mxfp4_moe_dispatch.argtypes = [dp, i32, vp, vp, i32, i64, vp, vp, vp, vp]
         lib.mxfp4_moe_combine.argtypes = [i32, i64, i64, i32, i64, vp, vp, vp, vp, vp, vp]
         lib.mxfp4_moe_combine_bwd.argtypes = [i32, i64, i64, i32, i64, vp, vp, vp, vp, vp, vp, vp]
-        op = ctypes.POINTER(_MxOperand)
-        lib.mxfp4_grouped_matmul_act.argtypes = [i64, i64, i64, op, op, vp, i32, i32, ctypes.POINTER(_Epilogue), i32, vp,
+        lib.mxfp4_grouped_matmul_act.argtypes = [i64, i64, i64, op, op, vp, i32, i32, vp, i32, vp,
                                                  i64, vp]
         lib.mxfp4_act_bwd_workspace.argtypes = [i32, i64, i64, i32]
         lib.mxfp4_act_bwd_workspace.restype = i64
@@ -102,6 +111,17 @@ def _arg(t, shape, dtype, what):
     return t.data_ptr()
 
 
+def _own(t, dtype, what):
+    """Address of a tensor of this type, of any shape (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{what} is a {dtype} tensor, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
 def _on_gpu(*tensors):
     for t in tensors:
         if t is not None and not t.is_cuda:
@@ -115,7 +135,7 @@ def _groups(group_list):
 
 
 def _list(gl):
-    return None if gl is None else _arg(gl, gl.shape, _I64, "group_list")
+    return _own(gl, _I64, "group_list")
 
 
 def _given(t, what):
@@ -127,13 +147,13 @@ def _given(t, what):
 _F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
 
 
-def _route_desc(logits, k, score, num_groups, topk_groups, renormalize, scale):
-    tokens, experts = _matrix(logits, "logits")
+def _route_desc(logits, shape, k, score, num_groups, topk_groups, renormalize, scale):
+    tokens, experts = shape
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
     topk_groups = num_groups if topk_groups is None else topk_groups
-    return _Route(_dtype(logits), _SCORES[score], 1 if renormalize else 0, experts, tokens, int(k), int(num_groups),
-                  int(topk_groups), float(scale), 0)
+    return _ROUTE.pack(_dtype(logits), _SCORES[score], 1 if renormalize else 0, experts, tokens, k, num_groups,
+                       topk_groups, scale, 0)
 
 
 def mxfp4_moe_route(logits, weights, ids, bias=None, score="softmax", num_groups=1, topk_groups=None,
@@ -143,8 +163,8 @@ def mxfp4_moe_route(logits, weights, ids, bias=None, score="softmax", num_groups
     second dimension; see include/mxfp4.h."""
     k = _matrix(ids, "ids")[1]
     shape = tokens, experts = _matrix(logits, "logits")
-    d = _route_desc(logits, k, score, num_groups, topk_groups, renormalize, scale)
-    args = (ctypes.byref(d), _arg(logits, shape, logits.dtype, "logits"), _arg(bias, (experts,), _F32, "bias"),
+    d = _route_desc(logits, shape, k, score, num_groups, topk_groups, renormalize, scale)
+    args = (d, _own(logits, logits.dtype, "logits"), _arg(bias, (experts,), _F32, "bias"),
             _arg(_given(weights, "weights"), (tokens, k), _F32, "weights"), _arg(ids, (tokens, k), _I32, "ids"))
     _on_gpu(logits, weights, ids, bias)
     _check(_lib().mxfp4_moe_route(*args, _stream()), "mxfp4_moe_route")
@@ -156,9 +176,9 @@ def mxfp4_moe_route_bwd(grad_weights, logits, ids, grad_logits, score="softmax",
     k = _matrix(ids, "ids")[1]
     shape = _matrix(logits, "logits")
     chosen = (shape[0], k)
-    d = _route_desc(logits, k, score, 1, 1, renormalize, scale)
-    args = (ctypes.byref(d), _arg(_given(grad_weights, "grad_weights"), chosen, _F32, "grad_weights"),
-            _arg(logits, shape, logits.dtype, "logits"), _arg(ids, chosen, _I32, "ids"),
+    d = _route_desc(logits, shape, k, score, 1, 1, renormalize, scale)
+    args = (d, _arg(_given(grad_weights, "grad_weights"), chosen, _F32, "grad_weights"),
+            _own(logits, logits.dtype, "logits"), _arg(ids, chosen, _I32, "ids"),
             _arg(_given(grad_logits, "grad_logits"), shape, logits.dtype, "grad_logits"))
     _on_gpu(grad_weights, logits, ids, grad_logits)
     _check(_lib().mxfp4_moe_route_bwd(*args, _stream()), "mxfp4_moe_route_bwd")
@@ -186,8 +206,8 @@ def mxfp4_moe_plan(ids, group_list, rows, workspace=None):
     if need and workspace is None:
         workspace = torch.empty(need, dtype=_U8, device=ids.device)
     _need(workspace, need, "workspace")
-    args = (slots, experts, _arg(ids, shape, _I32, "ids"), _arg(group_list, (experts,), _I64, "group_list"),
-            _arg(rows, shape, _I32, "rows"), _ptr(workspace, "u8") if need else None, need)
+    args = (slots, experts, _own(ids, _I32, "ids"), _own(group_list, _I64, "group_list"), _own(rows, _I32, "rows"),
+            _ptr(workspace, "u8") if need else None, need)
     _on_gpu(ids, group_list, rows)
     _check(_lib().mxfp4_moe_plan(*args, _stream()), "mxfp4_moe_plan")
 
@@ -203,10 +223,11 @@ def mxfp4_moe_dispatch(x, rows, y=None, q=None, scales=None, fmt="e4m3", block=3
     if not outs or outs[0] != outs[-1]:
         raise ValueError("y and / or q with the same number of rows is required")
     n = outs[0]
-    d = _Desc(_dtype(x), int(block), FLOOR, 0, tokens, cols, 6.0, 0)
-    args = (ctypes.byref(d), _FP8[fmt], _arg(x, shape, x.dtype, "x"), _arg(rows, (tokens, k), _I32, "rows"), k, n,
+    block = int(block)
+    args = (_DESC.pack(_dtype(x), block, FLOOR, 0, tokens, cols, 6.0, 0), _FP8[fmt], _own(x, x.dtype, "x"),
+            _arg(rows, (tokens, k), _I32, "rows"), k, n,
             _arg(y, (n, cols), x.dtype, "y"), _arg(q, (n, cols), _U8, "q"),
-            _arg(scales, (n, -(-cols // int(block))), _U8, "scales"))
+            _arg(scales, (n, -(-cols // block)), _U8, "scales"))
     _on_gpu(x, rows, y, q, scales)
     _check(_lib().mxfp4_moe_dispatch(*args, _stream()), "mxfp4_moe_dispatch")
 
@@ -214,10 +235,10 @@ def mxfp4_moe_dispatch(x, rows, y=None, q=None, scales=None, fmt="e4m3", block=3
 def mxfp4_moe_combine(h, rows, y, weights=None, residual=None):
     """Expert rows back to the tokens: y[t] = residual[t] + sum_j weights[t, j]
     * h[rows[t, j]]; y may be the residual."""
-    shape = n, cols = _matrix(h, "h")
+    n, cols = _matrix(h, "h")
     tokens, k = _matrix(rows, "rows")
     dt, out = h.dtype, (tokens, cols)
-    args = (_dtype(h), tokens, cols, k, n, _arg(h, shape, dt, "h"), _arg(rows, (tokens, k), _I32, "rows"),
+    args = (_dtype(h), tokens, cols, k, n, _own(h, dt, "h"), _own(rows, _I32, "rows"),
             _arg(weights, (tokens, k), _F32, "weights"), _arg(residual, out, dt, "residual"),
             _arg(_given(y, "y"), out, dt, "y"))
     _on_gpu(h, rows, y, weights, residual)
@@ -242,17 +263,16 @@ def mxfp4_moe_combine_bwd(grad_y, h, rows, weights=None, grad_h=None, grad_weigh
     _check(_lib().mxfp4_moe_combine_bwd(*args, _stream()), "mxfp4_moe_combine_bwd")
 
 
-def _mx(data, scales, fmt, block):
+def _mx(data, scales, shape, sshape, fmt, block):
     """mxfp4_mx_operand_t of codes [rows, ld] or [G, rows, ld] and their scales."""
     if fmt not in MX_FORMATS:
         raise ValueError(f"fmt must be one of {sorted(MX_FORMATS)}, got {fmt!r}")
-    shape, sshape = data.shape, scales.shape
-    if len(shape) != len(sshape):
-        raise ValueError("operand data and scales must have the same rank")
     three = len(shape) == 3
-    return _MxOperand(_arg(data, shape, _U8, "operand data"), _arg(scales, sshape, _U8, "operand scales"),
-                      MX_FORMATS[fmt], block, shape[-1], sshape[-1], shape[1] * shape[2] if three else 0,
-                      sshape[1] * sshape[2] if three else 0)
+    if len(sshape) != len(shape):
+        raise ValueError("operand data and scales must have the same rank")
+    ld, lds = shape[-1], sshape[-1]
+    return _OPERAND.pack(_own(data, _U8, "operand data"), _own(scales, _U8, "operand scales"), MX_FORMATS[fmt], block,
+                         ld, lds, shape[1] * ld if three else 0, sshape[1] * lds if three else 0)
 
 
 def _act(act):
@@ -271,35 +291,41 @@ def mxfp4_grouped_matmul_act(a, a_scales, b, b_scales, c, group_list=None, act="
     c's shape and type (c itself may be given); z [M, N] of c's type receives
     the products before the activation.  K defaults to a's row length."""
     code = _act(act)
-    if c is None or c.dtype not in (torch.bfloat16, torch.float32):
+    dt = None if c is None else c.dtype
+    if dt is not torch.bfloat16 and dt is not _F32:
         raise ValueError("c must be a bfloat16 or float32 tensor")
-    M = _matrix(a, "a")[0]
+    ashape = _matrix(a, "a")
+    M = ashape[0]
     n_list = _groups(group_list)
-    if a_scales is None or a_scales.dim() != 2 or a_scales.shape[0] < M:
+    asshape = None if a_scales is None else a_scales.shape
+    if asshape is None or len(asshape) != 2 or asshape[0] < M:
         raise ValueError(f"a_scales must have M={M} rows")
-    if b is None or b_scales is None or b.dim() < 2 or b_scales.dim() < 2 or b_scales.shape[-2] != b.shape[-2]:
+    bshape, bsshape = (None if t is None else t.shape for t in (b, b_scales))
+    if bshape is None or bsshape is None or len(bshape) < 2 or len(bsshape) < 2 or bsshape[-2] != bshape[-2]:
         raise ValueError("b_scales must have as many rows as b")
     groups = max(n_list, 1)
-    if b.dim() == 3 and (b.shape[0] < groups or b_scales.shape[0] < groups):
+    if len(bshape) == 3 and (bshape[0] < groups or bsshape[0] < groups):
         raise ValueError(f"b and b_scales must hold one matrix per group ({groups})")
-    nb = b.shape[-2]
+    nb = bshape[-2]
     if code & 4 and nb % 2:
         raise ValueError(f"a gated activation needs an even number of rows of b, got {nb}")
     N = nb // 2 if code & 4 else nb
-    if bias is not None and tuple(bias.shape) not in ((nb,), (groups, nb)):
-        raise ValueError(f"bias must be [{nb}] or [{groups}, {nb}], got {list(bias.shape)}")
-    K = a.shape[1] if K is None else int(K)
-    oa, ob = _mx(a, a_scales, a_fmt, a_block), _mx(b, b_scales, b_fmt, b_block)
-    dt, out = c.dtype, (M, N)
-    ep = _Epilogue(code, 0, None if bias is None else _arg(bias, bias.shape, _F32, "bias"),
-                   nb if bias is not None and bias.dim() == 2 else 0, _arg(residual, out, dt, "residual"), N,
-                   _arg(z, (M, nb), dt, "z"), nb)
+    per_group = False
+    if bias is not None:
+        per_group = bias.dim() == 2
+        if bias.shape != ((groups, nb) if per_group else (nb,)):
+            raise ValueError(f"bias must be [{nb}] or [{groups}, {nb}], got {list(bias.shape)}")
+    K = ashape[1] if K is None else int(K)
+    oa = _mx(a, a_scales, ashape, asshape, a_fmt, a_block)
+    ob = _mx(b, b_scales, bshape, bsshape, b_fmt, b_block)
+    out = (M, N)
+    ep = _EPILOGUE.pack(code, 0, _own(bias, _F32, "bias") or 0, nb if per_group else 0,
+                        _arg(residual, out, dt, "residual") or 0, N, _arg(z, (M, nb), dt, "z") or 0, nb)
     cp = _arg(c, out, dt, "c")
     _on_gpu(a, a_scales, b, b_scales, c, bias, residual, z)
     gl = _group_list(group_list, M, group_list_type)
-    _check(_lib().mxfp4_grouped_matmul_act(M, N, K, ctypes.byref(oa), ctypes.byref(ob), _list(gl), n_list,
-                                           int(group_list_type), ctypes.byref(ep), 1 if dt == _F32 else 0, cp, N,
-                                           _stream()), "mxfp4_grouped_matmul_act")
+    _check(_lib().mxfp4_grouped_matmul_act(M, N, K, oa, ob, _list(gl), n_list, int(group_list_type), ep,
+                                           1 if dt is _F32 else 0, cp, N, _stream()), "mxfp4_grouped_matmul_act")
 
 
 def mxfp4_act_bwd(grad_c, z, grad_z, act="none", grad_bias=None, group_list=None, group_list_type=1, workspace=None):
