@@ -158,6 +158,23 @@ def test_few_rows_exact(n, act):
          dtype="bf16" if n % 4 == 1 else "f32")
 
 
+# few rows, so many columns that a wave takes the whole K of its own: 16, 32 and
+# 64 rows a workgroup, one slab of K and several, the last one partial, odd
+# columns, rows past the total
+WIDE16, WIDE32, WIDE64 = [17, 0, 33, 16, 1, 40], [40, 0, 64, 33, 1, 70, 65], [64, 65, 1, 0, 120]
+
+
+@pytest.mark.parametrize("counts,rows,K,N,act,b_fmt,b_block", [
+    (WIDE16, 107, 1312, 11001, "none", "e2m1", 32), (WIDE16, 108, 288, 5471, "swiglu", "e2m1", 32),
+    (WIDE16, 107, 32, 11001, "relu", "e2m1", 32), (WIDE16, 107, 288, 11001, "none", "e4m3", 32),
+    (WIDE16, 107, 1184, 5471, "swiglu", "e2m1", 128), (WIDE32, 276, 608, 8777, "gelu", "e2m1", 32),
+    (WIDE32, 273, 288, 4390, "geglu", "e4m3", 32), (WIDE64, 250, 608, 16390, "none", "e2m1", 32),
+    (WIDE64, 253, 1056, 8210, "swiglu", "e2m1", 32)])
+def test_few_rows_of_many_columns_exact(counts, rows, K, N, act, b_fmt, b_block):
+    case(rows + K, counts, rows, K, N, act, b_fmt=b_fmt, b_block=b_block, bias="groups", res=K == 1312, keep_z=True,
+         dtype="bf16" if N % 2 else "f32")
+
+
 # many rows: whole and ragged tiles, the tail launch, odd columns
 MANY = [
     (None, 257, 256, 256, "relu"), (None, 300, 128, 100, "none"), (None, 600, 416, 257, "gelu"),
