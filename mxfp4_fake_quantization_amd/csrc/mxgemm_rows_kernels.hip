@@ -545,7 +545,15 @@ hipError_t launch_gemm_act(const GemmLaunch &L, const ActArgs &e, bool gated, hi
   //   K = 7168 -> 4096    103 / 128 / 120  138 / 145 / 130  201 / 165 / 150  340 / 251 / 209
   // (gated, 7168 -> 2 x 2048: 109 / 118 / 115 at 8, 130 / 122 / 118 at 12.)  A
   // longer K pays the larger workgroup's start and end off.
-  if (avg <= 64) {
+  // It also takes more rows where its pieces (64 rows by one run of columns) are
+  // at most one a CU: too few tiles to fill the chip, and here four waves share
+  // K.  us, the tiles and this form, by pieces: 64 (256 rows, 7168 -> 512) 43 /
+  // 20, 128 (1024, 7168 -> 256) 43 / 21, 90 (1787 in 3 groups, 3200 -> 96) 24 /
+  // 12, 185 (11217 in 10, 544 -> 32) 13 / 8, 256 (2048, 2048 -> 256) 18 / 19;
+  // 512 (1024, 2048 -> 2 x 512) 17 / 23, 640 (2048 in 8, 2048 -> 512) 19 / 27.
+  const int64_t pieces = (L.M / 64 + (L.group_list ? L.num_groups : (L.M % 64 ? 1 : 0))) *
+                         (gated ? (L.N + 15) / 16 : (L.N + 31) / 32);
+  if (avg <= 64 || pieces <= device_cus()) {
     const bool long_k = L.K >= 4096;
     const int mt = avg <= (long_k ? 10 : 18) ? 1 : (long_k || avg > 48 ? 4 : 2);
     return rows_act(L, e, gated, mt, 0, st);

@@ -191,6 +191,43 @@ def test_many_rows_exact(n, dtype):
          dtype=dtype)
 
 
+# as many rows, and columns enough for the tiles
+TILES = [
+    (None, 257, 256, 2100, "relu"), (None, 600, 416, 1025, "gelu"), ([300, 0, 212], 512, 384, 1030, "swiglu"),
+    ([130, 1, 400], 540, 160, 1060, "geglu"), ([0, 700, 3], 703, 96, 1315, "silu"), (None, 2000, 32, 331, "swiglu"),
+    ([200, 90, 310], 603, 288, 900, "geglu")]
+
+
+@pytest.mark.parametrize("n", range(len(TILES)))
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tiles_exact(n, dtype):
+    counts, rows, K, N, act = TILES[n]
+    case(150 + n, counts, rows, K, N, act, bias=(None, "one", "groups")[n % 3], res=n % 2 == 0, keep_z=n % 3 != 2,
+         dtype=dtype)
+
+
+@pytest.mark.parametrize("rows,counts,list_type", [(257, [257], 1), (300, [299], 1), (320, [250], 0), (290, [0], 1),
+                                                   (528, [513], 0)])
+@pytest.mark.parametrize("act,N", [("none", 2111), ("geglu", 1063)])
+def test_tiles_of_one_group_with_few_last_rows(rows, counts, list_type, act, N):
+    case(rows + 1, counts, rows, 320, N, act, bias="groups", res=True, keep_z=True, dtype="bf16", list_type=list_type)
+
+
+@pytest.mark.parametrize("a_fmt,b_fmt,a_block,b_block", [
+    ("e5m2", "e2m1", 32, 32), ("e4m3", "e4m3", 32, 32), ("e4m3", "e2m1", 128, 128), ("e5m2", "e4m3", 128, 32),
+    ("e4m3", "e4m3", 32, 128)])
+@pytest.mark.parametrize("K,act", [(96, "swiglu"), (640, "none"), (416, "gelu")])
+def test_tiles_of_formats_and_blocks(a_fmt, b_fmt, a_block, b_block, K, act):
+    case(K, [200, 130], 330, K, 1510, act, a_fmt, b_fmt, a_block, b_block, bias="groups", keep_z=True, dtype="f32",
+         list_type=K // 96 % 2)
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "swiglu"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tiles_of_realistic_operands(act, dtype):
+    case(4, [260, 140], 400, 512, 1200, act, bias="one", res=True, keep_z=True, dtype=dtype, exact=False)
+
+
 # one group whose last rows have a launch of their own, and a list that ends
 # before, inside and after them
 @pytest.mark.parametrize("rows,counts,list_type", [
@@ -219,14 +256,15 @@ def test_realistic_operands(rows, counts, act, dtype):
 
 
 def test_same_bits_as_the_plain_product():
-    """Without an epilogue, many rows: the plain product's result, bit for bit."""
+    """Without an epilogue, in tiles (many rows and columns): the plain
+    product's result, bit for bit."""
     g = torch.Generator().manual_seed(2)
     a, asc, _ = mx_codes(g, 900, 512, "e4m3", 32, False, 512)
-    b, bsc, _ = mx_codes(g, 2 * 300, 512, "e2m1", 32, False, 256)
+    b, bsc, _ = mx_codes(g, 2 * 1100, 512, "e2m1", 32, False, 256)
     gl = torch.tensor([500, 400], device="cuda")
-    args = [a.cuda(), asc.cuda(), b.view(2, 300, -1).cuda(), bsc.view(2, 300, -1).cuda()]
+    args = [a.cuda(), asc.cuda(), b.view(2, 1100, -1).cuda(), bsc.view(2, 1100, -1).cuda()]
     for dt in (torch.bfloat16, torch.float32):
-        c0, c1 = (torch.zeros(900, 300, dtype=dt, device="cuda") for _ in range(2))
+        c0, c1 = (torch.zeros(900, 1100, dtype=dt, device="cuda") for _ in range(2))
         M.mxfp4_grouped_matmul(*args, c0, group_list=gl)
         M.mxfp4_grouped_matmul_act(*args, c1, group_list=gl)
         assert torch.equal(c0, c1)
