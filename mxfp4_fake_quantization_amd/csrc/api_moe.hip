@@ -142,11 +142,11 @@ mxfp4_status_t mxfp4_moe_dispatch(const mxfp4_desc_t *desc, int32_t fmt, const v
   int64_t n;
   MXFP4_TRY(check_desc(desc, false, &n));
   MXFP4_TRY(check_slots(desc->rows, k, desc->cols, out_rows, "out_rows"));
-  if (!y && !q) return fail(MXFP4_EINVAL, "no output given");
-  if (!q != !scales) return fail(MXFP4_EINVAL, "q and scales come together");
   if (q && fmt != MXFP8_E4M3 && fmt != MXFP8_E5M2)
     return fail(MXFP4_EINVAL, "fmt %d is not MXFP8_E4M3 or MXFP8_E5M2", fmt);
-  if (n == 0 || out_rows == 0) return ok();
+  if (n == 0 || out_rows == 0) return ok();  // an array without elements may be NULL
+  if (!y && !q) return fail(MXFP4_EINVAL, "no output given");
+  if (!q != !scales) return fail(MXFP4_EINVAL, "q and scales come together");
   MXFP4_TRY(check_elems(x, desc->dtype, "x"));
   MXFP4_TRY(check_ptr(rows, 4, "rows"));
   if (y) MXFP4_TRY(check_elems(y, desc->dtype, "y"));
@@ -178,9 +178,10 @@ mxfp4_status_t mxfp4_moe_combine_bwd(int32_t dtype, int64_t tokens, int64_t cols
                                      void *grad_h, float *grad_weights, void *stream) {
   MXFP4_TRY(check_dtype(dtype));
   MXFP4_TRY(check_slots(tokens, k, cols, in_rows, "in_rows"));
-  if (!grad_h && !grad_weights) return fail(MXFP4_EINVAL, "no output given");
   const bool empty = cols == 0;  // every dot product is 0 then
-  if (tokens == 0 || (empty && !grad_weights)) return ok();
+  // no output elements: grad_h may be NULL because it is empty
+  if (tokens == 0 || ((empty || in_rows == 0) && !grad_weights)) return ok();
+  if (!grad_h && !grad_weights) return fail(MXFP4_EINVAL, "no output given");
   if (!empty) MXFP4_TRY(check_elems(grad_y, dtype, "grad_y"));
   MXFP4_TRY(check_ptr(rows, 4, "rows"));
   if (grad_weights && in_rows > 0 && !empty) MXFP4_TRY(check_elems(h, dtype, "h"));
