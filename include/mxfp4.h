@@ -48,7 +48,9 @@
  * block not 32 or 128, dtype not bf16/f32, or an axis combination a call
  * does not offer.  MXFP4_EHIP: a launch failed (the HIP error text is kept).
  * mxfp4_last_error() returns a message for the calling thread's last failed
- * call.  rows*cols == 0 returns MXFP4_OK without launching.
+ * call.  rows*cols == 0 returns MXFP4_OK without launching; the mxfp8, matrix
+ * product and mixture-of-experts calls then take NULL for arrays without
+ * elements too.
  *
  * Bitmap layouts (uint32 words; the saturation mask |x| > 6 * 2^k, one bit
  * per element, replacing the pages' bool tensor):

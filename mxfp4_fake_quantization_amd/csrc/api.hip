@@ -251,11 +251,11 @@ mxfp4_status_t mxfp8_quant(const mxfp4_desc_t *desc, int32_t fmt, const void *x,
   MXFP4_TRY(check_desc(desc, false, &n));
   if (fmt != MXFP8_E4M3 && fmt != MXFP8_E5M2)
     return fail(MXFP4_EINVAL, "fmt %d is not MXFP8_E4M3 or MXFP8_E5M2", fmt);
+  if (n == 0) return ok();  // arrays without elements may be NULL
   MXFP4_TRY(check_ptr(x, 16, "x"));
   MXFP4_TRY(check_ptr(q, 16, "q"));
   MXFP4_TRY(check_ptr(scales, 1, "scales"));
   if (!distinct({x, q, scales})) return fail(MXFP4_EINVAL, "x, q and scales must not alias");
-  if (n == 0) return ok();
   mxfp4::Mx8Launch L{desc->dtype, fmt, desc->rows, desc->cols, x, q, scales, desc->block};
   return hip_status(mxfp4::launch_mxfp8_rows(L, static_cast<hipStream_t>(stream)), "MXFP8 launch");
 }
@@ -275,13 +275,13 @@ mxfp4_status_t mxfp4_grouped_matmul(int32_t group_type, int64_t M, int64_t N, in
   if (group_list && (num_groups < 1 || (group_list_type != 0 && group_list_type != 1)))
     return fail(MXFP4_EINVAL, "num_groups must be >= 1 and group_list_type 0 or 1");
   MXFP4_TRY(check_opt(group_list, 8, "group_list"));
-  MXFP4_TRY(check_operand(a, "a", rows, K, k_blocks, true));
-  MXFP4_TRY(check_operand(b, "b", rows, K, k_blocks, false));
   if (out_dtype != MXGEMM_OUT_BF16 && out_dtype != MXGEMM_OUT_F32)
     return fail(MXFP4_EUNSUPPORTED, "out_dtype %d is not MXGEMM_OUT_BF16 or MXGEMM_OUT_F32", out_dtype);
+  if (M == 0 || N == 0) return ok();  // arrays without elements may be NULL
+  MXFP4_TRY(check_operand(a, "a", rows, K, k_blocks, true));
+  MXFP4_TRY(check_operand(b, "b", rows, K, k_blocks, false));
   MXFP4_TRY(check_ptr(c, out_dtype == MXGEMM_OUT_F32 ? 4 : 2, "c"));
   if (ldc < N) return fail(MXFP4_EINVAL, "ldc %lld < N %lld", (long long)ldc, (long long)N);
-  if (M == 0 || N == 0) return ok();
   if (rows && K == 0) return fail(MXFP4_EUNSUPPORTED, "K must be > 0 when groups split rows");
   mxfp4::GemmLaunch L{};
   L.group_type = group_type;
@@ -322,9 +322,11 @@ mxfp4_status_t mxfp8_quant_kmajor(const mxfp4_desc_t *desc, int32_t fmt, const v
     return fail(MXFP4_EUNSUPPORTED, "MXFP8 blocks are 32 elements (got block %d)", desc->block);
   if (fmt != MXFP8_E4M3 && fmt != MXFP8_E5M2)
     return fail(MXFP4_EINVAL, "fmt %d is not MXFP8_E4M3 or MXFP8_E5M2", fmt);
-  MXFP4_TRY(check_ptr(x, 16, "x"));
-  MXFP4_TRY(check_ptr(q_t, 16, "q_t"));
-  MXFP4_TRY(check_ptr(scales_t, 1, "scales_t"));
+  if (n > 0) {  // arrays without elements may be NULL
+    MXFP4_TRY(check_ptr(x, 16, "x"));
+    MXFP4_TRY(check_ptr(q_t, 16, "q_t"));
+    MXFP4_TRY(check_ptr(scales_t, 1, "scales_t"));
+  }
   const int64_t nb = (desc->rows + 31) / 32;
   int64_t need = nb;
   if (group_list) {

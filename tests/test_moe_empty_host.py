@@ -51,3 +51,34 @@ def test_combine_backward_of_nothing(lib, tokens, cols, in_rows):
 def test_combine_backward_of_something_needs_an_output(lib):
     f = lib.mxfp4_moe_combine_bwd
     assert f(BF16, 4, 64, 2, 8, P(A[0]), P(A[1]), P(A[2]), None, None, None, None) == EINVAL
+
+
+# ---- the older calls that the layer makes around them ---------------------------
+
+def test_mxfp8_of_nothing(lib):
+    for rows, cols in ((0, 64), (4, 0)):
+        d = desc(rows, cols)
+        assert lib.mxfp8_quant(ctypes.byref(d), 0, None, None, None, None) == OK
+        assert lib.mxfp8_quant(ctypes.byref(d), 5, None, None, None, None) == EINVAL
+        d = desc(rows, cols)
+        assert lib.mxfp8_quant_kmajor(ctypes.byref(d), 0, None, P(A[0]), 3, 1, 4, None, None, None) == OK
+        assert lib.mxfp8_quant_kmajor(ctypes.byref(d), 0, None, P(A[0]), 0, 1, 4, None, None, None) == EINVAL
+    d = desc(4, 64)
+    assert lib.mxfp8_quant(ctypes.byref(d), 0, None, None, None, None) == EINVAL
+    assert lib.mxfp8_quant_kmajor(ctypes.byref(d), 0, None, None, 0, 1, 1, None, None, None) == EINVAL
+
+
+def test_product_of_no_rows(lib):
+    """No rows of A (an empty batch): nothing to do, whatever the operands' addresses."""
+    def mm(group_type, m, n, k, kb, data, ld, gl):
+        a = M._MxOperand(data, data and data + 4096, 0, 32, ld, 4, 0, 0)
+        b = M._MxOperand(A[2], A[3], 4, 32, 64, 4, 0, 0)
+        return lib.mxfp4_grouped_matmul(group_type, m, n, k, ctypes.byref(a), ctypes.byref(b), P(gl), 3, 1, kb, 0, None,
+                                        n, None)
+    assert mm(M.GROUP_ROWS, 0, 48, 128, 0, None, 128, A[5]) == OK
+    assert mm(M.GROUP_ROWS, 5, 48, 128, 0, None, 128, A[5]) == EINVAL   # a is NULL
+    assert mm(M.GROUP_ROWS, 5, 0, 128, 0, None, 128, A[5]) == OK
+    assert mm(M.GROUP_K, 48, 48, 0, 0, None, 0, A[5]) == EINVAL          # no tokens: c, which gets zeros, is NULL
+    assert b"c is NULL" in lib.mxfp4_last_error()
+    assert mm(M.GROUP_K, 48, 48, 0, 1, None, 32, A[5]) == EINVAL
+    assert b"a is NULL" in lib.mxfp4_last_error()
