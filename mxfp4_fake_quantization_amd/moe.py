@@ -145,7 +145,8 @@ class PackedExperts:
         self.spec = spec
         _check_shapes(w1.new_empty(0, w1.shape[-1], dtype=torch.bfloat16), w1.new_empty(0, w1.shape[0]), w1, w2, spec)
         self.w1, self.w2 = _pack(w1), _pack(w2)
-        self.b1, self.b2 = b1, b2
+        # copies, as the packed weights are: all of one state
+        self.b1, self.b2 = (None if b is None else b.detach().clone() for b in (b1, b2))
 
     @torch.no_grad()
     def __call__(self, x, logits, residual=None, balance=None, out=None):

@@ -1,0 +1,24 @@
+"""What PackedExperts and MoELayer hold and refuse, on the CPU: the packing call
+is replaced by the identity, nothing reaches the library."""
+import pytest
+import torch
+
+from mxfp4_fake_quantization_amd import moe
+
+
+@pytest.fixture(autouse=True)
+def no_library(monkeypatch):
+    monkeypatch.setattr(moe, "_pack", lambda w: (w.detach().clone(), w.detach().clone()))
+
+
+def test_packed_experts_keep_the_biases_they_were_packed_with():
+    """Weights and biases of one state: a later training step changes neither."""
+    layer = moe.MoELayer(64, 32, 4, moe.MoESpec(k=2), bias=True)
+    experts = layer.packed()
+    before = [t.clone() for t in (experts.w1[0], experts.w2[0], experts.b1, experts.b2)]
+    with torch.no_grad():
+        for p in layer.parameters():
+            p.add_(1.0)
+    for a, b in zip(before, (experts.w1[0], experts.w2[0], experts.b1, experts.b2)):
+        assert torch.equal(a, b) and not b.requires_grad
+    assert moe.MoELayer(64, 32, 4).packed().b1 is None
