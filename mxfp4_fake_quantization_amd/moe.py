@@ -152,6 +152,8 @@ class PackedExperts:
     def __call__(self, x, logits, residual=None, balance=None, out=None):
         if x.dim() != 2 or x.dtype != torch.bfloat16 or x.shape[1] != self.w2[0].shape[1]:
             raise ValueError(f"x must be a bfloat16 tensor [tokens, {self.w2[0].shape[1]}]")
+        if tuple(logits.shape) != (x.shape[0], self.w1[0].shape[0]):
+            raise ValueError(f"logits must be [{x.shape[0]}, {self.w1[0].shape[0]}], got {list(logits.shape)}")
         weights, _, group_list, rows = _route(logits, self.spec, balance)
         _, h = _ffn(x, rows, group_list, self.w1, self.w2, self.b1, self.b2, self.spec)
         y = torch.empty_like(x) if out is None else out

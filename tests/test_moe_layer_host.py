@@ -22,3 +22,15 @@ def test_packed_experts_keep_the_biases_they_were_packed_with():
     for a, b in zip(before, (experts.w1[0], experts.w2[0], experts.b1, experts.b2)):
         assert torch.equal(a, b) and not b.requires_grad
     assert moe.MoELayer(64, 32, 4).packed().b1 is None
+
+
+def test_packed_experts_refuse_logits_of_another_width():
+    """Fewer logits than experts would route over the first experts alone."""
+    w1, w2 = torch.zeros(4, 64, 64, dtype=torch.bfloat16), torch.zeros(4, 64, 32, dtype=torch.bfloat16)
+    experts = moe.PackedExperts(w1, w2)
+    x = torch.zeros(5, 64, dtype=torch.bfloat16)
+    for shape in ((5, 3), (5, 5), (4, 4), (20,)):
+        with pytest.raises(ValueError, match=r"logits must be \[5, 4\]"):
+            experts(x, torch.zeros(*shape))
+    with pytest.raises(ValueError, match="64"):
+        experts(torch.zeros(5, 32, dtype=torch.bfloat16), torch.zeros(5, 4))
