@@ -29,6 +29,7 @@ from typing import Optional
 import torch
 import torch.nn.functional as F
 from torch import nn
+from torch.autograd.function import once_differentiable
 
 from . import (ACTIVATIONS, GROUP_K, kmajor_k_blocks, mxfp4_act_bwd, mxfp4_grouped_matmul, mxfp4_grouped_matmul_act,
                mxfp4_moe_combine, mxfp4_moe_combine_bwd, mxfp4_moe_dispatch, mxfp4_moe_plan, mxfp4_moe_route,
@@ -178,6 +179,7 @@ class _MoEFFN(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable  # raw buffers below: a second derivative would lack this layer's part
     def backward(ctx, dy):
         spec = ctx.spec
         logits, w1, w2, b1, b2, weights, ids, group_list, rows, xr, z, a, h = ctx.saved_tensors
@@ -228,7 +230,8 @@ class _MoEFFN(torch.autograd.Function):
 
 def moe_ffn(x, logits, w1, w2, spec: MoESpec = MoESpec(), b1=None, b2=None, balance=None):
     """Differentiable mixture-of-experts feed-forward layer: y [tokens, hidden]
-    (without a residual).  The selection bias ``balance`` has no gradient."""
+    (without a residual).  The selection bias ``balance`` has no gradient;
+    second derivatives are refused."""
     return _MoEFFN.apply(x, logits, w1, w2, b1, b2, balance, spec)
 
 
