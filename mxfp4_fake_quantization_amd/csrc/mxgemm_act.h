@@ -25,16 +25,28 @@ __device__ __forceinline__ float sigmoid_f(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * x));
 }
 
-// Phi(x) of the normal distribution, and exp(-x^2 / 2): the polynomial in
-// 1 / (1 + p |x| / sqrt 2) of Abramowitz and Stegun 7.1.26 times that
-// exponential, within 1.5e-7 / 2 of Phi everywhere, without a branch.
+// Phi(x) of the normal distribution, and exp(-x^2 / 2), without a branch: with w =
+// 3 |x| / (8 sqrt 2) and u = w / (1 + w), Phi(-|x|) = exp(-x^2 / 2) Q(u).  Q, of degree
+// 9 with Q(0) = 1/2, was fitted in 64 bits (least squares, weighted towards equal
+// ripple, its coefficients rounded to fp32 from the lowest): within 1.3e-8 of the
+// quotient for |x| up to 13, where exp(-x^2 / 2) reaches 2^-126.  In u, unlike in 1 -
+// u, the roundings of a small |x| stay small.  So the tail is good to (2.2 x^2 + 9)
+// 2^-24 of itself; over normal arguments gelu's error is 3.4e-8 of its norm and the
+// slope's 4.0e-8, as with 32-bit erf (3.8e-8, 4.0e-8).
 __device__ __forceinline__ float normal_cdf(float x, float *gauss) {
-  const float a = fabsf(x) * 0.707106781f;
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, a, 1.0f));
-  const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
-                           0.254829592f);
-  *gauss = __builtin_amdgcn_exp2f(-1.44269504f * (a * a));
-  const float tail = 0.5f * p * *gauss;
+  const float w = fminf(fabsf(x) * 0.265165043f, 1e30f);  // an infinite x keeps u = 1
+  const float u = w * __builtin_amdgcn_rcpf(1.0f + w);
+  float q = fmaf(u, -0.0303070173f, 0.131572232f);
+  q = fmaf(u, q, -0.171980724f);
+  q = fmaf(u, q, -0.0414950512f);
+  q = fmaf(u, q, 0.180597797f);
+  q = fmaf(u, q, 0.411485612f);
+  q = fmaf(u, q, -1.52645111f);
+  q = fmaf(u, q, 2.05108619f);
+  q = fmaf(u, q, -1.50450635f);
+  q = fmaf(u, q, 0.5f);
+  *gauss = __builtin_amdgcn_exp2f(-0.72134752f * (x * x));
+  const float tail = q * *gauss;
   return x > 0.0f ? 1.0f - tail : tail;
 }
 
