@@ -155,6 +155,14 @@ struct Turns {
 //
 // Few waves' worth of columns: the four waves of a workgroup share the K of
 // one column run (16 H columns, H tiles of output columns), in turns of 256.
+//
+// The waves a SIMD of both kernels are those that E2M1 weights run best with.  A
+// turn of E4M3 takes twice the registers: with 16 rows (both kernels) and with 64
+// (this one) its two sets do not fit and spill in the loop, 25 - 38 and 72 - 85
+// scratch accesses; E2M1 with 64 rows has 4 - 6 here.  8 experts of one row, 7168
+// -> 2 x 2048, take 73 us with E4M3 weights against 26 with E2M1, 32 groups of 6
+// rows, 2048 -> 7168, 135 against 64 (twice the bytes each); 32 and, over the
+// whole K, 64 rows do not spill: 32 groups of 25 rows 142 against 100.
 template <int AF, int BF, bool B32, int MT, int CT, int EPI>
 __global__ __launch_bounds__(kRowsThreads, (MT == 1 ? 4 : 2)) void mxgemm_rows_split_kernel(GemmArgs P, ActArgs E) {
   constexpr bool GATED = EPI == 2;

@@ -56,3 +56,32 @@ def test_no_scratch(asm, name):
     mine = {k: v for k, v in counts.items() if re.search(FILES[name], k)}
     assert mine, f"no kernels matched in {name}"
     assert not any(mine.values()), {k: v for k, v in mine.items() if v}
+
+
+# The few-rows forms whose two register sets do not fit the registers that their
+# waves a SIMD leave: (K shared by the waves, weights, 16-row tiles) -> the most
+# scratch accesses of a kernel, nearly all in its main loop.  All others have none.
+SPILLING = {("whole", "e4m3", 1): 31, ("split", "e4m3", 1): 38, ("split", "e4m3", 4): 85, ("split", "e2m1", 4): 6}
+
+
+def test_every_kernel_is_free_of_scratch_or_named(asm):
+    counts, cur = {}, None
+    for name, text in asm.items():
+        for line in text.split("\n"):
+            m = re.match(r"^(_Z\S+):", line)
+            if m:
+                cur = m.group(1)
+                counts[cur] = 0
+            elif cur and "scratch_" in line:
+                counts[cur] += 1
+    few = {}
+    for k, n in counts.items():
+        m = re.search(r"mxgemm_rows_(split_)?kernelILi[01]ELi([04])ELb[01]ELi([124])E", k)
+        if m:
+            form = ("split" if m.group(1) else "whole", "e4m3" if m.group(2) == "0" else "e2m1", int(m.group(3)))
+            few[form] = max(few.get(form, 0), n)
+        else:
+            assert n == 0, (k, n)
+    assert len(few) == 12, few                                   # every form was seen
+    for form, n in few.items():
+        assert n <= SPILLING.get(form, 0), (form, n)
