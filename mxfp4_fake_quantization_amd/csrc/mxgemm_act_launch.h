@@ -34,9 +34,13 @@ hipError_t act_tiles(const GemmArgs &a0, const ActArgs &e, hipStream_t st) {
   if (a.total > 0x7FFFFFFF) return hipErrorInvalidValue;
   a.ncu = device_cus();
   const int64_t half = a.ncu / 2;
-  // Row order and the tail launch up to 32 tiles a row (here it measured no
-  // slower than bands on the MoE layer, 944 and 947 us with 16, and 135 against
-  // 159 us on 4099 x 4095 x 4096); wider ones in bands, for the weights' re-reads.
+  // Row order with its tail launch up to 32 tiles a row, wider ones in bands for
+  // the weights' re-reads.  Measured, row order / bands: the tail's small tiles
+  // save up to 40 % where the rounds are few (5000 rows in 8 groups, 2048 -> 2560,
+  // 10 tiles a row, 50 / 82 us, -> 4864, 19 tiles, 94 / 125; 4099 rows, 4096 ->
+  // 4095 98 / 157; 16384 rows, 7168 -> 2 x 2304, 18 tiles, 562 / 607), bands 1 - 5 %
+  // where there are many (16384 rows, 2048 -> 4096, 16 tiles, 230 / 225, -> 8192,
+  // 32 tiles, 421 / 408; 32768 rows, 2048 -> 7168, 28 tiles, 695 / 663).
   a.row_order = a.tiles_n <= 32;
   if (a.total > half || !a.row_order) {
     const hipError_t r = act_tiles_one<AF, BF, false, EPI>(a, e, a.total, st);
