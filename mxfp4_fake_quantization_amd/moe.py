@@ -253,7 +253,8 @@ class MoELayer(nn.Module):
 
     def forward(self, x):
         flat = x.reshape(-1, x.shape[-1])
-        y = moe_ffn(flat, F.linear(flat, self.router.weight), self.w1, self.w2, self.spec, self.b1, self.b2)
+        logits = F.linear(flat.to(self.router.weight.dtype), self.router.weight)
+        y = moe_ffn(flat, logits, self.w1, self.w2, self.spec, self.b1, self.b2)
         return x + y.view(x.shape)
 
     def packed(self) -> PackedExperts:

@@ -34,3 +34,21 @@ def test_packed_experts_refuse_logits_of_another_width():
             experts(x, torch.zeros(*shape))
     with pytest.raises(ValueError, match="64"):
         experts(torch.zeros(5, 32, dtype=torch.bfloat16), torch.zeros(5, 4))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_layer_with_weights_of_another_type_than_x(dtype, monkeypatch):
+    """float32 master weights: the router takes x to its own type."""
+    layer = moe.MoELayer(64, 32, 4, dtype=dtype)
+    x, seen = torch.randn(2, 5, 64).bfloat16(), {}
+
+    def ffn(flat, logits, *a):
+        seen.update(x=flat, logits=logits)
+        return torch.zeros_like(flat)
+    monkeypatch.setattr(moe, "moe_ffn", ffn)
+    y = layer(x)
+    assert y.dtype == torch.bfloat16 and torch.equal(y, x) and seen["x"].dtype == torch.bfloat16
+    assert seen["logits"].dtype == dtype
+    want = x.view(10, 64).to(dtype) @ layer.router.weight.t()
+    assert torch.allclose(seen["logits"], want, rtol=2.0 ** -7 if dtype == torch.bfloat16 else 1e-5, atol=1e-2 if
+                          dtype == torch.bfloat16 else 1e-5)
