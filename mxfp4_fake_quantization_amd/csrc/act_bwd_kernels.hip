@@ -21,8 +21,8 @@ namespace {
 constexpr int kActBwdThreads = 256;
 // Rows of a run and lanes side by side (8 columns each), logarithms.  Small
 // pieces spread evenly over the CUs: swiglu with bias on 32768 x 2 x 2048 takes
-// 138 us (4.9 TB/s); 64-row runs 146, 64 lanes 151, 256 lanes of 64-row runs
-// (two workgroups a CU and a few more) 176.
+// 128 us (5.2 TB/s).  Measured when it took 138: 64-row runs 146, 64 lanes 151,
+// 256 lanes of 64-row runs (two workgroups a CU and a few more) 176.
 constexpr int kRunLog = 5, kColsLog = 5;
 
 struct ActBwdArgs {

@@ -13,9 +13,12 @@
 // than 32 values a lane or k > 16), every lane V consecutive experts of ONE
 // group (lanes are dealt to the groups first), so the loads are 16-byte
 // pieces, group sums are reductions over a lane range, and the maximum of a
-// token is one chain of DPP row operations.  Each of the k steps takes the
-// token's largest v and its lowest index by two such chains and clears it.
-// Bound by the VALU work of the k steps, not by the logits' bytes.
+// token is one chain of DPP row operations.  Up to k = 8 (16 lanes a token) the
+// lanes sort their values and merge them (top_by_sorting); where that does not
+// settle the choice, and for larger k, each of k steps takes the token's largest
+// v and its lowest index by two such chains and clears it.  Bound by VALU work,
+// not by the logits' bytes: 32768 tokens of 256 experts in 8 groups, k = 8, take
+// 17 us; the VALU issues for 87 % of the busy cycles (1005 instructions a wave).
 #include "moe_kernels.h"
 #include "mxfp4_device.h"
 #include "mxfp4_rows8.h"

@@ -32,7 +32,7 @@ __device__ __forceinline__ float sigmoid_f(float x) {
 // quotient for |x| up to 13, where exp(-x^2 / 2) reaches 2^-126.  In u, unlike in 1 -
 // u, the roundings of a small |x| stay small.  So the tail is good to (2.2 x^2 + 9)
 // 2^-24 of itself; over normal arguments gelu's error is 3.4e-8 of its norm and the
-// slope's 4.0e-8, as with 32-bit erf (3.8e-8, 4.0e-8).
+// slope's 3.8e-8, as with 32-bit erf (3.8e-8, 4.0e-8).
 __device__ __forceinline__ float normal_cdf(float x, float *gauss) {
   const float w = fminf(fabsf(x) * 0.265165043f, 1e30f);  // an infinite x keeps u = 1
   const float u = w * __builtin_amdgcn_rcpf(1.0f + w);

@@ -4,10 +4,12 @@
 // A group of a few rows reads its whole weight for them: the time is the
 // weights' bytes.  A workgroup takes up to 16 MT rows of one group and 16 CT
 // rows of B, as v_mfma_scale_f32_16x16x128_f8f6f4 tiles: its lanes 16 apart
-// hold 64 consecutive bytes of a B row, so B and A go from memory to the
-// matrix core without LDS.  K is split over the four waves in turns of 256
-// (two steps); a wave loads its next turn while the current one multiplies, and
-// the waves' sums meet in LDS once, where the epilogue takes them.  Operand
+// hold 64 consecutive bytes of a B row, so B goes from memory to the matrix
+// core without LDS, in turns of 256 along K (two steps), each loaded while the
+// one before multiplies.  With few workgroups the four waves share the turns of
+// one column run, read A as they read B, and their sums meet in LDS once, where
+// the epilogue takes them; with many each wave has a run and the whole K of its
+// own, and A passes through LDS.  Operand
 // layout of the instruction (lane l: row or column l % 16, quarter q = l / 16):
 // fp8 bytes 0-15 are K 16 q.., bytes 16-31 K 64 + 16 q..; fp4 nibble j is K
 // 32 q + j; the scale byte is that of K-block q; result register v is row
