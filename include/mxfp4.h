@@ -537,6 +537,91 @@ mxfp4_status_t mxfp4_act_bwd(int32_t dtype, int32_t act, int64_t rows, int64_t c
                              int32_t num_groups, int32_t group_list_type, void *workspace,
                              int64_t workspace_bytes, void *stream);
 
+/* ---- low-rank adapters beside a shared projection ----------------------------- */
+
+typedef struct mxfp4_adapter {
+  int32_t dtype;         /* of x, a, b, base, y and the gradients                 */
+  int32_t rank;          /* 1 .. 128 (adapters of smaller ranks: rows of 0)       */
+  int32_t adapters;      /* >= 1                                                  */
+  int32_t reserved;      /* must be 0                                             */
+  int64_t tokens;
+  int64_t in_features, out_features;  /* >= 1                                     */
+} mxfp4_adapter_t;
+
+/*
+ * The adapters of many requests in one call, beside a projection they share:
+ *     u[t] = x[t] A_i^T,   y[t] = base[t] + scale[i] * u[t] B_i^T,   i = ids[t],
+ * x [tokens, ldx], a [adapters, rank, in], b [adapters, out, rank], base and y
+ * [tokens, ld].  A token whose id is outside [0, adapters) has no adapter: y =
+ * base, u = 0.  base (the shared projection's result) may be NULL (0), and y may
+ * be base.  scale NULL: 1.  ids NULL: adapter 0 for all.  Tokens may come in any
+ * order; an adapter's weights are read once for each 64 consecutive rows that hold
+ * it, so tokens of one adapter next to one another are fastest.  u [tokens,
+ * rank] fp32 is written when given (the backward pass reads it).  Sums and u in
+ * fp32; y is rounded once.  Elements of any alignment, rows ld apart; a row's
+ * values depend on that row alone.  workspace: mxfp4_adapter_workspace bytes (-1
+ * for refused arguments), 16-byte aligned, in use until the call's kernels are done.
+ */
+int64_t mxfp4_adapter_workspace(const mxfp4_adapter_t *desc);
+mxfp4_status_t mxfp4_adapter_fwd(const mxfp4_adapter_t *desc, const void *x, int64_t ldx, const void *a,
+                                 const void *b, const float *scale, const int32_t *ids, const void *base,
+                                 int64_t ld_base, void *y, int64_t ldy, float *u, void *workspace,
+                                 int64_t workspace_bytes, void *stream);
+
+/*
+ * Its gradients, each NULL when not wanted:
+ *     du[t] = scale[i] * grad_y[t] B_i,   grad_x[t] = base[t] + du[t] A_i,
+ *     grad_a[i] = sum over t of du[t]^T x[t],
+ *     grad_b[i] = scale[i] * sum over t of grad_y[t]^T u[t]
+ * over the tokens with ids[t] = i (0 for an adapter without any).  base, the
+ * gradient that the shared projection gives x, may be NULL (0); grad_x may be base.
+ * x is needed for grad_a, a for grad_x, u (as the forward pass wrote it) for
+ * grad_b.  The gradient of the forward pass' base is grad_y itself.  Sums in fp32,
+ * each output rounded once; no atomics, the same bits on every call.  adapters <=
+ * 1024.  workspace: mxfp4_adapter_bwd_workspace bytes for the gradients wanted.
+ */
+int64_t mxfp4_adapter_bwd_workspace(const mxfp4_adapter_t *desc, int32_t grad_a, int32_t grad_b);
+mxfp4_status_t mxfp4_adapter_bwd(const mxfp4_adapter_t *desc, const void *grad_y, int64_t ld_grad_y,
+                                 const void *x, int64_t ldx, const void *a, const void *b, const float *scale,
+                                 const int32_t *ids, const float *u, const void *base, int64_t ld_base,
+                                 void *grad_x, int64_t ld_grad_x, void *grad_a, void *grad_b, void *workspace,
+                                 int64_t workspace_bytes, void *stream);
+
+/* ---- the norm over many gradients, and clipping -------------------------------- */
+
+enum { MXNORM_INF = 0, MXNORM_L1 = 1, MXNORM_L2 = 2 };
+
+typedef struct mxfp4_grad_item {
+  const void *grad;      /* device, count contiguous elements                      */
+  void *out;             /* device, mxfp4_grad_clip only: may be grad              */
+  int64_t count;
+  int32_t dtype;         /* MXFP4_BF16 or MXFP4_F32; may differ between tensors    */
+  int32_t reserved;      /* must be 0                                              */
+} mxfp4_grad_item_t;
+
+/*
+ * norm (one float on the device) = the largest |g|, the sum of |g|, or the square
+ * root of the sum of g^2 over all elements of n tensors (0 without any), summed in
+ * 64 bits and rounded once.  A NaN anywhere gives NaN.  items is a host array, read
+ * during the call.  workspace: mxfp4_grad_norm_workspace(n, elements of all tensors)
+ * bytes (-1 for refused arguments), 16-byte aligned, in use until the call's kernels
+ * are done.
+ */
+int64_t mxfp4_grad_norm_workspace(int32_t n, int64_t elements);
+mxfp4_status_t mxfp4_grad_norm(int32_t norm_type, int32_t n, const mxfp4_grad_item_t *items, float *norm,
+                               void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * out = grad * min(1, max_norm / (norm + 1e-6)) for every tensor, with the norm of
+ * the same tensors (compute_norm 1: computed and written to norm) or one that
+ * the caller holds (0: norm is read, for instance a norm over several processes;
+ * workspace may be NULL).  An infinite norm gives 0 (NaN for infinite elements), a
+ * NaN norm NaN.  Each element is rounded once.  out is grad, or overlaps no tensor.
+ */
+mxfp4_status_t mxfp4_grad_clip(int32_t norm_type, int32_t n, const mxfp4_grad_item_t *items, float max_norm,
+                               int32_t compute_norm, float *norm, void *workspace, int64_t workspace_bytes,
+                               void *stream);
+
 /* Message for the calling thread's most recent failed call ("" if none). */
 const char *mxfp4_last_error(void);
 

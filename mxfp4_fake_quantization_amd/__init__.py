@@ -623,3 +623,9 @@ from . import moe_ops as _moe_ops  # noqa: E402
 from .moe_ops import *  # noqa: E402,F401,F403
 
 __all__ += _moe_ops.__all__
+
+# Low-rank adapters and the gradient norm, likewise.
+from . import adapter_ops as _adapter_ops  # noqa: E402
+from .adapter_ops import *  # noqa: E402,F401,F403
+
+__all__ += _adapter_ops.__all__

@@ -24,7 +24,8 @@ ARCH = "gfx950"
 SOURCES = ["api.hip", "row_kernels.hip", "col_kernels.hip", "ste_kernels.hip",
            "kmajor_kernels.hip", "mxfp8_kernels.hip", "mxgemm_kernels.hip",
            "api_moe.hip", "moe_route_kernels.hip", "moe_rows_kernels.hip",
-           "mxgemm_act_kernels.hip", "mxgemm_gated_kernels.hip", "mxgemm_rows_kernels.hip", "act_bwd_kernels.hip"]
+           "mxgemm_act_kernels.hip", "mxgemm_gated_kernels.hip", "mxgemm_rows_kernels.hip", "act_bwd_kernels.hip",
+           "api_adapter.hip", "adapter_fwd_kernels.hip", "adapter_bwd_kernels.hip", "grad_norm_kernels.hip"]
 CFLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 

@@ -1,0 +1,288 @@
+// adapter_bwd_kernels.hip -- the backward pass of the low-rank adapters on gfx950:
+//     du[t] = s_i grad_y[t] B_i              (shrink with B read across its rows)
+//     grad_x[t] = base[t] + du[t] A_i        (expand with A read across its rows)
+//     grad_A_i = sum over t of du[t]^T x[t],  grad_B_i = s_i sum over t of grad_y[t]^T u[t]
+// i = ids[t].  grad_y is read twice, x once; the sums over rows are split into
+// pieces whose parts are added in their order: no atomics, the same bits each time.
+#include "adapter_launch.h"
+
+namespace mxfp4 {
+namespace {
+
+// ---- weight gradients ----------------------------------------------------------------
+//
+// out[r, c] = sum over an adapter's rows t of v[t, r] z[t, c], (v, z) = (du, x) or
+// (u, grad_y).  A workgroup takes 16 PE columns of a piece of rows, its four waves
+// every fourth step of KF rows.  The sum runs down the rows of both operands, so a
+// lane loads PE rows of 16 bytes and turns them in registers (one v_perm per two
+// bf16 elements, no LDS): its 16 bytes are then column PE l + j of fragment j.
+// v, in fp32, is split into two bf16 operands as in the other products.
+
+constexpr int kGradWaves = 4;
+
+struct GradSide {
+  const uint8_t *z;    // [tokens, ld]
+  const float *v;      // [tokens, rank]
+  float *part;         // [pieces][rank * cols]
+  int64_t ld, cols;
+  int groups;          // of columns; 0: not wanted
+};
+
+struct GradArgs {
+  GradSide a, b;
+  const int32_t *order, *first;
+  const int4 *pieces;
+  int adapters, rank;
+};
+
+template <int DT, int RT>
+__global__ __launch_bounds__(64 * kGradWaves) void adapter_grad_kernel(GradArgs A) {
+  using T = Tile<DT>;
+  __shared__ float sums[kGradWaves][T::PE][64][4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
+  const int groups = A.a.groups + A.b.groups;
+  const int piece = blockIdx.x / groups, g = blockIdx.x % groups;
+  if (piece >= A.first[A.adapters]) return;
+  const bool is_b = g >= A.a.groups;
+  const GradSide S = is_b ? A.b : A.a;
+  const int64_t n0 = (int64_t)(is_b ? g - A.a.groups : g) * (16 * T::PE);
+  const int4 pc = A.pieces[piece];
+  const int count = pc.z;
+  const int32_t *order = A.order + pc.y;
+  const int64_t col = n0 + T::PE * i;
+  const bool inside = n0 + 16 * T::PE <= S.cols;
+  int vr[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) vr[r] = 16 * r + i < A.rank ? 16 * r + i : A.rank - 1;
+  f32x4 acc[RT][T::PE];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int j = 0; j < T::PE; ++j) acc[r][j] = f32x4{0, 0, 0, 0};
+  for (int st = wave; st * T::KF < count; st += kGradWaves) {
+    const int at = st * T::KF + T::PE * q;
+    int32_t row[T::PE];
+#pragma unroll
+    for (int e = 0; e < T::PE; ++e) row[e] = order[at + e < count ? at + e : count - 1];
+    u32x4 z[T::PE];
+    float v[RT][T::PE];
+#pragma unroll
+    for (int e = 0; e < T::PE; ++e) {
+      const uint8_t *p = S.z + (row[e] * S.ld + col) * T::ES;
+      z[e] = inside ? ld_frag(p) : ld_frag_n<DT>(p, S.cols - col);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) v[r][e] = S.v[(int64_t)row[e] * A.rank + vr[r]];
+    }
+    if ((st + 1) * T::KF > count) {  // rows past the piece count as 0
+#pragma unroll
+      for (int e = 0; e < T::PE; ++e)
+        if (at + e >= count) {
+          z[e] = u32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int r = 0; r < RT; ++r) v[r][e] = 0.0f;
+        }
+    }
+    u32x4 hi[RT], lo[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        if constexpr (DT == kBF16) {
+          hi[r][d] = pack_hi(v[r][2 * d], v[r][2 * d + 1]);
+          lo[r][d] = pack_lo(v[r][2 * d], v[r][2 * d + 1]);
+        } else {
+          hi[r][d] = __builtin_bit_cast(uint32_t, v[r][d]);
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < T::PE; ++j) {
+      const u32x4 zf = turned<DT>(z, j);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        acc[r][j] = mma<DT>(hi[r], zf, acc[r][j]);
+        if constexpr (DT == kBF16) acc[r][j] = mma<DT>(lo[r], zf, acc[r][j]);
+      }
+    }
+  }
+  // the waves' sums, 16 ranks at a time
+  float *out = S.part + (int64_t)piece * A.rank * S.cols;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < T::PE; ++j) *reinterpret_cast<f32x4 *>(sums[wave][j][lane]) = acc[r][j];
+    __syncthreads();
+    if (!is_b) {  // [rank, cols]: a wave takes rank 4 q + wave, a lane PE columns
+      const int rank = 16 * r + 4 * q + wave;
+      if (rank < A.rank) {
+        float f[T::PE];
+#pragma unroll
+        for (int j = 0; j < T::PE; ++j) {
+          f[j] = sums[0][j][lane][wave];
+#pragma unroll
+          for (int w = 1; w < kGradWaves; ++w) f[j] += sums[w][j][lane][wave];
+        }
+        float *p = out + rank * S.cols + col;
+#pragma unroll
+        for (int j = 0; j < T::PE; ++j)
+          if (col + j < S.cols) p[j] = f[j];
+      }
+    } else {  // [cols, rank]: a wave takes every fourth column, a lane 4 ranks
+      for (int j = wave; j < T::PE; j += kGradWaves) {
+        f32x4 f = *reinterpret_cast<f32x4 *>(sums[0][j][lane]);
+#pragma unroll
+        for (int w = 1; w < kGradWaves; ++w) f += *reinterpret_cast<f32x4 *>(sums[w][j][lane]);
+        const int r0 = 16 * r + 4 * q;
+        float *p = out + (col + j) * A.rank + r0;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (col + j < S.cols && r0 + v < A.rank) p[v] = f[v];
+      }
+    }
+  }
+}
+
+// Each adapter's pieces added up, in their order, and rounded once; 0 for an adapter
+// without rows.
+struct GradSumArgs {
+  const float *part_a, *part_b;
+  uint8_t *grad_a, *grad_b;
+  const int32_t *first;
+  const float *scale;
+  int64_t size_a, size_b;        // elements of an adapter's gradient
+  int blocks_a, blocks_b;        // workgroups of each
+};
+constexpr int kSumThreads = 256, kSumEach = 4;
+
+template <int DT>
+__global__ __launch_bounds__(kSumThreads) void adapter_grad_sum_kernel(GradSumArgs A) {
+  const int blocks = A.blocks_a + A.blocks_b;
+  const int a = blockIdx.x / blocks;
+  int b = blockIdx.x % blocks;
+  const bool is_b = b >= A.blocks_a;
+  if (is_b) b -= A.blocks_a;
+  const int64_t size = is_b ? A.size_b : A.size_a;
+  const float *part = is_b ? A.part_b : A.part_a;
+  uint8_t *out = is_b ? A.grad_b : A.grad_a;
+  const int64_t e0 = ((int64_t)b * kSumThreads + threadIdx.x) * kSumEach;
+  if (e0 >= size) return;
+  const int lo = A.first[a], hi = A.first[a + 1];
+  const float s = is_b && A.scale ? A.scale[a] : 1.0f;
+  float f[kSumEach] = {};
+  for (int p = lo; p < hi; ++p) {
+    const u32x4 v = ld_frag_n<kF32>(reinterpret_cast<const uint8_t *>(part + p * size + e0), size - e0);
+#pragma unroll
+    for (int j = 0; j < kSumEach; ++j) f[j] += bits_f32(v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < kSumEach; ++j)
+    if (e0 + j < size) {
+      const int64_t at = a * size + e0 + j;
+      if (DT == kBF16) reinterpret_cast<uint16_t *>(out)[at] = (uint16_t)pack_bf16(s * f[j], 0.0f);
+      else reinterpret_cast<float *>(out)[at] = s * f[j];
+    }
+}
+
+// ---- host ------------------------------------------------------------------------------
+
+// Rows of a piece: about 1024 workgroups over the columns of both gradients.
+int piece_rows(int64_t tokens, int64_t in, int64_t out) {
+  const int64_t groups = (in + 127) / 128 + (out + 127) / 128;
+  const int64_t per = (tokens * groups / 1024 + 127) / 128 * 128;
+  return (int)(per < 128 ? 128 : per > 4096 ? 4096 : per);
+}
+
+struct BwdSpace {  // offsets of the workspace's parts, 16-byte aligned
+  int64_t du, order, first, pieces, part_a, part_b, total;
+  int64_t most;    // pieces
+  int rows;
+};
+BwdSpace bwd_space(int64_t tokens, int64_t in, int64_t out, int rank, int adapters, bool grad_a, bool grad_b) {
+  BwdSpace S;
+  int64_t at = 0;
+  auto take = [&at](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 15) / 16 * 16;
+    return here;
+  };
+  S.rows = piece_rows(tokens, in, out);
+  S.most = tokens / S.rows + (adapters < tokens ? adapters : tokens);
+  S.du = take(4 * tokens * rank);
+  const bool any = grad_a || grad_b;
+  S.order = take(any ? 4 * tokens : 0);
+  S.first = take(any ? 4 * (int64_t)(adapters + 1) : 0);
+  S.pieces = take(any ? 16 * S.most : 0);
+  S.part_a = take(grad_a ? 4 * S.most * rank * in : 0);
+  S.part_b = take(grad_b ? 4 * S.most * rank * out : 0);
+  S.total = at;
+  return S;
+}
+
+template <int DT>
+hipError_t launch_grads(const AdapterBwdLaunch &L, const BwdSpace &S, hipStream_t stream) {
+  constexpr int cols = 16 * Tile<DT>::PE;
+  uint8_t *ws = L.workspace;
+  float *part_a = reinterpret_cast<float *>(ws + S.part_a), *part_b = reinterpret_cast<float *>(ws + S.part_b);
+  const int32_t *first = reinterpret_cast<const int32_t *>(ws + S.first);
+  GradArgs G{};
+  if (L.grad_a) G.a = {static_cast<const uint8_t *>(L.x), reinterpret_cast<const float *>(ws + S.du), part_a, L.ldx, L.in,
+                       (int)((L.in + cols - 1) / cols)};
+  if (L.grad_b) G.b = {static_cast<const uint8_t *>(L.grad_y), L.u, part_b, L.ld_gy, L.out,
+                       (int)((L.out + cols - 1) / cols)};
+  G.order = reinterpret_cast<const int32_t *>(ws + S.order);
+  G.first = first;
+  G.pieces = reinterpret_cast<const int4 *>(ws + S.pieces);
+  G.adapters = L.adapters;
+  G.rank = L.rank;
+  if (S.most > 0) {
+    const unsigned grid = (unsigned)(S.most * (G.a.groups + G.b.groups));
+    const int rt = (L.rank + 15) / 16, th = 64 * kGradWaves;
+    if (rt <= 1) adapter_grad_kernel<DT, 1><<<grid, th, 0, stream>>>(G);
+    else if (rt <= 2) adapter_grad_kernel<DT, 2><<<grid, th, 0, stream>>>(G);
+    else if (rt <= 4) adapter_grad_kernel<DT, 4><<<grid, th, 0, stream>>>(G);
+    else adapter_grad_kernel<DT, 8><<<grid, th, 0, stream>>>(G);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int64_t sa = L.grad_a ? L.rank * L.in : 0, sb = L.grad_b ? L.rank * L.out : 0;
+  constexpr int each = kSumThreads * kSumEach;
+  GradSumArgs R{part_a, part_b, static_cast<uint8_t *>(L.grad_a), static_cast<uint8_t *>(L.grad_b), first, L.scale, sa, sb,
+                (int)((sa + each - 1) / each), (int)((sb + each - 1) / each)};
+  adapter_grad_sum_kernel<DT><<<(unsigned)((R.blocks_a + R.blocks_b) * L.adapters), kSumThreads, 0, stream>>>(R);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t adapter_bwd_workspace(int64_t tokens, int64_t in, int64_t out, int rank, int adapters, bool grad_a, bool grad_b) {
+  return bwd_space(tokens, in, out, rank, adapters, grad_a, grad_b).total;
+}
+
+hipError_t launch_adapter_bwd(const AdapterBwdLaunch &L, hipStream_t stream) {
+  const BwdSpace S = bwd_space(L.tokens, L.in, L.out, L.rank, L.adapters, L.grad_a, L.grad_b);
+  uint8_t *ws = L.workspace;
+  float *du = reinterpret_cast<float *>(ws + S.du);
+  PlanArgs P{};
+  if (L.grad_a || L.grad_b) {
+    P.order = reinterpret_cast<int32_t *>(ws + S.order);
+    P.first = reinterpret_cast<int32_t *>(ws + S.first);
+    P.pieces = reinterpret_cast<int4 *>(ws + S.pieces);
+    P.rows = S.rows;
+    while ((1 << P.bits) < L.adapters) ++P.bits;
+  }
+  const int64_t part = L.tokens * L.rank;
+  ShrinkArgs D{static_cast<const uint8_t *>(L.grad_y), static_cast<const uint8_t *>(L.b), L.ids, L.scale, du, L.tokens,
+               L.ld_gy, L.out, part, L.adapters, L.rank, 1};
+  hipError_t e = launch_shrink<true>(L.dtype, D, P, stream);
+  if (e != hipSuccess) return e;
+  if (L.grad_x && L.tokens > 0) {
+    ExpandArgs X{du, static_cast<const uint8_t *>(L.a), L.ids, nullptr, static_cast<const uint8_t *>(L.base),
+                 static_cast<uint8_t *>(L.grad_x), nullptr, L.tokens, L.in, L.ld_base, L.ld_gx, part, L.adapters, L.rank, 1};
+    e = launch_expand<true>(L.dtype, X, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (!L.grad_a && !L.grad_b) return hipSuccess;
+  return L.dtype == kBF16 ? launch_grads<kBF16>(L, S, stream) : launch_grads<kF32>(L, S, stream);
+}
+
+}  // namespace mxfp4

@@ -1,0 +1,350 @@
+// adapter_device.h -- what the low-rank adapters' kernels share: matrix-core
+// tiles of 16-byte fragments, the rows of a window by adapter, and the two
+// products
+//     u[t, r] = sum_k x[t, k] W[r, k]     ("shrink": k long, r <= 128)
+//     y[t, n] = base[t, n] + sum_r u[t, r] W[n, r]     ("expand")
+// with the weights of each row's adapter.  The forward pass has W = A [r, in],
+// then W = B [out, r]; the backward pass has the same products with the
+// transposes of B and A, which are read across their rows.
+//
+// Fragments.  An operand of a 16 x 16 tile is 16 bytes a lane: lane l holds row
+// l % 16 and, of the summed dimension, 8 bf16 (one v_mfma 16x16x32) or 4 fp32
+// values (four v_mfma 16x16x4, one a component) of part q = l / 16.  A sum does
+// not depend on the order of its terms as long as both operands agree, so every
+// fragment is one contiguous 16-byte piece of a row.  The result's lane l holds
+// row 4 q + v (v = 0..3) of the first operand and row l % 16 of the second.
+//
+// u is kept in fp32.  As an operand of a bf16 product it is split into
+// u = hi + lo, hi the upper 16 bits and lo the rest rounded to bf16: 2^-16 of u
+// are lost at most, so y is rounded once, to its type.
+#pragma once
+
+#include "adapter_kernels.h"
+#include "mxfp4_rows8.h"
+
+namespace mxfp4 {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef u32x4 u32x4_a1 __attribute__((aligned(2)));
+
+template <int DT>
+struct Tile {
+  static constexpr int ES = DT == kBF16 ? 2 : 4;  // bytes of an element
+  static constexpr int PE = 16 / ES;              // elements of a fragment's lane
+  static constexpr int KF = 4 * PE;               // summed elements of a fragment
+};
+
+template <int DT>
+__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (DT == kBF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(bits_f32(a[i]), bits_f32(b[i]), c, 0, 0, 0);
+    return c;
+  }
+}
+
+// A whole 16-byte piece at any element alignment.
+__device__ __forceinline__ u32x4 ld_frag(const uint8_t *p) { return *reinterpret_cast<const u32x4_a1 *>(p); }
+
+// The first n elements of a piece, the others 0.
+template <int DT>
+__device__ __forceinline__ u32x4 ld_frag_n(const uint8_t *p, int64_t n) {
+  u32x4 w = {0, 0, 0, 0};
+  if (n >= Tile<DT>::PE) return ld_frag(p);
+#pragma unroll
+  for (int j = 0; j < Tile<DT>::PE; ++j)
+    if (j < n) {
+      if (DT == kBF16) w[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[j] << (16 * (j & 1));
+      else w[j & 3] = reinterpret_cast<const uint32_t *>(p)[j];
+    }
+  return w;
+}
+
+template <int DT>
+__device__ __forceinline__ void st_frag_n(uint8_t *p, u32x4 w, int64_t n) {
+  if (n >= Tile<DT>::PE) {
+    *reinterpret_cast<u32x4_a1 *>(p) = w;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < Tile<DT>::PE; ++j)
+    if (j < n) {
+      if (DT == kBF16) reinterpret_cast<uint16_t *>(p)[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+      else reinterpret_cast<uint32_t *>(p)[j] = w[j & 3];
+    }
+}
+
+// A fragment's lane across rows: elements (k0 + e, col), e < PE, of a matrix with
+// `ld` elements a row; without WHOLE, rows from `rows` on read as 0.  (col is
+// inside the row.)
+template <int DT, bool WHOLE>
+__device__ __forceinline__ u32x4 ld_across(const uint8_t *p, int64_t k0, int64_t rows, int64_t ld, int64_t col) {
+  u32x4 w = {0, 0, 0, 0};
+  const int64_t at = k0 * ld + col;
+#pragma unroll
+  for (int e = 0; e < Tile<DT>::PE; ++e) {
+    if (WHOLE || k0 + e < rows) {
+      if (DT == kBF16) w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[at + e * ld] << (16 * (e & 1));
+      else w[e & 3] = reinterpret_cast<const uint32_t *>(p)[at + e * ld];
+    }
+  }
+  return w;
+}
+
+// PE rows of PE elements a lane become PE fragments' lanes: fragment j holds
+// element j of every row.
+template <int DT>
+__device__ __forceinline__ u32x4 turned(const u32x4 (&rows)[Tile<DT>::PE], int j) {
+  u32x4 w;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    if constexpr (DT == kBF16)
+      w[d] = __builtin_amdgcn_perm(rows[2 * d + 1][j >> 1], rows[2 * d][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
+    else
+      w[d] = rows[d][j];
+  }
+  return w;
+}
+
+// fp32 values as bf16 operands: the upper halves, and what they leave (0 beside
+// an infinity, whose rest would be NaN).
+__device__ __forceinline__ uint32_t pack_hi(float a, float b) {
+  return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
+}
+__device__ __forceinline__ float rest(float a) {
+  const float hi = bits_f32(__builtin_bit_cast(uint32_t, a) & 0xFFFF0000u);
+  return __builtin_fabsf(hi) == __builtin_inff() ? 0.0f : a - hi;
+}
+__device__ __forceinline__ uint32_t pack_lo(float a, float b) { return pack_bf16(rest(a), rest(b)); }
+
+// ---- rows by adapter -----------------------------------------------------------
+//
+// Tokens come in any order of adapters.  A wave looks at a window of 64 rows, one
+// a lane, and takes the adapters of the window one after the other: the lanes
+// that share the first remaining row's adapter are found by one ballot, and one
+// cross-lane move lines their rows up.  No sorted copy, no plan, no extra launch;
+// a window of one adapter (a long prompt) costs a single turn.
+
+constexpr int kWindow = 64;
+
+// Adapter of a row, -1 for none.
+__device__ __forceinline__ int row_adapter(const int32_t *ids, int64_t row, int adapters) {
+  const int id = ids ? ids[row] : 0;
+  return id >= 0 && id < adapters ? id : -1;
+}
+
+// Lane i gets the i-th lane of `match`; lanes from popcount(match) on the others.
+__device__ __forceinline__ int lined_up(uint64_t match, int lane) {
+  const uint64_t below = (1ull << lane) - 1;
+  const int at = (match >> lane) & 1 ? __popcll(match & below) : __popcll(match) + __popcll(~match & below);
+  return __builtin_amdgcn_ds_permute(at << 2, lane);
+}
+
+// ---- shrink ---------------------------------------------------------------------
+//
+// A wave's part of u for MT tiles of 16 rows and all ranks: blocks of four
+// fragments (256 bytes of a row) from `lo` on, `step` blocks apart.  Rows beyond
+// a tile's end repeat its first row and ranks beyond the last repeat it: their
+// results are not stored.  ACROSS: W is [K, rank] and read down its columns.
+template <int DT, int RT, int MT, bool ACROSS>
+__device__ __forceinline__ void shrink_part(f32x4 (&acc)[MT][RT], const uint8_t *const (&xrow)[MT], const uint8_t *w,
+                                            int64_t K, int rank, int64_t lo, int64_t hi, int step, int lane) {
+  using T = Tile<DT>;
+  constexpr int U = ACROSS && RT > 4 ? 1 : 4;  // fragments loaded at a time, as the registers allow
+  const int i = lane & 15, q = lane >> 4;
+  int wr[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) wr[r] = 16 * r + i < rank ? 16 * r + i : rank - 1;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[m][r] = f32x4{0, 0, 0, 0};
+  for (int64_t blk = lo; blk < hi; blk += step) {
+    const int64_t k0 = blk * (4 * T::KF) + T::PE * q;
+    if ((blk + 1) * (4 * T::KF) <= K) {
+#pragma unroll
+      for (int c0 = 0; c0 < 4; c0 += U) {
+        u32x4 xf[U][MT], wf[U][RT];
+#pragma unroll
+        for (int c = 0; c < U; ++c) {
+          const int64_t k = k0 + (c0 + c) * T::KF;
+#pragma unroll
+          for (int m = 0; m < MT; ++m) xf[c][m] = ld_frag(xrow[m] + k * T::ES);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            wf[c][r] = ACROSS ? ld_across<DT, true>(w, k, K, rank, wr[r]) : ld_frag(w + (wr[r] * K + k) * T::ES);
+        }
+#pragma unroll
+        for (int c = 0; c < U; ++c)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) acc[m][r] = mma<DT>(wf[c][r], xf[c][m], acc[m][r]);
+        if (U < 4) __builtin_amdgcn_sched_barrier(0);  // no loads of the next fragments above these
+      }
+    } else {  // the last block
+#pragma unroll 1
+      for (int64_t k = k0; k - T::PE * q < K; k += T::KF) {
+        u32x4 xf[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xf[m] = ld_frag_n<DT>(xrow[m] + k * T::ES, K - k);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const u32x4 wf =
+              ACROSS ? ld_across<DT, false>(w, k, K, rank, wr[r]) : ld_frag_n<DT>(w + (wr[r] * K + k) * T::ES, K - k);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[m][r] = mma<DT>(wf, xf[m], acc[m][r]);
+        }
+      }
+    }
+  }
+}
+
+// ---- expand ----------------------------------------------------------------------
+//
+// A wave takes 16 PE columns (128 bf16, 64 fp32) and keeps their weights in
+// registers while the rows of a window pass: u comes from the caches, base and y
+// pass once.  The tiles' columns are numbered such that a lane's results are four
+// pieces of PE consecutive columns, piece p at 16 PE / 4 p + PE q, and four lanes'
+// pieces are 64 consecutive bytes of a row.
+//   W [N, rank]: tile j, row i -> its column; PE / 4 tiles make a piece.
+//   W [rank, N] (ACROSS): a lane loads PE ranks of piece 4 (i % 4) + i / 4 and
+//   turns them; tile j has element j of every piece.
+// NF fragments of the ranks; NF 0: ranks up to 16 in bf16, whose hi and lo halves
+// share one fragment.
+
+template <int DT>
+constexpr int frag_count(int rank_tiles) {  // of 16-rank tiles
+  return DT == kBF16 ? rank_tiles / 2 : rank_tiles;
+}
+
+template <int DT, int NF, bool ACROSS>
+struct Expand {
+  using T = Tile<DT>;
+  static constexpr int F = NF ? NF : 1;
+  static constexpr int COLS = 16 * T::PE;
+  u32x4 w[F][T::PE];
+
+  // ranks that lane q of fragment f holds: PE from here on
+  __device__ __forceinline__ static int rank0(int f, int q) {
+    return NF ? f * T::KF + T::PE * q : T::PE * (q & 1);
+  }
+
+  // (Whole pieces are loaded without a branch: those past the last rank are dropped.)
+  __device__ __forceinline__ void load(const uint8_t *wp, int64_t N, int rank, int64_t n0, int lane) {
+    const int i = lane & 15, q = lane >> 4;
+    const u32x4 zero = {0, 0, 0, 0};
+    if constexpr (ACROSS) {
+      const int64_t col = n0 + T::PE * (4 * (i & 3) + (i >> 2));
+      const bool inside = n0 + COLS <= N;
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int r0 = rank0(f, q);
+        u32x4 rows[T::PE];
+        if (inside) {
+#pragma unroll
+          for (int e = 0; e < T::PE; ++e) {
+            const int r = r0 + e < rank ? r0 + e : rank - 1;
+            const u32x4 v = ld_frag(wp + (r * N + col) * T::ES);
+            rows[e] = r0 + e < rank ? v : zero;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < T::PE; ++e) {
+            rows[e] = zero;
+            if (r0 + e < rank) rows[e] = ld_frag_n<DT>(wp + ((r0 + e) * N + col) * T::ES, N - col);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < T::PE; ++j) w[f][j] = turned<DT>(rows, j);
+      }
+    } else {
+      constexpr int TP = T::PE / 4;  // tiles a piece
+      const bool whole = rank % T::PE == 0;
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int r0 = rank0(f, q);
+#pragma unroll
+        for (int j = 0; j < T::PE; ++j) {
+          const int64_t col = n0 + 4 * T::PE * (j / TP) + T::PE * (i >> 2) + 4 * (j % TP) + (i & 3);
+          const uint8_t *row = wp + (col < N ? col : N - 1) * rank * T::ES;
+          if (whole) {
+            const u32x4 v = ld_frag(row + (r0 < rank ? r0 : 0) * T::ES);
+            w[f][j] = r0 < rank ? v : zero;
+          } else {
+            w[f][j] = ld_frag_n<DT>(row + r0 * T::ES, rank - r0);
+          }
+        }
+      }
+    }
+  }
+
+  // Column of piece p, from n0.
+  __device__ __forceinline__ static int piece(int p, int q) { return 4 * T::PE * p + T::PE * q; }
+
+  // acc: the PE tiles' results; element e of piece p.
+  __device__ __forceinline__ static float at(const f32x4 (&acc)[T::PE], int p, int e) {
+    constexpr int TP = T::PE / 4;
+    return ACROSS ? acc[e][p] : acc[TP * p + (e >> 2)][e & 3];
+  }
+
+  // uf: hi fragments, then lo ones (bf16); the fragments of u (fp32)
+  static constexpr int UF = DT == kBF16 && NF ? 2 * F : F;
+  __device__ __forceinline__ void product(f32x4 (&acc)[T::PE], const u32x4 (&uf)[UF]) const {
+#pragma unroll
+    for (int j = 0; j < T::PE; ++j) {
+      acc[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int f = 0; f < UF; ++f) acc[j] = mma<DT>(w[f % F][j], uf[f], acc[j]);
+    }
+  }
+
+  // Fragments of one row's u, given get(r, n): PE fp32 values from rank r on, those
+  // from n on 0.
+  template <typename G>
+  __device__ __forceinline__ static void u_frags(u32x4 (&uf)[UF], int rank, int q, G get) {
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int r0 = rank0(f, q);
+      float v[T::PE];
+      get(v, r0, rank - r0);
+      if constexpr (DT == kF32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) uf[f][e] = __builtin_bit_cast(uint32_t, v[e]);
+      } else {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          hi[d] = pack_hi(v[2 * d], v[2 * d + 1]);
+          lo[d] = pack_lo(v[2 * d], v[2 * d + 1]);
+        }
+        if constexpr (NF == 0) {
+          uf[0] = q < 2 ? hi : lo;
+        } else {
+          uf[f] = hi;
+          uf[F + f] = lo;
+        }
+      }
+    }
+  }
+};
+
+// base + the products, rounded once.
+template <int DT>
+__device__ __forceinline__ u32x4 add_base(u32x4 base, const float (&f)[Tile<DT>::PE]) {
+  u32x4 w;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    if constexpr (DT == kBF16)
+      w[d] = pack_bf16(bits_f32(base[d] << 16) + f[2 * d], bits_f32(base[d] & 0xFFFF0000u) + f[2 * d + 1]);
+    else
+      w[d] = __builtin_bit_cast(uint32_t, bits_f32(base[d]) + f[d]);
+  }
+  return w;
+}
+
+}  // namespace mxfp4

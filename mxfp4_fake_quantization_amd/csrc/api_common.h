@@ -93,6 +93,27 @@ inline bool distinct(std::initializer_list<const void *> ps) {
   return true;
 }
 
+inline mxfp4_status_t check_dtype(int32_t dtype) {
+  if (dtype != MXFP4_BF16 && dtype != MXFP4_F32)
+    return fail(MXFP4_EUNSUPPORTED, "dtype %d is not MXFP4_BF16 or MXFP4_F32", dtype);
+  return MXFP4_OK;
+}
+
+// Outputs apart from each other and from every input (NULL entries are
+// skipped); inputs may share memory.
+inline bool apart(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
+  if (!distinct(outs)) return false;
+  for (const void *o : outs)
+    for (const void *i : ins)
+      if (o && o == i) return false;
+  return true;
+}
+
+// Pointers of elements: aligned to one element.
+inline mxfp4_status_t check_elems(const void *p, int32_t dtype, const char *what) {
+  return check_ptr(p, dtype == MXFP4_F32 ? 4 : 2, what);
+}
+
 // One operand of the grouped products.
 inline mxfp4_status_t check_operand(const mxfp4_mx_operand_t *o, const char *what, bool rows_split, int64_t K,
                              int64_t k_blocks, bool is_a) {

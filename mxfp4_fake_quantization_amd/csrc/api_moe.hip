@@ -11,27 +11,6 @@ using namespace mxfp4_api;
 
 namespace {
 
-mxfp4_status_t check_dtype(int32_t dtype) {
-  if (dtype != MXFP4_BF16 && dtype != MXFP4_F32)
-    return fail(MXFP4_EUNSUPPORTED, "dtype %d is not MXFP4_BF16 or MXFP4_F32", dtype);
-  return MXFP4_OK;
-}
-
-// Outputs apart from each other and from every input (NULL entries are
-// skipped); inputs may share memory.
-bool apart(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
-  if (!distinct(outs)) return false;
-  for (const void *o : outs)
-    for (const void *i : ins)
-      if (o && o == i) return false;
-  return true;
-}
-
-// Pointers of elements: aligned to one element.
-mxfp4_status_t check_elems(const void *p, int32_t dtype, const char *what) {
-  return check_ptr(p, dtype == MXFP4_F32 ? 4 : 2, what);
-}
-
 mxfp4_status_t check_act(int32_t act) {
   if ((act < MXACT_NONE || act > MXACT_GELU) && act != MXACT_SWIGLU && act != MXACT_GEGLU)
     return fail(MXFP4_EUNSUPPORTED, "act %d is not one of the MXACT_ activations", act);
