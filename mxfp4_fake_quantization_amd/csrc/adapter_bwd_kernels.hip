@@ -183,6 +183,12 @@ __global__ __launch_bounds__(kSumThreads) void adapter_grad_sum_kernel(GradSumAr
     }
 }
 
+// du from its parts, as the kernel of grad_x adds them where that is wanted too.
+__global__ __launch_bounds__(256) void adapter_parts_kernel(const float *parts, float *du, int64_t part, int splits) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e < part) du[e] = parts_sum(parts + e, part, splits);
+}
+
 // ---- host ------------------------------------------------------------------------------
 
 // Rows of a piece: about 1024 workgroups over the columns of both gradients.
@@ -193,7 +199,7 @@ int piece_rows(int64_t tokens, int64_t in, int64_t out) {
 }
 
 struct BwdSpace {  // offsets of the workspace's parts, 16-byte aligned
-  int64_t du, order, first, pieces, part_a, part_b, total;
+  int64_t du, parts, order, first, pieces, part_a, part_b, total;
   int64_t most;    // pieces
   int rows;
 };
@@ -208,6 +214,8 @@ BwdSpace bwd_space(int64_t tokens, int64_t in, int64_t out, int rank, int adapte
   S.rows = piece_rows(tokens, in, out);
   S.most = tokens / S.rows + (adapters < tokens ? adapters : tokens);
   S.du = take(4 * tokens * rank);
+  const int splits = shrink_splits(tokens, out);
+  S.parts = take(splits > 1 ? 4 * tokens * rank * splits : 0);
   const bool any = grad_a || grad_b;
   S.order = take(any ? 4 * tokens : 0);
   S.first = take(any ? 4 * (int64_t)(adapters + 1) : 0);
@@ -271,14 +279,23 @@ hipError_t launch_adapter_bwd(const AdapterBwdLaunch &L, hipStream_t stream) {
     while ((1 << P.bits) < L.adapters) ++P.bits;
   }
   const int64_t part = L.tokens * L.rank;
-  ShrinkArgs D{static_cast<const uint8_t *>(L.grad_y), static_cast<const uint8_t *>(L.b), L.ids, L.scale, du, L.tokens,
-               L.ld_gy, L.out, part, L.adapters, L.rank, 1};
+  const int splits = shrink_splits(L.tokens, L.out);
+  float *parts = splits > 1 ? reinterpret_cast<float *>(ws + S.parts) : du;
+  ShrinkArgs D{static_cast<const uint8_t *>(L.grad_y), static_cast<const uint8_t *>(L.b), L.ids, L.scale, parts, L.tokens,
+               L.ld_gy, L.out, part, L.adapters, L.rank, splits, shrink_slots(L.tokens, L.adapters, splits),
+               L.grad_x || L.grad_a ? window_count(L.tokens) : 0};
   hipError_t e = launch_shrink<true>(L.dtype, D, P, stream);
   if (e != hipSuccess) return e;
   if (L.grad_x && L.tokens > 0) {
-    ExpandArgs X{du, static_cast<const uint8_t *>(L.a), L.ids, nullptr, static_cast<const uint8_t *>(L.base),
-                 static_cast<uint8_t *>(L.grad_x), nullptr, L.tokens, L.in, L.ld_base, L.ld_gx, part, L.adapters, L.rank, 1};
+    ExpandArgs X{parts, static_cast<const uint8_t *>(L.a), L.ids, nullptr, static_cast<const uint8_t *>(L.base),
+                 static_cast<uint8_t *>(L.grad_x), splits > 1 && L.grad_a ? du : nullptr, L.tokens, L.in, L.ld_base,
+                 L.ld_gx, part, L.adapters, L.rank, splits};
     e = launch_expand<true>(L.dtype, X, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (L.grad_a && !L.grad_x && splits > 1 && part > 0) {
+    adapter_parts_kernel<<<(unsigned)((part + 255) / 256), 256, 0, stream>>>(parts, du, part, splits);
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (!L.grad_a && !L.grad_b) return hipSuccess;

@@ -78,23 +78,6 @@ __device__ __forceinline__ void st_frag_n(uint8_t *p, u32x4 w, int64_t n) {
     }
 }
 
-// A fragment's lane across rows: elements (k0 + e, col), e < PE, of a matrix with
-// `ld` elements a row; without WHOLE, rows from `rows` on read as 0.  (col is
-// inside the row.)
-template <int DT, bool WHOLE>
-__device__ __forceinline__ u32x4 ld_across(const uint8_t *p, int64_t k0, int64_t rows, int64_t ld, int64_t col) {
-  u32x4 w = {0, 0, 0, 0};
-  const int64_t at = k0 * ld + col;
-#pragma unroll
-  for (int e = 0; e < Tile<DT>::PE; ++e) {
-    if (WHOLE || k0 + e < rows) {
-      if (DT == kBF16) w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[at + e * ld] << (16 * (e & 1));
-      else w[e & 3] = reinterpret_cast<const uint32_t *>(p)[at + e * ld];
-    }
-  }
-  return w;
-}
-
 // PE rows of PE elements a lane become PE fragments' lanes: fragment j holds
 // element j of every row.
 template <int DT>
@@ -144,76 +127,14 @@ __device__ __forceinline__ int lined_up(uint64_t match, int lane) {
   return __builtin_amdgcn_ds_permute(at << 2, lane);
 }
 
-// ---- shrink ---------------------------------------------------------------------
-//
-// A wave's part of u for MT tiles of 16 rows and all ranks: blocks of four
-// fragments (256 bytes of a row) from `lo` on, `step` blocks apart.  Rows beyond
-// a tile's end repeat its first row and ranks beyond the last repeat it: their
-// results are not stored.  ACROSS: W is [K, rank] and read down its columns.
-template <int DT, int RT, int MT, bool ACROSS>
-__device__ __forceinline__ void shrink_part(f32x4 (&acc)[MT][RT], const uint8_t *const (&xrow)[MT], const uint8_t *w,
-                                            int64_t K, int rank, int64_t lo, int64_t hi, int step, int lane) {
-  using T = Tile<DT>;
-  constexpr int U = ACROSS && RT > 4 ? 1 : 4;  // fragments loaded at a time, as the registers allow
-  const int i = lane & 15, q = lane >> 4;
-  int wr[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) wr[r] = 16 * r + i < rank ? 16 * r + i : rank - 1;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) acc[m][r] = f32x4{0, 0, 0, 0};
-  for (int64_t blk = lo; blk < hi; blk += step) {
-    const int64_t k0 = blk * (4 * T::KF) + T::PE * q;
-    if ((blk + 1) * (4 * T::KF) <= K) {
-#pragma unroll
-      for (int c0 = 0; c0 < 4; c0 += U) {
-        u32x4 xf[U][MT], wf[U][RT];
-#pragma unroll
-        for (int c = 0; c < U; ++c) {
-          const int64_t k = k0 + (c0 + c) * T::KF;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) xf[c][m] = ld_frag(xrow[m] + k * T::ES);
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-            wf[c][r] = ACROSS ? ld_across<DT, true>(w, k, K, rank, wr[r]) : ld_frag(w + (wr[r] * K + k) * T::ES);
-        }
-#pragma unroll
-        for (int c = 0; c < U; ++c)
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) acc[m][r] = mma<DT>(wf[c][r], xf[c][m], acc[m][r]);
-        if (U < 4) __builtin_amdgcn_sched_barrier(0);  // no loads of the next fragments above these
-      }
-    } else {  // the last block
-#pragma unroll 1
-      for (int64_t k = k0; k - T::PE * q < K; k += T::KF) {
-        u32x4 xf[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) xf[m] = ld_frag_n<DT>(xrow[m] + k * T::ES, K - k);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const u32x4 wf =
-              ACROSS ? ld_across<DT, false>(w, k, K, rank, wr[r]) : ld_frag_n<DT>(w + (wr[r] * K + k) * T::ES, K - k);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) acc[m][r] = mma<DT>(wf, xf[m], acc[m][r]);
-        }
-      }
-    }
-  }
-}
-
 // ---- expand ----------------------------------------------------------------------
 //
 // A wave takes 16 PE columns (128 bf16, 64 fp32) and keeps their weights in
-// registers while the rows of a window pass: u comes from the caches, base and y
-// pass once.  The tiles' columns are numbered such that a lane's results are four
-// pieces of PE consecutive columns, piece p at 16 PE / 4 p + PE q, and four lanes'
-// pieces are 64 consecutive bytes of a row.
-//   W [N, rank]: tile j, row i -> its column; PE / 4 tiles make a piece.
-//   W [rank, N] (ACROSS): a lane loads PE ranks of piece 4 (i % 4) + i / 4 and
-//   turns them; tile j has element j of every piece.
+// registers while rows pass: u comes from the caches, base and y pass once.  Column
+// PE n + j is row n of tile j, so a lane's results over the tiles are PE consecutive
+// columns of a row, 16 bytes, and 16 lanes' are 256 consecutive bytes of it.
+//   W [N, rank]: lane n loads the ranks of its PE columns.
+//   W [rank, N] (ACROSS): a lane loads its PE columns of PE ranks and turns them.
 // NF fragments of the ranks; NF 0: ranks up to 16 in bf16, whose hi and lo halves
 // share one fragment.
 
@@ -239,7 +160,7 @@ struct Expand {
     const int i = lane & 15, q = lane >> 4;
     const u32x4 zero = {0, 0, 0, 0};
     if constexpr (ACROSS) {
-      const int64_t col = n0 + T::PE * (4 * (i & 3) + (i >> 2));
+      const int64_t col = n0 + T::PE * i;
       const bool inside = n0 + COLS <= N;
 #pragma unroll
       for (int f = 0; f < F; ++f) {
@@ -263,14 +184,13 @@ struct Expand {
         for (int j = 0; j < T::PE; ++j) w[f][j] = turned<DT>(rows, j);
       }
     } else {
-      constexpr int TP = T::PE / 4;  // tiles a piece
       const bool whole = rank % T::PE == 0;
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const int r0 = rank0(f, q);
 #pragma unroll
         for (int j = 0; j < T::PE; ++j) {
-          const int64_t col = n0 + 4 * T::PE * (j / TP) + T::PE * (i >> 2) + 4 * (j % TP) + (i & 3);
+          const int64_t col = n0 + T::PE * i + j;
           const uint8_t *row = wp + (col < N ? col : N - 1) * rank * T::ES;
           if (whole) {
             const u32x4 v = ld_frag(row + (r0 < rank ? r0 : 0) * T::ES);
@@ -283,23 +203,15 @@ struct Expand {
     }
   }
 
-  // Column of piece p, from n0.
-  __device__ __forceinline__ static int piece(int p, int q) { return 4 * T::PE * p + T::PE * q; }
-
-  // acc: the PE tiles' results; element e of piece p.
-  __device__ __forceinline__ static float at(const f32x4 (&acc)[T::PE], int p, int e) {
-    constexpr int TP = T::PE / 4;
-    return ACROSS ? acc[e][p] : acc[TP * p + (e >> 2)][e & 3];
-  }
-
   // uf: hi fragments, then lo ones (bf16); the fragments of u (fp32)
   static constexpr int UF = DT == kBF16 && NF ? 2 * F : F;
-  __device__ __forceinline__ void product(f32x4 (&acc)[T::PE], const u32x4 (&uf)[UF]) const {
+  // acc[j][v]: row 4 q + v of the tile, column n0 + PE n + h + j
+  __device__ __forceinline__ void product(f32x4 (&acc)[4], const u32x4 (&uf)[UF], int h) const {
 #pragma unroll
-    for (int j = 0; j < T::PE; ++j) {
+    for (int j = 0; j < 4; ++j) {
       acc[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int f = 0; f < UF; ++f) acc[j] = mma<DT>(w[f % F][j], uf[f], acc[j]);
+      for (int f = 0; f < UF; ++f) acc[j] = mma<DT>(uf[f], w[f % F][h + j], acc[j]);
     }
   }
 
@@ -333,18 +245,19 @@ struct Expand {
   }
 };
 
-// base + the products, rounded once.
+// Columns h to h + 3 of a lane's piece: base + the products of row v, rounded once.
 template <int DT>
-__device__ __forceinline__ u32x4 add_base(u32x4 base, const float (&f)[Tile<DT>::PE]) {
-  u32x4 w;
+__device__ __forceinline__ void add_products(u32x4 &piece, const f32x4 (&acc)[4], int h, int v) {
+  if constexpr (DT == kBF16) {
 #pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    if constexpr (DT == kBF16)
-      w[d] = pack_bf16(bits_f32(base[d] << 16) + f[2 * d], bits_f32(base[d] & 0xFFFF0000u) + f[2 * d + 1]);
-    else
-      w[d] = __builtin_bit_cast(uint32_t, bits_f32(base[d]) + f[d]);
+    for (int d = 0; d < 2; ++d) {
+      const uint32_t b = piece[h / 2 + d];
+      piece[h / 2 + d] = pack_bf16(bits_f32(b << 16) + acc[2 * d][v], bits_f32(b & 0xFFFF0000u) + acc[2 * d + 1][v]);
+    }
+  } else {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) piece[d] = __builtin_bit_cast(uint32_t, bits_f32(piece[d]) + acc[d][v]);
   }
-  return w;
 }
 
 }  // namespace mxfp4

@@ -13,7 +13,8 @@ hipError_t launch_adapter(const AdapterLaunch &L, hipStream_t stream) {
   float *u = splits == 1 && keep ? L.u : L.workspace;
   const int64_t part = L.tokens * L.rank;
   ShrinkArgs S{static_cast<const uint8_t *>(L.x), static_cast<const uint8_t *>(L.a), L.ids, nullptr, u, L.tokens, L.ldx,
-               L.in, part, L.adapters, L.rank, splits};
+               L.in, part, L.adapters, L.rank, splits, shrink_slots(L.tokens, L.adapters, splits),
+               window_count(L.tokens)};
   hipError_t e = launch_shrink<false>(L.dtype, S, PlanArgs{}, stream);
   if (e != hipSuccess) return e;
   ExpandArgs E{u, static_cast<const uint8_t *>(L.b), L.ids, L.scale, static_cast<const uint8_t *>(L.base),

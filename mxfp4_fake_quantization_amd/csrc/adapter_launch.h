@@ -5,6 +5,8 @@
 
 #include "adapter_device.h"
 
+#include <type_traits>
+
 namespace mxfp4 {
 namespace {
 
@@ -14,7 +16,8 @@ struct ShrinkArgs {
   const float *scale;  // of each adapter, or NULL
   float *u;            // [splits][tokens, rank]
   int64_t tokens, ldx, K, part;
-  int adapters, rank, splits;
+  int adapters, rank, splits, slots;
+  int windows;         // 0: only the plan is wanted
 };
 
 struct ExpandArgs {
@@ -51,9 +54,23 @@ __device__ void plan_rows(const PlanArgs &P, const int32_t *ids, int64_t tokens,
   const int64_t part = (tokens + 64 * WAVES - 1) / (64 * WAVES) * 64;
   const int64_t lo = wave * part, hi = lo + part < tokens ? lo + part : tokens;
   int32_t *mine = cnt + wave * adapters;
-  for (int64_t i = lo + lane; i < hi; i += 64) {
-    const int id = row_adapter(ids, i, adapters);
-    if (id >= 0) atomicAdd(&mine[id], 1);  // a count: the order of the additions does not matter
+  // (8 steps' ids are loaded at once: one at a time, a wave waits for memory at every step
+  // and 16384 tokens took 44 us, longer than the products beside it)
+  constexpr int AHEAD = 8;
+  auto load_ids = [&](int64_t base, int(&id)[AHEAD]) {
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s) {
+      const int64_t i = base + 64 * s + lane;
+      const int v = ids ? ids[i < hi ? i : hi - 1] : 0;
+      id[s] = i < hi && v >= 0 && v < adapters ? v : -1;
+    }
+  };
+  for (int64_t base = lo; base < hi; base += 64 * AHEAD) {
+    int id[AHEAD];
+    load_ids(base, id);
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s)
+      if (id[s] >= 0) atomicAdd(&mine[id[s]], 1);  // a count: the order of the additions does not matter
   }
   __syncthreads();
   if (wave == 0) {  // first places and pieces, 64 adapters at a time
@@ -93,104 +110,231 @@ __device__ void plan_rows(const PlanArgs &P, const int32_t *ids, int64_t tokens,
   }
   __syncthreads();
   // Every lane of a wave takes part in the ballots: the loop count is the wave's.
-  for (int64_t base = lo; base < hi; base += 64) {
-    const int64_t i = base + lane;
-    const int id = i < hi ? row_adapter(ids, i, adapters) : -1;
-    uint64_t same = __ballot(id >= 0);
-    for (int b = 0; b < P.bits; ++b) {
-      const uint64_t on = __ballot((id >> b) & 1);
-      same &= (id >> b) & 1 ? on : ~on;
+  for (int64_t base = lo; base < hi; base += 64 * AHEAD) {
+    int id[AHEAD];
+    load_ids(base, id);
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s) {
+      uint64_t same = __ballot(id[s] >= 0);
+      for (int b = 0; b < P.bits; ++b) {
+        const uint64_t on = __ballot((id[s] >> b) & 1);
+        same &= (id[s] >> b) & 1 ? on : ~on;
+      }
+      if (id[s] >= 0) {
+        const int32_t at = mine[id[s]];
+        P.order[at + __popcll(same & ((1ull << lane) - 1))] = (int32_t)(base + 64 * s + lane);
+        // the group's last lane moves the count on (a wave's LDS operations keep
+        // their order: the reads above come first)
+        if ((same >> lane) == 1ull) mine[id[s]] = at + (int32_t)__popcll(same);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
-    if (id >= 0) {
-      const int32_t at = mine[id];
-      P.order[at + __popcll(same & ((1ull << lane) - 1))] = (int32_t)i;
-      // the group's last lane moves the count on (a wave's LDS operations keep
-      // their order: the reads above come first)
-      if ((same >> lane) == 1ull) mine[id] = at + (int32_t)__popcll(same);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
   }
+}
+
+// Workgroup id -> place in [0, total) such that each of the 8 XCDs (workgroups go to
+// them in turn) has a run of consecutive places: neighbouring windows mostly hold one
+// adapter, whose weights then stay in that XCD's L2.
+__device__ __forceinline__ int64_t xcd_share(int64_t id, int64_t total) {
+  const int64_t q = total >> 3, r = total & 7, x = id & 7;
+  return x * q + (x < r ? x : r) + (id >> 3);
 }
 
 // ---- shrink ----------------------------------------------------------------------
 //
-// A workgroup takes tiles of 16 MT rows of one adapter in a window; its eight
-// waves share out the blocks of the long dimension and add their parts in LDS, in
-// the order of the waves.
+// A workgroup takes the rows of one adapter in a window of 64, wave w the w-th 16 of
+// them, over a part of the long dimension.  256 bytes of every row and of every
+// rank's weights at a time go through LDS (two buffers, the next block's loads in
+// flight during a block's products): global reads are 256 consecutive bytes of a
+// row, and the weights are read once for all four waves.  Piece p of LDS row r lies
+// at p ^ (r % 16), which spreads a fragment's 16 rows over all banks.
+//
+// Windows of several adapters: workgroup `slot` of a window takes every slots-th of
+// its adapters.
 
-constexpr int kShrinkWaves = 8;
+constexpr int kShrinkWaves = 4, kShrinkThreads = 64 * kShrinkWaves;
+constexpr int kBlockBytes = 256, kPieces = kBlockBytes / 16;
 
-template <int DT, int RT, int MT, bool ACROSS>
-__global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(ShrinkArgs A, PlanArgs P) {
+__device__ __forceinline__ int piece_at(int row, int piece) { return row * kPieces + (piece ^ (row & 15)); }
+
+template <int DT, int RT, bool ACROSS>
+__global__ __launch_bounds__(kShrinkThreads) void adapter_shrink_kernel(ShrinkArgs A, PlanArgs P) {
   using T = Tile<DT>;
-  __shared__ f32x4 part[kShrinkWaves][MT * RT][64];
-  int block = blockIdx.x;
+  constexpr int BK = kBlockBytes / T::ES;        // elements of a block
+  constexpr int XP = kWindow * kPieces / kShrinkThreads;  // pieces of x a thread stages
+  // pieces of W: of its rows, or (ACROSS) squares of PE x PE elements, PE pieces each
+  constexpr int WT = ACROSS ? kPieces * (16 * RT / T::PE) : 16 * RT * kPieces;
+  constexpr int WP = (WT + kShrinkThreads - 1) / kShrinkThreads, WN = ACROSS ? T::PE : 1;
+  __shared__ u32x4 xs[2][kWindow * kPieces];
+  __shared__ u32x4 ws[2][16 * RT * kPieces];
+  int64_t block = blockIdx.x;
   if constexpr (ACROSS) {  // the backward pass
-    if (P.order && --block < 0) {
-      __shared__ int32_t cnt[kShrinkWaves * kAdapterMaxTrained];
-      plan_rows<kShrinkWaves>(P, A.ids, A.tokens, A.adapters, cnt);
-      return;
+    if (P.order) {
+      static_assert(sizeof xs >= sizeof(int32_t) * kShrinkWaves * kAdapterMaxTrained, "the plan's counts");
+      if (block == 0) plan_rows<kShrinkWaves>(P, A.ids, A.tokens, A.adapters, reinterpret_cast<int32_t *>(xs));
+      block -= 8;  // (the others keep their XCDs)
+      if (block < 0) return;
     }
   }
-  constexpr int SLOTS = kWindow / (16 * MT);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-  const int64_t row0 = (int64_t)(block / SLOTS) * kWindow;
-  const int slot = block % SLOTS;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, q = lane >> 4;
+  // (window, part) pairs, in the outer order of the slots: those of windows with one
+  // adapter have nothing to do
+  const int64_t pairs = (int64_t)A.windows * A.splits;
+  const int slot = (int)(block / ((pairs + 7) / 8 * 8));
+  block -= slot * ((pairs + 7) / 8 * 8);
+  if (block >= pairs) return;
+  const int64_t pair = xcd_share(block, pairs);
+  const int split = (int)(pair % A.splits);
+  const int64_t row0 = pair / A.splits * kWindow;
   const bool live = row0 + lane < A.tokens;
   const int id = live ? row_adapter(A.ids, row0 + lane, A.adapters) : -1;
-  float *u = A.u + (int64_t)blockIdx.y * A.part;
-  const int64_t blocks = (A.K + 4 * T::KF - 1) / (4 * T::KF);
-  const int64_t lo = blocks * blockIdx.y / A.splits, hi = blocks * (blockIdx.y + 1) / A.splits;
+  float *u = A.u + split * A.part;
+  const int64_t blocks = (A.K + BK - 1) / BK;
+  const int64_t lo = blocks * split / A.splits, hi = blocks * (split + 1) / A.splits;
   // rows without an adapter: u = 0
   if (slot == 0 && wave == 0 && live && id < 0)
     for (int r = 0; r < A.rank; ++r) u[(row0 + lane) * A.rank + r] = 0.0f;
   int seen = 0;
-  for (uint64_t rem = __ballot(id >= 0); rem;) {
+  for (uint64_t rem = __ballot(id >= 0); rem; ++seen) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(rem));
     const uint64_t match = __ballot(id == a);
     rem &= ~match;
-    const int n = __popcll(match), tiles = (n + 16 * MT - 1) / (16 * MT);
+    if (seen % A.slots != slot) continue;
+    const int n = __popcll(match);
     const int line = lined_up(match, lane);
     const uint8_t *w = A.w + (int64_t)a * A.rank * A.K * T::ES;
-    // this workgroup's tiles of the window's: slot, slot + SLOTS, ...
-    for (int j = (slot - seen % SLOTS + SLOTS) % SLOTS; j < tiles; j += SLOTS) {
-      const uint8_t *xrow[MT];
-      int row[MT];
+    // the thread's rows of x: tid / 16 and every 16th from there (rows past the last repeat it)
+    const uint8_t *xrow[XP];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int at = 16 * (j * MT + m) + i;
-        const int to = __builtin_amdgcn_ds_bpermute(at << 2, line);  // (every lane takes part)
-        row[m] = at < n ? to : -1;
+    for (int j = 0; j < XP; ++j) {
+      const int r = tid / kPieces + j * (kShrinkThreads / kPieces);
+      const int to = __builtin_amdgcn_ds_bpermute((r < n ? r : n - 1) << 2, line);
+      xrow[j] = A.x + ((row0 + to) * A.ldx + T::PE * (tid % kPieces)) * T::ES;
+    }
+    struct Stage {
+      u32x4 x[XP], w[WP][WN];
+    };
+    Stage s0, s1;  // blocks on their way
+    // Block blk; WHOLE: it lies inside the rows, and no load hangs on a condition (the
+    // compiler then waits for the loads it needs, not for all that are under way).
+    auto load = [&](Stage &S, int64_t blk, auto whole) {
+      constexpr bool WHOLE = decltype(whole)::value;
+      const int64_t k0 = blk * BK;
+#pragma unroll
+      for (int j = 0; j < XP; ++j) {
+        const uint8_t *p = xrow[j] + k0 * T::ES;
+        S.x[j] = WHOLE ? ld_frag(p) : ld_frag_n<DT>(p, A.K - k0 - T::PE * (tid % kPieces));
       }
-      const int first = __builtin_amdgcn_readfirstlane(row[0]);  // at 16 j MT < n
 #pragma unroll
-      for (int m = 0; m < MT; ++m) xrow[m] = A.x + (row0 + (row[m] < 0 ? first : row[m])) * A.ldx * T::ES;
-      f32x4 acc[MT][RT];
-      shrink_part<DT, RT, MT, ACROSS>(acc, xrow, w, A.K, A.rank, lo + wave, hi, kShrinkWaves, lane);
-      __syncthreads();  // the tile before has been read
+      for (int j = 0; j < WP; ++j) {
+        const int e = tid + j * kShrinkThreads;
+        if constexpr (ACROSS) {  // PE rows k of PE ranks (threads past the last square repeat it)
+          const int t = WT % kShrinkThreads == 0 || e < WT ? e : WT - 1;
+          const int64_t k = k0 + T::PE * (t % kPieces);
+          const int r = T::PE * (t / kPieces);
+          const uint8_t *p = w + (k * A.rank + r) * T::ES;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+          for (int v = 0; v < WN; ++v) {
+            if constexpr (WHOLE) {
+              S.w[j][v] = ld_frag(r < A.rank ? p + v * A.rank * T::ES : w);
+            } else {
+              S.w[j][v] = u32x4{0, 0, 0, 0};
+              if (k + v < A.K && r < A.rank) S.w[j][v] = ld_frag_n<DT>(p + v * A.rank * T::ES, A.rank - r);
+            }
+          }
+        } else {
+          const int r = e / kPieces;  // (WT is a multiple of the threads)
+          const int64_t k = k0 + T::PE * (e % kPieces);
+          const uint8_t *p = w + ((r < A.rank ? r : A.rank - 1) * A.K + k) * T::ES;
+          S.w[j][0] = WHOLE ? ld_frag(p) : ld_frag_n<DT>(p, A.K - k);
+        }
+      }
+    };
+    auto store = [&](const Stage &S, int buf) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) part[wave][m * RT + r][lane] = acc[m][r];
+      for (int j = 0; j < XP; ++j)
+        xs[buf][piece_at(tid / kPieces + j * (kShrinkThreads / kPieces), tid % kPieces)] = S.x[j];
+#pragma unroll
+      for (int j = 0; j < WP; ++j) {
+        const int e = tid + j * kShrinkThreads;
+        if constexpr (ACROSS) {
+          if (WT % kShrinkThreads == 0 || e < WT)
+#pragma unroll
+            for (int v = 0; v < WN; ++v)
+              ws[buf][piece_at(T::PE * (e / kPieces) + v, e % kPieces)] = turned<DT>(S.w[j], v);
+        } else {
+          ws[buf][piece_at(e / kPieces, e % kPieces)] = S.w[j][0];
+        }
+      }
+    };
+    f32x4 acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
+    auto compute = [&](int buf) {
+      if (16 * wave >= n) return;
+#pragma unroll
+      for (int c = 0; c < kPieces / 4; ++c) {
+        const u32x4 xf = xs[buf][piece_at(16 * wave + i, 4 * c + q)];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r] = mma<DT>(ws[buf][piece_at(16 * r + i, 4 * c + q)], xf, acc[r]);
+      }
+    };
+    __syncthreads();  // the adapter before has been read
+    // Two blocks' loads are under way while one is computed.  Workgroups start at
+    // different blocks: rows a power of two apart would all ask the same few memory
+    // channels at a time otherwise.
+    using Yes = std::integral_constant<bool, true>;
+    using No = std::integral_constant<bool, false>;
+    // ranks that are no whole pieces: the squares of W are guarded, block by block
+    const bool squares = !ACROSS || A.rank % T::PE == 0;
+    const int64_t full = !squares ? lo : hi * BK <= A.K ? hi : hi - 1;
+    const int64_t count = full - lo;
+    if (count > 0) {
+      int64_t next = lo + (pair / A.splits * 5) % count;
+      auto following = [&]() {
+        const int64_t here = next;
+        if (++next == full) next = lo;
+        return here;
+      };
+      load(s0, following(), Yes());
+      load(s1, following(), Yes());
+      store(s0, 0);
       __syncthreads();
-      const float s = A.scale ? A.scale[a] : 1.0f;
-      for (int e = wave; e < MT * RT; e += kShrinkWaves) {
-        f32x4 sum = part[0][e][lane];
-#pragma unroll
-        for (int v = 1; v < kShrinkWaves; ++v) sum += part[v][e][lane];
-        const int at = 16 * (j * MT + e / RT) + i;
-        const int to = __builtin_amdgcn_ds_bpermute(at << 2, line);
-        const int r0 = 16 * (e % RT) + 4 * q;
-        if (at < n) {
-          float *p = u + (row0 + to) * A.rank + r0;
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (r0 + v < A.rank) p[v] = s * sum[v];
+      // (blocks past the last are loaded again and not used)
+      for (int64_t b = 0; b < count; b += 2) {
+        load(s0, following(), Yes());
+        compute(0);
+        store(s1, 1);
+        __syncthreads();
+        if (b + 1 < count) {
+          load(s1, following(), Yes());
+          compute(1);
+          store(s0, 0);
+          __syncthreads();
         }
       }
     }
-    seen += tiles;
+    for (int64_t blk = full; blk < hi; ++blk) {
+      load(s0, blk, No());
+      __syncthreads();
+      store(s0, 0);
+      __syncthreads();
+      compute(0);
+    }
+    const float s = A.scale ? A.scale[a] : 1.0f;
+    const int at = 16 * wave + i;
+    const int to = __builtin_amdgcn_ds_bpermute(at << 2, line);  // (every lane takes part)
+    if (at < n) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int r0 = 16 * r + 4 * q;
+        float *p = u + (row0 + to) * A.rank + r0;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (r0 + v < A.rank) p[v] = s * acc[r][v];
+      }
+    }
   }
 }
 
@@ -198,113 +342,184 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void adapter_shrink_kernel(Shrin
 
 constexpr int kExpandWaves = 4;
 
+__device__ __forceinline__ float parts_sum(const float *u, int64_t part, int splits) {
+  float s = u[0];
+  for (int k = 1; k < splits; ++k) s += u[k * part];
+  return s;
+}
+
+// A workgroup takes 64 rows by 4 waves of columns.  Everything that does not hang on
+// the rows' adapters is under way before those are known: the base of all rows
+// (the wave's 16 KB) and u, of which wave w makes the fragments of rows 16 w to 16 w +
+// 15 for all.  Then the adapters of the window pass one after the other; a row takes
+// the result of its own one, so that no other adapter's values (an infinity, say) reach it.
+constexpr int kExpandTiles = 4, kExpandRows = 16 * kExpandTiles;
+
 template <int DT, int NF, bool ACROSS>
-__global__ __launch_bounds__(64 * kExpandWaves) void adapter_expand_kernel(ExpandArgs A, int chunks) {
+__global__ __launch_bounds__(64 * kExpandWaves, NF <= 1 ? 3 : 2) void adapter_expand_kernel(ExpandArgs A, int chunks) {
   using T = Tile<DT>;
   using X = Expand<DT, NF, ACROSS>;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-  const int64_t row0 = (int64_t)(blockIdx.x / chunks) * kWindow;
-  const int chunk = blockIdx.x % chunks;
+  constexpr int TILES = kExpandTiles;
+  __shared__ u32x4 us[TILES][X::UF][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
+  const int64_t tile = xcd_share(blockIdx.x, gridDim.x);
+  const int64_t row0 = tile / chunks * kExpandRows;
+  const int chunk = (int)(tile % chunks);
   const int64_t n0 = ((int64_t)chunk * kExpandWaves + wave) * X::COLS;
-  const bool live = row0 + lane < A.tokens;
-  const int id = live ? row_adapter(A.ids, row0 + lane, A.adapters) : -1;
-  if (A.u_out && chunk == 0) {
-    const int64_t from = row0 * A.rank;
-    const int64_t count = (A.tokens - row0 < kWindow ? A.tokens - row0 : kWindow) * A.rank;
-    for (int64_t e = threadIdx.x; e < count; e += 64 * kExpandWaves) {
-      float s = A.u[from + e];
-      for (int k = 1; k < A.splits; ++k) s += A.u[k * A.part + from + e];
-      A.u_out[from + e] = s;
+  const int rows = A.tokens - row0 < kExpandRows ? (int)(A.tokens - row0) : kExpandRows;
+  const int id = lane < rows ? row_adapter(A.ids, row0 + lane, A.adapters) : -2;
+  const bool mine = n0 < A.N;  // (a wave past the columns still makes fragments)
+  const bool inside = (int64_t)(chunk + 1) * kExpandWaves * X::COLS <= A.N && rows == kExpandRows;
+  const int64_t col = n0 + T::PE * i;
+  // out[j][v]: row 16 j + 4 q + v; base at first
+  u32x4 out[TILES][4];
+  if (inside && A.base) {
+    const uint8_t *from = A.base + (row0 * A.ld_base + n0) * T::ES;
+    const uint32_t mine_at = (4 * q * (uint32_t)A.ld_base + T::PE * i) * T::ES;  // (the rest is the wave's)
+#pragma unroll
+    for (int j = 0; j < TILES; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        out[j][v] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a1 *>(from + (16 * j + v) * A.ld_base * T::ES + mine_at));
+  } else {
+#pragma unroll
+    for (int j = 0; j < TILES; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int r = 16 * j + 4 * q + v;
+        out[j][v] = u32x4{0, 0, 0, 0};
+        if (A.base && r < rows) out[j][v] = ld_frag_n<DT>(A.base + ((row0 + r) * A.ld_base + col) * T::ES, A.N - col);
+      }
+  }
+  const uint64_t live = ~0ull >> (64 - rows);
+  uint64_t rem = __ballot(id >= 0);
+  X W;
+  auto weights = [&](int a) {
+    if (mine) W.load(A.w + (int64_t)a * A.N * A.rank * T::ES, A.N, A.rank, n0, lane);
+  };
+  int a = 0;
+  if (rem) {
+    a = __builtin_amdgcn_readlane(id, __builtin_ctzll(rem));
+    weights(a);
+    // the row's scale goes into u
+    const int r_u = 16 * wave + i;
+    const int own = __builtin_amdgcn_ds_bpermute(r_u << 2, id);
+    if (wave < TILES) {
+      u32x4 uf[X::UF];
+      X::u_frags(uf, A.rank, q, [&](float(&v)[T::PE], int r, int left) {
+      const bool whole = A.rank % T::PE == 0;
+      const float s = A.scale && own >= 0 ? A.scale[own] : 1.0f;
+#pragma unroll
+      for (int e = 0; e < T::PE; ++e) v[e] = 0.0f;
+      if (own < 0 || left <= 0) return;
+      const float *up = A.u + (row0 + r_u) * A.rank + r;
+      for (int k = 0; k < A.splits; ++k) {
+#pragma unroll
+        for (int h = 0; h < T::PE; h += 4) {
+          const uint8_t *p = reinterpret_cast<const uint8_t *>(up + k * A.part + h);
+          const u32x4 t = whole ? ld_frag(p) : ld_frag_n<kF32>(p, left - h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[h + e] += bits_f32(t[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < T::PE; ++e) v[e] *= s;
+    });
+#pragma unroll
+      for (int f = 0; f < X::UF; ++f) us[wave][f][lane] = uf[f];
+    }
+    if (A.u_out && chunk == 0) {
+      for (int e = threadIdx.x; e < rows * A.rank; e += 64 * kExpandWaves)
+        A.u_out[row0 * A.rank + e] = parts_sum(A.u + row0 * A.rank + e, A.part, A.splits);
+    }
+  } else if (A.u_out && chunk == 0) {
+    for (int e = threadIdx.x; e < rows * A.rank; e += 64 * kExpandWaves) A.u_out[row0 * A.rank + e] = 0.0f;
+  }
+  __syncthreads();
+  if (!mine) return;
+  while (rem) {
+    const uint64_t match = __ballot(id == a);
+    rem &= ~match;
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+      const uint32_t here = (uint32_t)(match >> (16 * j)) & 0xFFFFu;
+      if (!here) continue;
+      u32x4 uf[X::UF];
+#pragma unroll
+      for (int f = 0; f < X::UF; ++f) uf[f] = us[j][f][lane];
+#pragma unroll
+      for (int h = 0; h < T::PE; h += 4) {  // four tiles at a time, for the registers
+        f32x4 acc[4];
+        W.product(acc, uf, h);
+        if (here == 0xFFFFu) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) add_products<DT>(out[j][v], acc, h, v);
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if ((here >> (4 * q + v)) & 1) add_products<DT>(out[j][v], acc, h, v);
+        }
+      }
+    }
+    if (rem) {
+      a = __builtin_amdgcn_readlane(id, __builtin_ctzll(rem));
+      weights(a);
     }
   }
-  if (n0 >= A.N) return;
-  const bool inside = n0 + X::COLS <= A.N, whole = A.rank % T::PE == 0;
-  for (uint64_t rem = __ballot(live); rem;) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(rem));
-    const uint64_t match = __ballot(id == a) & __ballot(live);
-    rem &= ~match;
-    const int n = __popcll(match);
-    const int line = lined_up(match, lane);
-    if (a < 0 && A.base == A.y) continue;  // already there
-    X W;
-    if (a >= 0) W.load(A.w + (int64_t)a * A.N * A.rank * T::ES, A.N, A.rank, n0, lane);
-    const float s = a >= 0 && A.scale ? A.scale[a] : 1.0f;
-    for (int j = 0; 16 * j < n; ++j) {
-      const int at = 16 * j + i;
-      const int to = __builtin_amdgcn_ds_bpermute((at < n ? at : 16 * j) << 2, line);
-      const int64_t row = row0 + to;
-      u32x4 base[4];
+  // rows without an adapter are in place already where y is base
+  const uint64_t wanted = A.base == A.y ? __ballot(id >= 0) : live;
+  if (inside && wanted == live) {
+    uint8_t *to = A.y + (row0 * A.ldy + n0) * T::ES;
+    const uint32_t mine_at = (4 * q * (uint32_t)A.ldy + T::PE * i) * T::ES;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int64_t col = n0 + X::piece(p, q);
-        const uint8_t *from = A.base + (row * A.ld_base + col) * T::ES;
-        if (!A.base) base[p] = u32x4{0, 0, 0, 0};
-        else if (inside) base[p] = ld_frag(from);
-        else base[p] = ld_frag_n<DT>(from, A.N - col);
+    for (int j = 0; j < TILES; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        __builtin_nontemporal_store(out[j][v], reinterpret_cast<u32x4_a1 *>(to + (16 * j + v) * A.ldy * T::ES + mine_at));
+  } else {
+#pragma unroll
+    for (int j = 0; j < TILES; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int r = 16 * j + 4 * q + v;
+        if ((wanted >> r) & 1) st_frag_n<DT>(A.y + ((row0 + r) * A.ldy + col) * T::ES, out[j][v], A.N - col);
       }
-      if (a >= 0) {
-        u32x4 uf[X::UF];
-        X::u_frags(uf, A.rank, q, [&](float(&v)[T::PE], int r, int left) {
-          const float *up = A.u + row * A.rank + (whole && left <= 0 ? 0 : r);
-#pragma unroll
-          for (int e = 0; e < T::PE; ++e) v[e] = 0.0f;
-          for (int k = 0; k < A.splits; ++k) {
-#pragma unroll
-            for (int h = 0; h < T::PE; h += 4) {
-              const uint8_t *p = reinterpret_cast<const uint8_t *>(up + k * A.part + h);
-              const u32x4 t = whole ? ld_frag(p) : ld_frag_n<kF32>(p, left - h);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[h + e] += bits_f32(t[e]);
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < T::PE; ++e) v[e] = whole && left <= 0 ? 0.0f : v[e] * s;
-        });
-        f32x4 acc[T::PE];
-        W.product(acc, uf);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          float f[T::PE];
-#pragma unroll
-          for (int e = 0; e < T::PE; ++e) f[e] = X::at(acc, p, e);
-          base[p] = add_base<DT>(base[p], f);
-        }
-      }
-      if (at < n) {
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const int64_t col = n0 + X::piece(p, q);
-          uint8_t *to_y = A.y + (row * A.ldy + col) * T::ES;
-          if (inside) *reinterpret_cast<u32x4_a1 *>(to_y) = base[p];
-          else st_frag_n<DT>(to_y, base[p], A.N - col);
-        }
-      }
-    }
   }
 }
 
 // ---- launches ----------------------------------------------------------------------
 
-// Parts of the long dimension: as many as fill the chip's 256 CUs twice, each with
-// work for the eight waves.
+inline int window_count(int64_t tokens) { return (int)((tokens + kWindow - 1) / kWindow); }
+
+// Parts of the long dimension: as many as put two workgroups on each of the 256 CUs.
 inline int shrink_splits(int64_t tokens, int64_t K) {
-  const int64_t groups = (tokens + 15) / 16;
-  const int64_t most = (K + 1023) / 1024;
-  int64_t s = 512 / (groups > 0 ? groups : 1);
+  const int64_t windows = window_count(tokens);
+  const int64_t most = (K + 511) / 512;
+  int64_t s = 512 / (windows > 0 ? windows : 1);
   if (s > most) s = most;
+  if (s > 16) s = 16;
+  return s < 1 ? 1 : (int)s;
+}
+
+// Workgroups that share a window's adapters.
+inline int shrink_slots(int64_t tokens, int adapters, int splits) {
+  const int64_t windows = window_count(tokens);
+  int64_t s = 2048 / ((windows > 0 ? windows : 1) * splits);
+  if (s > 64) s = 64;
+  if (s > adapters) s = adapters;
   return s < 1 ? 1 : (int)s;
 }
 
 template <int DT, bool ACROSS>
 hipError_t launch_shrink_dt(const ShrinkArgs &A, const PlanArgs &P, hipStream_t stream) {
-  const int64_t windows = (A.tokens + kWindow - 1) / kWindow;
   const int rt = (A.rank + 15) / 16;
-  const dim3 grid((unsigned)(windows * 4 + (P.order ? 1 : 0)), A.splits);
-  const int th = 64 * kShrinkWaves;
-  if (rt <= 1) adapter_shrink_kernel<DT, 1, 1, ACROSS><<<grid, th, 0, stream>>>(A, P);
-  else if (rt <= 2) adapter_shrink_kernel<DT, 2, 1, ACROSS><<<grid, th, 0, stream>>>(A, P);
-  else if (rt <= 4) adapter_shrink_kernel<DT, 4, 1, ACROSS><<<grid, th, 0, stream>>>(A, P);
-  else adapter_shrink_kernel<DT, 8, 1, ACROSS><<<grid, th, 0, stream>>>(A, P);
+  const int64_t pairs = (int64_t)A.windows * A.splits;
+  const dim3 grid((unsigned)((pairs + 7) / 8 * 8 * A.slots + (P.order ? 8 : 0)));
+  const int th = kShrinkThreads;
+  if (rt <= 1) adapter_shrink_kernel<DT, 1, ACROSS><<<grid, th, 0, stream>>>(A, P);
+  else if (rt <= 2) adapter_shrink_kernel<DT, 2, ACROSS><<<grid, th, 0, stream>>>(A, P);
+  else if (rt <= 4) adapter_shrink_kernel<DT, 4, ACROSS><<<grid, th, 0, stream>>>(A, P);
+  else adapter_shrink_kernel<DT, 8, ACROSS><<<grid, th, 0, stream>>>(A, P);
   return hipGetLastError();
 }
 
@@ -315,7 +530,7 @@ hipError_t launch_shrink(int dtype, const ShrinkArgs &A, const PlanArgs &P, hipS
 
 template <int DT, bool ACROSS>
 hipError_t launch_expand_dt(const ExpandArgs &A, hipStream_t stream) {
-  const int64_t windows = (A.tokens + kWindow - 1) / kWindow;
+  const int64_t windows = (A.tokens + kExpandRows - 1) / kExpandRows;
   const int64_t cols = kExpandWaves * Expand<DT, 1, ACROSS>::COLS;
   const int chunks = (int)((A.N + cols - 1) / cols);
   const int rt = (A.rank + 15) / 16;

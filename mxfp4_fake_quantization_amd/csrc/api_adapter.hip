@@ -38,7 +38,7 @@ mxfp4_status_t check_adapter(const mxfp4_adapter_t *d) {
 
 mxfp4_status_t check_rows(const void *p, int64_t ld, int64_t cols, int32_t dtype, const char *what) {
   MXFP4_TRY(check_elems(p, dtype, what));
-  if (ld < cols || ld > (int64_t)1 << 40)
+  if (ld < cols || ld > (int64_t)1 << 26)
     return fail(MXFP4_EINVAL, "%s: %lld elements between rows of %lld", what, (long long)ld, (long long)cols);
   return MXFP4_OK;
 }
