@@ -3,7 +3,7 @@
 //     grad_x[t] = base[t] + du[t] A_i        (expand with A read across its rows)
 //     grad_A_i = sum over t of du[t]^T x[t],  grad_B_i = s_i sum over t of grad_y[t]^T u[t]
 // i = ids[t].  grad_y is read twice, x once; the sums over rows are split into
-// pieces whose parts are added in their order: no atomics, the same bits each time.
+// pieces whose parts are added in a fixed order: no atomics, the same bits each time.
 #include "adapter_launch.h"
 
 namespace mxfp4 {
@@ -35,7 +35,7 @@ struct GradArgs {
   int adapters, rank;
 };
 
-template <int DT, int RT>
+template <int DT, int RT, int MODE>
 __global__ __launch_bounds__(64 * kGradWaves) void adapter_grad_kernel(GradArgs A) {
   using T = Tile<DT>;
   __shared__ float sums[kGradWaves][T::PE][64][4];
@@ -50,7 +50,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void adapter_grad_kernel(GradArgs 
   const int count = pc.z;
   const int32_t *order = A.order + pc.y;
   const int64_t col = n0 + T::PE * i;
-  const bool inside = n0 + 16 * T::PE <= S.cols;
+  const RowPiece<DT, MODE> piece_z(col, S.cols);
   int vr[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) vr[r] = 16 * r + i < A.rank ? 16 * r + i : A.rank - 1;
@@ -68,10 +68,13 @@ __global__ __launch_bounds__(64 * kGradWaves) void adapter_grad_kernel(GradArgs 
     float v[RT][T::PE];
 #pragma unroll
     for (int e = 0; e < T::PE; ++e) {
-      const uint8_t *p = S.z + (row[e] * S.ld + col) * T::ES;
-      z[e] = inside ? ld_frag(p) : ld_frag_n<DT>(p, S.cols - col);
+      z[e] = piece_z.raw(S.z + row[e] * S.ld * T::ES);
 #pragma unroll
       for (int r = 0; r < RT; ++r) v[r][e] = S.v[(int64_t)row[e] * A.rank + vr[r]];
+    }
+    if constexpr (MODE == kCut) {
+#pragma unroll
+      for (int e = 0; e < T::PE; ++e) z[e] = piece_z.settled(z[e]);
     }
     if ((st + 1) * T::KF > count) {  // rows past the piece count as 0
 #pragma unroll
@@ -142,7 +145,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void adapter_grad_kernel(GradArgs 
   }
 }
 
-// Each adapter's pieces added up, in their order, and rounded once; 0 for an adapter
+// Each adapter's pieces added up, in a fixed order, and rounded once; 0 for an adapter
 // without rows.
 struct GradSumArgs {
   const float *part_a, *part_b;
@@ -152,10 +155,14 @@ struct GradSumArgs {
   int64_t size_a, size_b;        // elements of an adapter's gradient
   int blocks_a, blocks_b;        // workgroups of each
 };
-constexpr int kSumThreads = 256, kSumEach = 4;
+// Four groups of 64 threads share out the pieces, four loads of each under way at a
+// time (16 pieces one after the other took 7 us).
+constexpr int kSumLanes = 64, kSumGroups = 4, kSumEach = 4, kSumThreads = kSumLanes * kSumGroups;
 
 template <int DT>
 __global__ __launch_bounds__(kSumThreads) void adapter_grad_sum_kernel(GradSumArgs A) {
+  __shared__ f32x4 sums[kSumGroups][kSumLanes];
+  const int lane = threadIdx.x & 63, group = threadIdx.x >> 6;
   const int blocks = A.blocks_a + A.blocks_b;
   const int a = blockIdx.x / blocks;
   int b = blockIdx.x % blocks;
@@ -164,16 +171,30 @@ __global__ __launch_bounds__(kSumThreads) void adapter_grad_sum_kernel(GradSumAr
   const int64_t size = is_b ? A.size_b : A.size_a;
   const float *part = is_b ? A.part_b : A.part_a;
   uint8_t *out = is_b ? A.grad_b : A.grad_a;
-  const int64_t e0 = ((int64_t)b * kSumThreads + threadIdx.x) * kSumEach;
-  if (e0 >= size) return;
+  const int64_t e0 = ((int64_t)b * kSumLanes + lane) * kSumEach;
   const int lo = A.first[a], hi = A.first[a + 1];
   const float s = is_b && A.scale ? A.scale[a] : 1.0f;
-  float f[kSumEach] = {};
-  for (int p = lo; p < hi; ++p) {
-    const u32x4 v = ld_frag_n<kF32>(reinterpret_cast<const uint8_t *>(part + p * size + e0), size - e0);
+  f32x4 f = {0, 0, 0, 0};
+  auto piece = [&](int p) {
+    const uint8_t *at = reinterpret_cast<const uint8_t *>(part + p * size);
+    return size >= 4 ? RowPiece<kF32, kCut>(e0, size).load(at) : ld_single<kF32>(at, size - e0);
+  };
+  if (e0 < size) {
+    int p = lo + group;
+    for (; p + 3 * kSumGroups < hi; p += 4 * kSumGroups) {
+      u32x4 v[4];
 #pragma unroll
-    for (int j = 0; j < kSumEach; ++j) f[j] += bits_f32(v[j]);
+      for (int k = 0; k < 4; ++k) v[k] = piece(p + k * kSumGroups);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f += __builtin_bit_cast(f32x4, v[k]);
+    }
+    for (; p < hi; p += kSumGroups) f += __builtin_bit_cast(f32x4, piece(p));
   }
+  sums[group][lane] = f;
+  __syncthreads();
+  if (group > 0 || e0 >= size) return;
+#pragma unroll
+  for (int g = 1; g < kSumGroups; ++g) f += sums[g][lane];
 #pragma unroll
   for (int j = 0; j < kSumEach; ++j)
     if (e0 + j < size) {
@@ -227,7 +248,7 @@ BwdSpace bwd_space(int64_t tokens, int64_t in, int64_t out, int rank, int adapte
 }
 
 template <int DT>
-hipError_t launch_grads(const AdapterBwdLaunch &L, const BwdSpace &S, hipStream_t stream) {
+hipError_t launch_grads(const AdapterBwdLaunch &L, const BwdSpace &S, int mode, hipStream_t stream) {
   constexpr int cols = 16 * Tile<DT>::PE;
   uint8_t *ws = L.workspace;
   float *part_a = reinterpret_cast<float *>(ws + S.part_a), *part_b = reinterpret_cast<float *>(ws + S.part_b);
@@ -244,29 +265,23 @@ hipError_t launch_grads(const AdapterBwdLaunch &L, const BwdSpace &S, hipStream_
   G.rank = L.rank;
   if (S.most > 0) {
     const unsigned grid = (unsigned)(S.most * (G.a.groups + G.b.groups));
-    const int rt = (L.rank + 15) / 16, th = 64 * kGradWaves;
-    if (rt <= 1) adapter_grad_kernel<DT, 1><<<grid, th, 0, stream>>>(G);
-    else if (rt <= 2) adapter_grad_kernel<DT, 2><<<grid, th, 0, stream>>>(G);
-    else if (rt <= 4) adapter_grad_kernel<DT, 4><<<grid, th, 0, stream>>>(G);
-    else adapter_grad_kernel<DT, 8><<<grid, th, 0, stream>>>(G);
+    by_rank_and_mode(L.rank, mode, [&](auto rt, auto m) {
+      adapter_grad_kernel<DT, decltype(rt)::value, decltype(m)::value><<<grid, 64 * kGradWaves, 0, stream>>>(G);
+    });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const int64_t sa = L.grad_a ? L.rank * L.in : 0, sb = L.grad_b ? L.rank * L.out : 0;
-  constexpr int each = kSumThreads * kSumEach;
+  constexpr int each = kSumLanes * kSumEach;
   GradSumArgs R{part_a, part_b, static_cast<uint8_t *>(L.grad_a), static_cast<uint8_t *>(L.grad_b), first, L.scale, sa, sb,
                 (int)((sa + each - 1) / each), (int)((sb + each - 1) / each)};
   adapter_grad_sum_kernel<DT><<<(unsigned)((R.blocks_a + R.blocks_b) * L.adapters), kSumThreads, 0, stream>>>(R);
   return hipGetLastError();
 }
 
-}  // namespace
-
-int64_t adapter_bwd_workspace(int64_t tokens, int64_t in, int64_t out, int rank, int adapters, bool grad_a, bool grad_b) {
-  return bwd_space(tokens, in, out, rank, adapters, grad_a, grad_b).total;
-}
-
-hipError_t launch_adapter_bwd(const AdapterBwdLaunch &L, hipStream_t stream) {
+template <int DT>
+hipError_t backward(const AdapterBwdLaunch &L, hipStream_t stream) {
+  const int mode = piece_mode(DT, L.tokens, L.in, L.out, L.rank);
   const BwdSpace S = bwd_space(L.tokens, L.in, L.out, L.rank, L.adapters, L.grad_a, L.grad_b);
   uint8_t *ws = L.workspace;
   float *du = reinterpret_cast<float *>(ws + S.du);
@@ -284,13 +299,13 @@ hipError_t launch_adapter_bwd(const AdapterBwdLaunch &L, hipStream_t stream) {
   ShrinkArgs D{static_cast<const uint8_t *>(L.grad_y), static_cast<const uint8_t *>(L.b), L.ids, L.scale, parts, L.tokens,
                L.ld_gy, L.out, part, L.adapters, L.rank, splits, shrink_slots(L.tokens, L.adapters, splits),
                L.grad_x || L.grad_a ? window_count(L.tokens) : 0};
-  hipError_t e = launch_shrink<true>(L.dtype, D, P, stream);
+  hipError_t e = launch_shrink<DT, true>(D, P, mode, stream);
   if (e != hipSuccess) return e;
   if (L.grad_x && L.tokens > 0) {
     ExpandArgs X{parts, static_cast<const uint8_t *>(L.a), L.ids, nullptr, static_cast<const uint8_t *>(L.base),
                  static_cast<uint8_t *>(L.grad_x), splits > 1 && L.grad_a ? du : nullptr, L.tokens, L.in, L.ld_base,
                  L.ld_gx, part, L.adapters, L.rank, splits};
-    e = launch_expand<true>(L.dtype, X, stream);
+    e = launch_expand<DT, true>(X, mode, stream);
     if (e != hipSuccess) return e;
   }
   if (L.grad_a && !L.grad_x && splits > 1 && part > 0) {
@@ -299,7 +314,17 @@ hipError_t launch_adapter_bwd(const AdapterBwdLaunch &L, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   if (!L.grad_a && !L.grad_b) return hipSuccess;
-  return L.dtype == kBF16 ? launch_grads<kBF16>(L, S, stream) : launch_grads<kF32>(L, S, stream);
+  return launch_grads<DT>(L, S, mode, stream);
+}
+
+}  // namespace
+
+int64_t adapter_bwd_workspace(int64_t tokens, int64_t in, int64_t out, int rank, int adapters, bool grad_a, bool grad_b) {
+  return bwd_space(tokens, in, out, rank, adapters, grad_a, grad_b).total;
+}
+
+hipError_t launch_adapter_bwd(const AdapterBwdLaunch &L, hipStream_t stream) {
+  return L.dtype == kBF16 ? backward<kBF16>(L, stream) : backward<kF32>(L, stream);
 }
 
 }  // namespace mxfp4

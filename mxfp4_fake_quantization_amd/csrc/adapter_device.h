@@ -47,14 +47,27 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
   }
 }
 
-// A whole 16-byte piece at any element alignment.
+// ---- pieces of 16 bytes ----------------------------------------------------------
+//
+// A row's last piece may be cut short, and rows start at any element (the hardware
+// takes unaligned accesses).  How a kernel meets that, chosen by its sizes:
+//   kExact   every row has a whole number of pieces: a piece is there or not;
+//   kCut     rows of any length: a piece that sticks out is loaded from the last 16
+//            bytes of its row (or array) and shifted down, zeros following, so the load
+//            itself hangs on no condition and the loads of a loop stay in flight
+//            together (a branch around a load made the compiler wait for all of them);
+//   kSingle  rows shorter than a piece: element by element.
+enum { kExact = 0, kCut = 1, kSingle = 2 };
+
 __device__ __forceinline__ u32x4 ld_frag(const uint8_t *p) { return *reinterpret_cast<const u32x4_a1 *>(p); }
+__device__ __forceinline__ u32x4 ld_frag_nt(const uint8_t *p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a1 *>(p));
+}
 
 // The first n elements of a piece, the others 0.
 template <int DT>
-__device__ __forceinline__ u32x4 ld_frag_n(const uint8_t *p, int64_t n) {
+__device__ __forceinline__ u32x4 ld_single(const uint8_t *p, int64_t n) {
   u32x4 w = {0, 0, 0, 0};
-  if (n >= Tile<DT>::PE) return ld_frag(p);
 #pragma unroll
   for (int j = 0; j < Tile<DT>::PE; ++j)
     if (j < n) {
@@ -62,6 +75,75 @@ __device__ __forceinline__ u32x4 ld_frag_n(const uint8_t *p, int64_t n) {
       else w[j & 3] = reinterpret_cast<const uint32_t *>(p)[j];
     }
   return w;
+}
+
+// A piece without its first d elements, zeros following; none for d >= PE.
+template <int DT>
+__device__ __forceinline__ u32x4 shifted(u32x4 w, int d) {
+  if (d <= 0) return w;
+  if (d >= Tile<DT>::PE) return u32x4{0, 0, 0, 0};
+  const int bits = d * 8 * Tile<DT>::ES;
+  if (bits & 64) w = u32x4{w[2], w[3], 0, 0};
+  if (bits & 32) w = u32x4{w[1], w[2], w[3], 0};
+  if (DT == kBF16 && (bits & 16))
+    w = u32x4{w[0] >> 16 | w[1] << 16, w[1] >> 16 | w[2] << 16, w[2] >> 16 | w[3] << 16, w[3] >> 16};
+  return w;
+}
+
+// The first n elements, the others 0.
+template <int DT>
+__device__ __forceinline__ u32x4 only(u32x4 w, int n) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    if (DT == kBF16) w[d] = n >= 2 * d + 2 ? w[d] : n == 2 * d + 1 ? w[d] & 0xFFFFu : 0u;
+    else w[d] = n > d ? w[d] : 0u;
+  }
+  return w;
+}
+
+// Piece at element e of a row of `len` elements at `row` (len >= PE but for kSingle):
+// where to load it, what to shift it by.  kExact: 0 or PE.
+template <int DT, int MODE>
+struct RowPiece {
+  int64_t at;
+  int shift;
+  __device__ __forceinline__ RowPiece(int64_t e, int64_t len) {
+    const int64_t last = len - Tile<DT>::PE;
+    at = MODE == kSingle || e <= last ? e : last;
+    const int64_t d = e - at;
+    shift = d > Tile<DT>::PE ? Tile<DT>::PE : (int)d;
+    n = MODE == kSingle ? len - e : 0;
+  }
+  int64_t n;  // kSingle: elements there
+  __device__ __forceinline__ u32x4 raw(const uint8_t *row) const {
+    if constexpr (MODE == kSingle) return ld_single<DT>(row + at * Tile<DT>::ES, n);
+    return ld_frag(row + at * Tile<DT>::ES);
+  }
+  __device__ __forceinline__ u32x4 settled(u32x4 w) const {
+    if constexpr (MODE == kSingle) return w;
+    if constexpr (MODE == kExact) return shift ? u32x4{0, 0, 0, 0} : w;
+    return shifted<DT>(w, shift);
+  }
+  __device__ __forceinline__ u32x4 load(const uint8_t *row) const { return settled(raw(row)); }
+};
+
+// The n elements (of at most PE; the others 0) at p in an array whose last 16 bytes are
+// at `last`, for rows that may be shorter than a piece: the load, and what is left to do
+// when the value is needed.
+template <int DT, int MODE>
+__device__ __forceinline__ u32x4 ld_inside(const uint8_t *p, const uint8_t *last, int n) {
+  if constexpr (MODE == kSingle) return ld_single<DT>(p, n);
+  return ld_frag(MODE == kCut && p > last ? last : p);
+}
+template <int DT, int MODE>
+__device__ __forceinline__ u32x4 settle_inside(u32x4 w, const uint8_t *p, const uint8_t *last, int n) {
+  if constexpr (MODE == kSingle) return w;
+  if constexpr (MODE == kExact) return n > 0 ? w : u32x4{0, 0, 0, 0};
+  if (p > last) {
+    const int64_t d = (p - last) / Tile<DT>::ES;
+    w = shifted<DT>(w, d > Tile<DT>::PE ? Tile<DT>::PE : (int)d);
+  }
+  return only<DT>(w, n);
 }
 
 template <int DT>
@@ -143,7 +225,7 @@ constexpr int frag_count(int rank_tiles) {  // of 16-rank tiles
   return DT == kBF16 ? rank_tiles / 2 : rank_tiles;
 }
 
-template <int DT, int NF, bool ACROSS>
+template <int DT, int NF, bool ACROSS, int MODE>
 struct Expand {
   using T = Tile<DT>;
   static constexpr int F = NF ? NF : 1;
@@ -155,51 +237,56 @@ struct Expand {
     return NF ? f * T::KF + T::PE * q : T::PE * (q & 1);
   }
 
-  // (Whole pieces are loaded without a branch: those past the last rank are dropped.)
-  __device__ __forceinline__ void load(const uint8_t *wp, int64_t N, int rank, int64_t n0, int lane) {
-    const int i = lane & 15, q = lane >> 4;
-    const u32x4 zero = {0, 0, 0, 0};
+  // The weights of columns n0 to n0 + COLS - 1 of one adapter's W, loaded; settle() makes
+  // the fragments of them.  Columns past the last hold anything, ranks past the last 0.
+  struct From {
+    const uint8_t *w;
+    int64_t N, n0;
+    int rank, lane;
+  };
+  __device__ __forceinline__ const uint8_t *row_of(const From &S, int f, int j) const {
+    const int64_t col = S.n0 + T::PE * (S.lane & 15) + j;
+    const int r0 = rank0(f, S.lane >> 4);  // (ranks past the last: any piece, dropped)
+    return S.w + ((col < S.N ? col : S.N - 1) * S.rank + (r0 < S.rank ? r0 : 0)) * T::ES;
+  }
+  __device__ __forceinline__ void load(const From &S) {
     if constexpr (ACROSS) {
-      const int64_t col = n0 + T::PE * i;
-      const bool inside = n0 + COLS <= N;
+      const RowPiece<DT, MODE> col(S.n0 + T::PE * (S.lane & 15), S.N);
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int e = 0; e < T::PE; ++e) {
+          const int r = rank0(f, S.lane >> 4) + e;
+          w[f][e] = col.raw(S.w + (r < S.rank ? r : S.rank - 1) * S.N * T::ES);
+        }
+    } else {
+      const uint8_t *last = S.w + S.N * S.rank * T::ES - 16;
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int j = 0; j < T::PE; ++j)
+          w[f][j] = ld_inside<DT, MODE>(row_of(S, f, j), last, S.rank - rank0(f, S.lane >> 4));
+    }
+  }
+  __device__ __forceinline__ void settle(const From &S) {
+    if constexpr (ACROSS) {
+      const RowPiece<DT, MODE> col(S.n0 + T::PE * (S.lane & 15), S.N);
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        const int r0 = rank0(f, q);
         u32x4 rows[T::PE];
-        if (inside) {
 #pragma unroll
-          for (int e = 0; e < T::PE; ++e) {
-            const int r = r0 + e < rank ? r0 + e : rank - 1;
-            const u32x4 v = ld_frag(wp + (r * N + col) * T::ES);
-            rows[e] = r0 + e < rank ? v : zero;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < T::PE; ++e) {
-            rows[e] = zero;
-            if (r0 + e < rank) rows[e] = ld_frag_n<DT>(wp + ((r0 + e) * N + col) * T::ES, N - col);
-          }
-        }
+        for (int e = 0; e < T::PE; ++e)
+          rows[e] = rank0(f, S.lane >> 4) + e < S.rank ? col.settled(w[f][e]) : u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < T::PE; ++j) w[f][j] = turned<DT>(rows, j);
       }
     } else {
-      const bool whole = rank % T::PE == 0;
+      const uint8_t *last = S.w + S.N * S.rank * T::ES - 16;
 #pragma unroll
-      for (int f = 0; f < F; ++f) {
-        const int r0 = rank0(f, q);
+      for (int f = 0; f < F; ++f)
 #pragma unroll
-        for (int j = 0; j < T::PE; ++j) {
-          const int64_t col = n0 + T::PE * i + j;
-          const uint8_t *row = wp + (col < N ? col : N - 1) * rank * T::ES;
-          if (whole) {
-            const u32x4 v = ld_frag(row + (r0 < rank ? r0 : 0) * T::ES);
-            w[f][j] = r0 < rank ? v : zero;
-          } else {
-            w[f][j] = ld_frag_n<DT>(row + r0 * T::ES, rank - r0);
-          }
-        }
-      }
+        for (int j = 0; j < T::PE; ++j)
+          w[f][j] = settle_inside<DT, MODE>(w[f][j], row_of(S, f, j), last, S.rank - rank0(f, S.lane >> 4));
     }
   }
 

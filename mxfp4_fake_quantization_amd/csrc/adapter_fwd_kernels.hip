@@ -1,26 +1,360 @@
 // adapter_fwd_kernels.hip -- low-rank adapters of many requests beside a shared
 // projection on gfx950: y[t] = base[t] + s_i B_i (A_i x[t]), i = ids[t].
+//
+// Two launches, u = x A^T and y = base + s u B^T; many rows as in adapter_launch.h, few
+// rows (decode) as below.
 #include "adapter_launch.h"
 
 namespace mxfp4 {
-int64_t adapter_workspace(int64_t tokens, int64_t in, int64_t out, int rank, int adapters, int dtype) {
-  return tokens * rank * shrink_splits(tokens, in);
+namespace {
+
+// ---- few rows ----------------------------------------------------------------------
+//
+// Bound by reading each adapter's weights once, and by latency: many small workgroups,
+// each with all its loads under way at once.  A workgroup takes the rows of one adapter
+// in a window of 64 (it is the workgroup of the first of them; those of the others end
+// at once) and a part of the long dimension (u) or of the columns (y).
+// One launch that computed u again for every part of the columns read A once a part
+// through each CU's L1 at 64 bytes a clock: 64 tokens of 48 adapters, 8192 -> 28672, rank
+// 16 took 51 us, one token 4096 -> 4096 9.4.
+
+struct FewArgs {
+  const uint8_t *x, *a, *b;
+  const int32_t *ids;
+  const float *scale;
+  const uint8_t *base;
+  uint8_t *y;
+  float *u;             // [splits][tokens, rank]
+  float *u_out;         // [tokens, rank] or NULL
+  int64_t tokens, in, out, ldx, ld_base, ldy, part;
+  int adapters, rank, splits, parts;
+};
+
+constexpr int kFewWaves = 4;
+
+// The rows of one adapter in a window.
+struct FewRows {
+  int64_t row0;
+  int own, n, line;     // line: lane t holds the t-th row
+  bool mine;            // this workgroup's
+  __device__ __forceinline__ FewRows(const FewArgs &A, int m, int lane) {
+    row0 = m / kWindow * kWindow;
+    const int id = row0 + lane < A.tokens ? row_adapter(A.ids, row0 + lane, A.adapters) : -2;
+    own = __builtin_amdgcn_readlane(id, m % kWindow);
+    const uint64_t match = __ballot(id == own);
+    mine = __builtin_ctzll(match) == m % kWindow;
+    n = __popcll(match);
+    line = lined_up(match, lane);
+  }
+  // Row `at`, the last one from n on (every lane takes part).
+  __device__ __forceinline__ int64_t row(int at) const {
+    return row0 + __builtin_amdgcn_ds_bpermute((at < n ? at : n - 1) << 2, line);
+  }
+};
+
+template <int DT, int RT, int MODE>
+__global__ __launch_bounds__(64 * kFewWaves) void adapter_few_u_kernel(FewArgs A) {
+  using T = Tile<DT>;
+  constexpr int U = RT <= 1 ? 8 : RT <= 4 ? 4 : 2;  // fragments of a turn, as the registers allow
+  __shared__ f32x4 part[kFewWaves][RT][64];
+  const int m = blockIdx.x;
+  if (m >= A.tokens) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
+  const FewRows R(A, m, lane);
+  if (!R.mine || R.own < 0) return;
+  float *u = A.u + blockIdx.y * A.part;
+  const uint8_t *wa = A.a + (int64_t)R.own * A.rank * A.in * T::ES;
+  uint32_t at_w[RT];  // the lane's row of each 16 ranks, from the first (few_rows() bounds it)
+#pragma unroll
+  for (int r = 0; r < RT; ++r) at_w[r] = ((16 * r + i < A.rank ? 16 * r + i : A.rank - 1) * (uint32_t)A.in + T::PE * q) * T::ES;
+  const int64_t turns = A.in / (U * T::KF);
+  const int first = blockIdx.y * kFewWaves + wave, step = kFewWaves * A.splits;
+  for (int t = 0; 16 * t < R.n; ++t) {
+    const int at = 16 * t + i;
+    const int64_t row_x = R.row(at);
+    const uint8_t *xp = A.x + row_x * A.ldx * T::ES;
+    f32x4 acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
+    for (int64_t turn = first; turn < turns; turn += step) {
+      u32x4 xf[U], wf[U][RT];
+#pragma unroll
+      for (int c = 0; c < U; ++c)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) wf[c][r] = ld_frag(wa + (turn * U + c) * T::KF * T::ES + at_w[r]);
+#pragma unroll
+      for (int c = 0; c < U; ++c) xf[c] = u32x4{0, 0, 0, 0};
+      if (at < R.n) {  // (lanes without a row would cost the L1 a cycle for each 64 bytes)
+#pragma unroll
+        for (int c = 0; c < U; ++c) xf[c] = ld_frag(xp + ((turn * U + c) * T::KF + T::PE * q) * T::ES);
+      }
+#pragma unroll
+      for (int c = 0; c < U; ++c)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r] = mma<DT>(wf[c][r], xf[c], acc[r]);
+    }
+    // the rest of the row, fragment by fragment
+    for (int64_t k0 = (turns * U + first) * T::KF; k0 < A.in; k0 += step * T::KF) {
+      const RowPiece<DT, MODE> piece(k0 + T::PE * q, A.in);
+      const u32x4 xf = piece.load(xp);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r] = mma<DT>(piece.load(wa + at_w[r] - T::PE * q * T::ES), xf, acc[r]);
+    }
+    __syncthreads();  // the tile before has been read
+#pragma unroll
+    for (int r = 0; r < RT; ++r) part[wave][r][lane] = acc[r];
+    __syncthreads();
+    for (int r = wave; r < RT; r += kFewWaves) {
+      f32x4 sum = part[0][r][lane];
+#pragma unroll
+      for (int w = 1; w < kFewWaves; ++w) sum += part[w][r][lane];
+      const int r0 = 16 * r + 4 * q;
+      if (at < R.n) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (r0 + v < A.rank) u[row_x * A.rank + r0 + v] = sum[v];
+      }
+    }
+  }
 }
 
-hipError_t launch_adapter(const AdapterLaunch &L, hipStream_t stream) {
-  const int splits = shrink_splits(L.tokens, L.in);
-  const bool keep = L.u != nullptr;
-  float *u = splits == 1 && keep ? L.u : L.workspace;
+// Columns are the rows of the first operand here: tile j of a run has columns 16 j to
+// 16 j + 15, whose weights are one contiguous piece of B, and a lane's results are four
+// consecutive columns of token l % 16.  (The other way round, as for many rows, a tile's
+// weights come in 16 pieces; that way pays in stores, of which few rows have few.)
+template <int DT>
+struct Quad {  // four consecutive elements of a row
+  uint32_t w[DT == kBF16 ? 2 : 4];
+  __device__ __forceinline__ void load(const uint8_t *p, int64_t left, bool inside) {
+    if (inside) {
+      if constexpr (DT == kBF16) {
+        typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+        const u32x2 v = *reinterpret_cast<const u32x2_a2 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+      } else {
+        const u32x4 v = ld_frag(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e % (DT == kBF16 ? 2 : 4)] = v[e];
+      }
+    } else {
+      const u32x4 v = ld_single<DT>(p, left < 4 ? left : 4);
+#pragma unroll
+      for (int e = 0; e < (DT == kBF16 ? 2 : 4); ++e) w[e] = v[e];
+    }
+  }
+  __device__ __forceinline__ void add(f32x4 f) {
+    if constexpr (DT == kBF16) {
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+        w[d] = pack_bf16(bits_f32(w[d] << 16) + f[2 * d], bits_f32(w[d] & 0xFFFF0000u) + f[2 * d + 1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e % (DT == kBF16 ? 2 : 4)] = __builtin_bit_cast(uint32_t, bits_f32(w[e % (DT == kBF16 ? 2 : 4)]) + f[e]);
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t *p, int64_t left, bool inside) const {
+    if (inside) {
+      if constexpr (DT == kBF16) {
+        typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+        *reinterpret_cast<u32x2_a2 *>(p) = u32x2{w[0], w[1]};
+      } else {
+        *reinterpret_cast<u32x4_a1 *>(p) = u32x4{w[0], w[1], w[2 % (DT == kBF16 ? 2 : 4)], w[3 % (DT == kBF16 ? 2 : 4)]};
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < left) {
+          if (DT == kBF16) reinterpret_cast<uint16_t *>(p)[e] = (uint16_t)(w[(e >> 1) % 2] >> (16 * (e & 1)));
+          else reinterpret_cast<uint32_t *>(p)[e] = w[e % (DT == kBF16 ? 2 : 4)];
+        }
+    }
+  }
+};
+
+constexpr int few_tiles(int rt) { return rt <= 2 ? 8 : 4; }  // of a run, as the registers allow
+
+template <int DT, int RT, int MODE>
+__global__ __launch_bounds__(64 * kFewWaves) void adapter_few_y_kernel(FewArgs A) {
+  using T = Tile<DT>;
+  using X = Expand<DT, frag_count<DT>(RT), false, MODE>;
+  constexpr int F = X::F, TILES = few_tiles(RT), COLS = 16 * TILES;
+  const int m = blockIdx.x;
+  if (m >= A.tokens) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
+  const FewRows R(A, m, lane);
+  if (!R.mine) return;
+  const int own = R.own, n = R.n;
+  const bool out_u = A.u_out && blockIdx.y == 0;
+  const int64_t runs = (A.out + COLS - 1) / COLS;
+  const int64_t first = blockIdx.y * kFewWaves + wave, step = kFewWaves * A.parts;
+  const uint8_t *wb = A.b + (int64_t)(own < 0 ? 0 : own) * A.out * A.rank * T::ES;
+  const uint8_t *w_last = wb + A.out * A.rank * T::ES - 16;
+  const float s = own >= 0 && A.scale ? A.scale[own] : 1.0f;
+  // The lane's pieces of a run's weights lie at one distance each from the run's first
+  // row, which is the wave's: loads take no arithmetic (it was what bound this kernel).
+  uint32_t at_w[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const int r0 = X::rank0(f, q);
+    at_w[f] = (i * A.rank + (r0 < A.rank ? r0 : 0)) * T::ES;
+  }
+  const uint32_t tile_bytes = 16 * A.rank * T::ES;
+  const bool full = MODE == kExact && A.rank == 16 * RT;  // no fragment holds a rank past the last
+  for (int t = 0; 16 * t < n; ++t) {
+    const int64_t row = R.row(16 * t + i);
+    const bool wanted = 16 * t + i < n;
+    u32x4 uf[X::UF];
+    bool have_u = false;
+    const uint8_t *base_row = A.base + (row * A.ld_base + 4 * q) * T::ES;
+    uint8_t *y_row = A.y + (row * A.ldy + 4 * q) * T::ES;
+    for (int64_t run = first; run < runs; run += step) {
+      const int64_t n0 = run * COLS, left = A.out - n0 - 4 * q;
+      // (rows shorter than a piece end in the last 16 bytes: one run more is met with care)
+      const bool inside = n0 + COLS + (MODE == kCut ? T::PE : 0) <= A.out;
+      u32x4 w[F][TILES];
+      if (own >= 0) {
+        const uint8_t *from = wb + n0 * A.rank * T::ES;
+        if (inside && MODE != kSingle) {
+#pragma unroll
+          for (int f = 0; f < F; ++f)
+#pragma unroll
+            for (int j = 0; j < TILES; ++j) w[f][j] = ld_frag(from + j * tile_bytes + at_w[f]);
+        } else {
+#pragma unroll
+          for (int f = 0; f < F; ++f)
+#pragma unroll
+            for (int j = 0; j < TILES; ++j) {
+              const int64_t col = n0 + 16 * j + i;
+              const int r0 = X::rank0(f, q);
+              const uint8_t *p = wb + ((col < A.out ? col : A.out - 1) * A.rank + (r0 < A.rank ? r0 : 0)) * T::ES;
+              w[f][j] = settle_inside<DT, MODE>(ld_inside<DT, MODE>(p, w_last, A.rank - r0), p, w_last, A.rank - r0);
+            }
+        }
+      }
+      Quad<DT> out[TILES];
+#pragma unroll
+      for (int j = 0; j < TILES; ++j) out[j] = Quad<DT>{};
+      if (A.base && wanted) {
+        const uint8_t *from = base_row + n0 * T::ES;
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) out[j].load(from + 16 * j * T::ES, left - 16 * j, inside);
+      }
+      if (own >= 0) {
+        if (!have_u) {  // (once, when the first weights are under way)
+          const uint8_t *u_last = reinterpret_cast<const uint8_t *>(A.u + A.tokens * A.rank - 4);
+          const float *up = A.u + row * A.rank;
+          X::u_frags(uf, A.rank, q, [&](float(&v)[T::PE], int r, int rest) {
+#pragma unroll
+            for (int e = 0; e < T::PE; ++e) v[e] = 0.0f;
+#pragma unroll 2
+            for (int k = 0; k < A.splits; ++k) {
+#pragma unroll
+              for (int h = 0; h < T::PE; h += 4) {
+                const uint8_t *p = reinterpret_cast<const uint8_t *>(up + k * A.part + (rest > h ? r + h : 0));
+                const uint8_t *end = u_last + k * A.part * 4;
+                const u32x4 g = settle_inside<kF32, MODE>(ld_inside<kF32, MODE>(p, end, rest - h), p, end, rest - h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[h + e] += bits_f32(g[e]);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < T::PE; ++e) v[e] *= s;
+          });
+          have_u = true;
+        }
+        if (!full && inside && MODE != kSingle) {
+#pragma unroll
+          for (int f = 0; f < F; ++f)
+#pragma unroll
+            for (int j = 0; j < TILES; ++j) w[f][j] = only<DT>(w[f][j], A.rank - X::rank0(f, q));
+        }
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+          f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+          for (int f = 0; f < X::UF; ++f) acc = mma<DT>(w[f % F][j], uf[f], acc);
+          out[j].add(acc);
+        }
+      }
+      if (wanted && (own >= 0 || A.base != A.y)) {
+        uint8_t *to = y_row + n0 * T::ES;
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) out[j].store(to + 16 * j * T::ES, left - 16 * j, inside);
+      }
+    }
+    if (out_u && wanted)
+      for (int r = wave * 4 + q; r < A.rank; r += 4 * kFewWaves)
+        A.u_out[row * A.rank + r] = own >= 0 ? parts_sum(A.u + row * A.rank + r, A.part, A.splits) : 0.0f;
+  }
+}
+
+// Few rows: the weights' reading is all there is.
+// (A's rows are reached by 32-bit distances.)
+bool few_rows(const AdapterLaunch &L) { return L.tokens <= 256 && L.rank * L.in < (int64_t)1 << 29; }
+
+// Parts of the long dimension, for about 768 workgroups, each wave with 512 bytes or more of a row.
+int few_splits(const AdapterLaunch &L) {
+  const int64_t most = L.adapters < L.tokens ? L.adapters : L.tokens;
+  const int64_t useful = (L.in * (L.dtype == kBF16 ? 2 : 4) + 512 * kFewWaves - 1) / (512 * kFewWaves);
+  int64_t s = most > 0 ? 512 / most : 1;
+  if (s > useful) s = useful;
+  if (s > 4) s = 4;
+  return s < 1 ? 1 : (int)s;
+}
+
+template <int DT>
+hipError_t launch_few(const AdapterLaunch &L, hipStream_t stream) {
+  const int cols = 16 * few_tiles((L.rank + 15) / 16);
+  const int64_t most = L.adapters < L.tokens ? L.adapters : L.tokens;
+  const int64_t useful = ((L.out + cols - 1) / cols + kFewWaves - 1) / kFewWaves;
+  int64_t parts = 2048 / most;
+  if (parts > useful) parts = useful;
+  if (parts < 1) parts = 1;
+  const int splits = few_splits(L), mode = piece_mode(DT, L.tokens, L.in, L.out, L.rank);
+  float *u = splits == 1 && L.u ? L.u : L.workspace;
+  FewArgs A{static_cast<const uint8_t *>(L.x), static_cast<const uint8_t *>(L.a), static_cast<const uint8_t *>(L.b), L.ids,
+            L.scale, static_cast<const uint8_t *>(L.base), static_cast<uint8_t *>(L.y), u, L.u, L.tokens, L.in, L.out, L.ldx,
+            L.ld_base, L.ldy, L.tokens * L.rank, L.adapters, L.rank, splits, (int)parts};
+  // (an odd number of rows: the parts of one go to all XCDs in turn)
+  by_rank_and_mode(L.rank, mode, [&](auto rt, auto m) {
+    adapter_few_u_kernel<DT, decltype(rt)::value, decltype(m)::value>
+        <<<dim3((unsigned)L.tokens | 1, (unsigned)splits), 64 * kFewWaves, 0, stream>>>(A);
+  });
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  by_rank_and_mode(L.rank, mode, [&](auto rt, auto m) {
+    adapter_few_y_kernel<DT, decltype(rt)::value, decltype(m)::value>
+        <<<dim3((unsigned)L.tokens | 1, (unsigned)parts), 64 * kFewWaves, 0, stream>>>(A);
+  });
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_many(const AdapterLaunch &L, hipStream_t stream) {
+  const int splits = shrink_splits(L.tokens, L.in), mode = piece_mode(DT, L.tokens, L.in, L.out, L.rank);
+  float *u = splits == 1 && L.u ? L.u : L.workspace;
   const int64_t part = L.tokens * L.rank;
   ShrinkArgs S{static_cast<const uint8_t *>(L.x), static_cast<const uint8_t *>(L.a), L.ids, nullptr, u, L.tokens, L.ldx,
                L.in, part, L.adapters, L.rank, splits, shrink_slots(L.tokens, L.adapters, splits),
                window_count(L.tokens)};
-  hipError_t e = launch_shrink<false>(L.dtype, S, PlanArgs{}, stream);
+  const hipError_t e = launch_shrink<DT, false>(S, PlanArgs{}, mode, stream);
   if (e != hipSuccess) return e;
   ExpandArgs E{u, static_cast<const uint8_t *>(L.b), L.ids, L.scale, static_cast<const uint8_t *>(L.base),
                static_cast<uint8_t *>(L.y), u == L.u ? nullptr : L.u, L.tokens, L.out, L.ld_base, L.ldy, part,
                L.adapters, L.rank, splits};
-  return launch_expand<false>(L.dtype, E, stream);
+  return launch_expand<DT, false>(E, mode, stream);
+}
+
+}  // namespace
+
+int64_t adapter_workspace(const AdapterLaunch &L) {
+  return L.tokens * L.rank * (few_rows(L) ? few_splits(L) : shrink_splits(L.tokens, L.in));
+}
+
+hipError_t launch_adapter(const AdapterLaunch &L, hipStream_t stream) {
+  if (few_rows(L)) return L.dtype == kBF16 ? launch_few<kBF16>(L, stream) : launch_few<kF32>(L, stream);
+  return L.dtype == kBF16 ? launch_many<kBF16>(L, stream) : launch_many<kF32>(L, stream);
 }
 
 }  // namespace mxfp4

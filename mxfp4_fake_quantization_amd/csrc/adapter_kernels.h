@@ -27,7 +27,7 @@ struct AdapterLaunch {
   float *u;               // [tokens, rank] or NULL
   float *workspace;       // adapter_workspace floats
 };
-int64_t adapter_workspace(int64_t tokens, int64_t in, int64_t out, int rank, int adapters, int dtype);
+int64_t adapter_workspace(const AdapterLaunch &L);  // by its sizes alone
 hipError_t launch_adapter(const AdapterLaunch &L, hipStream_t stream);
 
 struct AdapterBwdLaunch {

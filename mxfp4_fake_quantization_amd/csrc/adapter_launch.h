@@ -54,9 +54,9 @@ __device__ void plan_rows(const PlanArgs &P, const int32_t *ids, int64_t tokens,
   const int64_t part = (tokens + 64 * WAVES - 1) / (64 * WAVES) * 64;
   const int64_t lo = wave * part, hi = lo + part < tokens ? lo + part : tokens;
   int32_t *mine = cnt + wave * adapters;
-  // (8 steps' ids are loaded at once: one at a time, a wave waits for memory at every step
+  // (32 steps' ids are loaded at once: one at a time, a wave waits for memory at every step
   // and 16384 tokens took 44 us, longer than the products beside it)
-  constexpr int AHEAD = 8;
+  constexpr int AHEAD = 32;
   auto load_ids = [&](int64_t base, int(&id)[AHEAD]) {
 #pragma unroll
     for (int s = 0; s < AHEAD; ++s) {
@@ -115,6 +115,7 @@ __device__ void plan_rows(const PlanArgs &P, const int32_t *ids, int64_t tokens,
     load_ids(base, id);
 #pragma unroll
     for (int s = 0; s < AHEAD; ++s) {
+      if (base + 64 * s >= hi) break;
       uint64_t same = __ballot(id[s] >= 0);
       for (int b = 0; b < P.bits; ++b) {
         const uint64_t on = __ballot((id[s] >> b) & 1);
@@ -158,7 +159,7 @@ constexpr int kBlockBytes = 256, kPieces = kBlockBytes / 16;
 
 __device__ __forceinline__ int piece_at(int row, int piece) { return row * kPieces + (piece ^ (row & 15)); }
 
-template <int DT, int RT, bool ACROSS>
+template <int DT, int RT, bool ACROSS, int MODE>
 __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink_kernel(ShrinkArgs A, PlanArgs P) {
   using T = Tile<DT>;
   constexpr int BK = kBlockBytes / T::ES;        // elements of a block
@@ -210,22 +211,22 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink_kernel(ShrinkAr
     for (int j = 0; j < XP; ++j) {
       const int r = tid / kPieces + j * (kShrinkThreads / kPieces);
       const int to = __builtin_amdgcn_ds_bpermute((r < n ? r : n - 1) << 2, line);
-      xrow[j] = A.x + ((row0 + to) * A.ldx + T::PE * (tid % kPieces)) * T::ES;
+      xrow[j] = A.x + (row0 + to) * A.ldx * T::ES;
     }
+    const uint8_t *w_last = w + A.K * A.rank * T::ES - 16;
     struct Stage {
       u32x4 x[XP], w[WP][WN];
     };
     Stage s0, s1;  // blocks on their way
-    // Block blk; WHOLE: it lies inside the rows, and no load hangs on a condition (the
-    // compiler then waits for the loads it needs, not for all that are under way).
+    // Block blk; WHOLE: it lies inside the rows.  No load hangs on a condition (but for
+    // kSingle), so the compiler waits for the loads it needs, not for all under way.
     auto load = [&](Stage &S, int64_t blk, auto whole) {
       constexpr bool WHOLE = decltype(whole)::value;
       const int64_t k0 = blk * BK;
+      const RowPiece<DT, MODE> xp(k0 + T::PE * (tid % kPieces), A.K);
 #pragma unroll
-      for (int j = 0; j < XP; ++j) {
-        const uint8_t *p = xrow[j] + k0 * T::ES;
-        S.x[j] = WHOLE ? ld_frag(p) : ld_frag_n<DT>(p, A.K - k0 - T::PE * (tid % kPieces));
-      }
+      for (int j = 0; j < XP; ++j)
+        S.x[j] = WHOLE ? ld_frag(xrow[j] + (k0 + T::PE * (tid % kPieces)) * T::ES) : xp.load(xrow[j]);
 #pragma unroll
       for (int j = 0; j < WP; ++j) {
         const int e = tid + j * kShrinkThreads;
@@ -233,21 +234,21 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink_kernel(ShrinkAr
           const int t = WT % kShrinkThreads == 0 || e < WT ? e : WT - 1;
           const int64_t k = k0 + T::PE * (t % kPieces);
           const int r = T::PE * (t / kPieces);
-          const uint8_t *p = w + (k * A.rank + r) * T::ES;
 #pragma unroll
           for (int v = 0; v < WN; ++v) {
-            if constexpr (WHOLE) {
-              S.w[j][v] = ld_frag(r < A.rank ? p + v * A.rank * T::ES : w);
+            if constexpr (WHOLE) {  // (ranks past the last hold anything)
+              S.w[j][v] = ld_frag(w + ((k + v) * A.rank + (r < A.rank ? r : 0)) * T::ES);
             } else {
-              S.w[j][v] = u32x4{0, 0, 0, 0};
-              if (k + v < A.K && r < A.rank) S.w[j][v] = ld_frag_n<DT>(p + v * A.rank * T::ES, A.rank - r);
+              const uint8_t *p = w + ((k + v < A.K ? k + v : A.K - 1) * A.rank + (r < A.rank ? r : 0)) * T::ES;
+              const u32x4 t = settle_inside<DT, MODE>(ld_inside<DT, MODE>(p, w_last, A.rank - r), p, w_last, A.rank - r);
+              S.w[j][v] = k + v < A.K ? t : u32x4{0, 0, 0, 0};
             }
           }
         } else {
           const int r = e / kPieces;  // (WT is a multiple of the threads)
+          const uint8_t *row = w + (r < A.rank ? r : A.rank - 1) * A.K * T::ES;
           const int64_t k = k0 + T::PE * (e % kPieces);
-          const uint8_t *p = w + ((r < A.rank ? r : A.rank - 1) * A.K + k) * T::ES;
-          S.w[j][0] = WHOLE ? ld_frag(p) : ld_frag_n<DT>(p, A.K - k);
+          S.w[j][0] = WHOLE ? ld_frag(row + k * T::ES) : RowPiece<DT, MODE>(k, A.K).load(row);
         }
       }
     };
@@ -286,9 +287,9 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink_kernel(ShrinkAr
     // channels at a time otherwise.
     using Yes = std::integral_constant<bool, true>;
     using No = std::integral_constant<bool, false>;
-    // ranks that are no whole pieces: the squares of W are guarded, block by block
-    const bool squares = !ACROSS || A.rank % T::PE == 0;
-    const int64_t full = !squares ? lo : hi * BK <= A.K ? hi : hi - 1;
+    // blocks inside the rows; (ACROSS) and whose pieces of short rows end inside W
+    const int64_t inside = (A.K - (ACROSS && MODE == kCut ? T::PE : 0)) / BK;
+    const int64_t full = hi <= inside ? hi : inside > lo ? inside : lo;
     const int64_t count = full - lo;
     if (count > 0) {
       int64_t next = lo + (pair / A.splits * 5) % count;
@@ -355,10 +356,10 @@ __device__ __forceinline__ float parts_sum(const float *u, int64_t part, int spl
 // the result of its own one, so that no other adapter's values (an infinity, say) reach it.
 constexpr int kExpandTiles = 4, kExpandRows = 16 * kExpandTiles;
 
-template <int DT, int NF, bool ACROSS>
+template <int DT, int NF, bool ACROSS, int MODE>
 __global__ __launch_bounds__(64 * kExpandWaves, NF <= 1 ? 3 : 2) void adapter_expand_kernel(ExpandArgs A, int chunks) {
   using T = Tile<DT>;
-  using X = Expand<DT, NF, ACROSS>;
+  using X = Expand<DT, NF, ACROSS, MODE>;
   constexpr int TILES = kExpandTiles;
   __shared__ u32x4 us[TILES][X::UF][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
@@ -379,52 +380,60 @@ __global__ __launch_bounds__(64 * kExpandWaves, NF <= 1 ? 3 : 2) void adapter_ex
 #pragma unroll
     for (int j = 0; j < TILES; ++j)
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        out[j][v] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a1 *>(from + (16 * j + v) * A.ld_base * T::ES + mine_at));
-  } else {
+      for (int v = 0; v < 4; ++v) out[j][v] = ld_frag_nt(from + (16 * j + v) * A.ld_base * T::ES + mine_at);
+  } else if (A.base && mine) {  // rows and columns past the last hold anything
+    const RowPiece<DT, MODE> piece(col, A.N);
 #pragma unroll
     for (int j = 0; j < TILES; ++j)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int r = 16 * j + 4 * q + v;
-        out[j][v] = u32x4{0, 0, 0, 0};
-        if (A.base && r < rows) out[j][v] = ld_frag_n<DT>(A.base + ((row0 + r) * A.ld_base + col) * T::ES, A.N - col);
+        out[j][v] = piece.raw(A.base + (row0 + (r < rows ? r : rows - 1)) * A.ld_base * T::ES);
       }
+#pragma unroll
+    for (int j = 0; j < TILES; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) out[j][v] = piece.settled(out[j][v]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < TILES; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) out[j][v] = u32x4{0, 0, 0, 0};
   }
   const uint64_t live = ~0ull >> (64 - rows);
   uint64_t rem = __ballot(id >= 0);
   X W;
   auto weights = [&](int a) {
-    if (mine) W.load(A.w + (int64_t)a * A.N * A.rank * T::ES, A.N, A.rank, n0, lane);
+    if (mine) W.load({A.w + (int64_t)a * A.N * A.rank * T::ES, A.N, n0, A.rank, lane});
   };
   int a = 0;
   if (rem) {
     a = __builtin_amdgcn_readlane(id, __builtin_ctzll(rem));
     weights(a);
-    // the row's scale goes into u
-    const int r_u = 16 * wave + i;
-    const int own = __builtin_amdgcn_ds_bpermute(r_u << 2, id);
     if (wave < TILES) {
+      // fragments of the rows' own u, the row's scale in it; 0 for a row without an adapter
+      const int r_u = 16 * wave + i;
+      const int own = __builtin_amdgcn_ds_bpermute(r_u << 2, id);
+      const float s = own < 0 ? 0.0f : A.scale ? A.scale[own] : 1.0f;
+      const float *up = A.u + (row0 + (r_u < rows ? r_u : rows - 1)) * A.rank;
+      const uint8_t *u_last = reinterpret_cast<const uint8_t *>(A.u + A.tokens * A.rank - 4);
       u32x4 uf[X::UF];
       X::u_frags(uf, A.rank, q, [&](float(&v)[T::PE], int r, int left) {
-      const bool whole = A.rank % T::PE == 0;
-      const float s = A.scale && own >= 0 ? A.scale[own] : 1.0f;
 #pragma unroll
-      for (int e = 0; e < T::PE; ++e) v[e] = 0.0f;
-      if (own < 0 || left <= 0) return;
-      const float *up = A.u + (row0 + r_u) * A.rank + r;
-      for (int k = 0; k < A.splits; ++k) {
+        for (int e = 0; e < T::PE; ++e) v[e] = 0.0f;
+        for (int k = 0; k < A.splits; ++k) {
 #pragma unroll
-        for (int h = 0; h < T::PE; h += 4) {
-          const uint8_t *p = reinterpret_cast<const uint8_t *>(up + k * A.part + h);
-          const u32x4 t = whole ? ld_frag(p) : ld_frag_n<kF32>(p, left - h);
+          for (int h = 0; h < T::PE; h += 4) {
+            const uint8_t *p = reinterpret_cast<const uint8_t *>(up + k * A.part + (left > h ? r + h : 0));
+            const uint8_t *end = u_last + k * A.part * 4;
+            const u32x4 t = settle_inside<kF32, MODE>(ld_inside<kF32, MODE>(p, end, left - h), p, end, left - h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[h + e] += bits_f32(t[e]);
+            for (int e = 0; e < 4; ++e) v[h + e] += bits_f32(t[e]);
+          }
         }
-      }
 #pragma unroll
-      for (int e = 0; e < T::PE; ++e) v[e] *= s;
-    });
+        for (int e = 0; e < T::PE; ++e) v[e] = own < 0 ? 0.0f : v[e] * s;
+      });
 #pragma unroll
       for (int f = 0; f < X::UF; ++f) us[wave][f][lane] = uf[f];
     }
@@ -440,6 +449,7 @@ __global__ __launch_bounds__(64 * kExpandWaves, NF <= 1 ? 3 : 2) void adapter_ex
   while (rem) {
     const uint64_t match = __ballot(id == a);
     rem &= ~match;
+    W.settle({A.w + (int64_t)a * A.N * A.rank * T::ES, A.N, n0, A.rank, lane});
 #pragma unroll
     for (int j = 0; j < TILES; ++j) {
       const uint32_t here = (uint32_t)(match >> (16 * j)) & 0xFFFFu;
@@ -510,42 +520,51 @@ inline int shrink_slots(int64_t tokens, int adapters, int splits) {
   return s < 1 ? 1 : (int)s;
 }
 
+// How the rows' pieces are met (adapter_device.h).
+inline int piece_mode(int dtype, int64_t tokens, int64_t in, int64_t out, int rank) {
+  const int pe = dtype == kBF16 ? 8 : 4;
+  if (in % pe == 0 && out % pe == 0 && rank % pe == 0) return kExact;
+  return in < pe || out < pe || tokens * rank < 4 ? kSingle : kCut;
+}
+
+// Calls f(rank tiles, mode) with both as constants.  Problems of kSingle are tiny:
+// one form of the kernels serves all ranks.
+template <typename F>
+void by_rank_and_mode(int rank, int mode, F f) {
+  using std::integral_constant;
+  const int rt = (rank + 15) / 16;
+  auto ranks = [&](auto m) {
+    if (rt <= 1) f(integral_constant<int, 1>(), m);
+    else if (rt <= 2) f(integral_constant<int, 2>(), m);
+    else if (rt <= 4) f(integral_constant<int, 4>(), m);
+    else f(integral_constant<int, 8>(), m);
+  };
+  if (mode == kExact) ranks(integral_constant<int, kExact>());
+  else if (mode == kCut) ranks(integral_constant<int, kCut>());
+  else f(integral_constant<int, 8>(), integral_constant<int, kSingle>());
+}
+
 template <int DT, bool ACROSS>
-hipError_t launch_shrink_dt(const ShrinkArgs &A, const PlanArgs &P, hipStream_t stream) {
-  const int rt = (A.rank + 15) / 16;
+hipError_t launch_shrink(const ShrinkArgs &A, const PlanArgs &P, int mode, hipStream_t stream) {
   const int64_t pairs = (int64_t)A.windows * A.splits;
   const dim3 grid((unsigned)((pairs + 7) / 8 * 8 * A.slots + (P.order ? 8 : 0)));
-  const int th = kShrinkThreads;
-  if (rt <= 1) adapter_shrink_kernel<DT, 1, ACROSS><<<grid, th, 0, stream>>>(A, P);
-  else if (rt <= 2) adapter_shrink_kernel<DT, 2, ACROSS><<<grid, th, 0, stream>>>(A, P);
-  else if (rt <= 4) adapter_shrink_kernel<DT, 4, ACROSS><<<grid, th, 0, stream>>>(A, P);
-  else adapter_shrink_kernel<DT, 8, ACROSS><<<grid, th, 0, stream>>>(A, P);
+  by_rank_and_mode(A.rank, mode, [&](auto rt, auto m) {
+    adapter_shrink_kernel<DT, decltype(rt)::value, ACROSS, decltype(m)::value><<<grid, kShrinkThreads, 0, stream>>>(A, P);
+  });
   return hipGetLastError();
-}
-
-template <bool ACROSS>
-hipError_t launch_shrink(int dtype, const ShrinkArgs &A, const PlanArgs &P, hipStream_t stream) {
-  return dtype == kBF16 ? launch_shrink_dt<kBF16, ACROSS>(A, P, stream) : launch_shrink_dt<kF32, ACROSS>(A, P, stream);
 }
 
 template <int DT, bool ACROSS>
-hipError_t launch_expand_dt(const ExpandArgs &A, hipStream_t stream) {
+hipError_t launch_expand(const ExpandArgs &A, int mode, hipStream_t stream) {
   const int64_t windows = (A.tokens + kExpandRows - 1) / kExpandRows;
-  const int64_t cols = kExpandWaves * Expand<DT, 1, ACROSS>::COLS;
+  const int64_t cols = kExpandWaves * 16 * Tile<DT>::PE;
   const int chunks = (int)((A.N + cols - 1) / cols);
-  const int rt = (A.rank + 15) / 16;
   const dim3 grid((unsigned)(windows * chunks));
-  const int th = 64 * kExpandWaves;
-  if (rt <= 1) adapter_expand_kernel<DT, frag_count<DT>(1), ACROSS><<<grid, th, 0, stream>>>(A, chunks);
-  else if (rt <= 2) adapter_expand_kernel<DT, frag_count<DT>(2), ACROSS><<<grid, th, 0, stream>>>(A, chunks);
-  else if (rt <= 4) adapter_expand_kernel<DT, frag_count<DT>(4), ACROSS><<<grid, th, 0, stream>>>(A, chunks);
-  else adapter_expand_kernel<DT, frag_count<DT>(8), ACROSS><<<grid, th, 0, stream>>>(A, chunks);
+  by_rank_and_mode(A.rank, mode, [&](auto rt, auto m) {
+    adapter_expand_kernel<DT, frag_count<DT>(decltype(rt)::value), ACROSS, decltype(m)::value>
+        <<<grid, 64 * kExpandWaves, 0, stream>>>(A, chunks);
+  });
   return hipGetLastError();
-}
-
-template <bool ACROSS>
-hipError_t launch_expand(int dtype, const ExpandArgs &A, hipStream_t stream) {
-  return dtype == kBF16 ? launch_expand_dt<kBF16, ACROSS>(A, stream) : launch_expand_dt<kF32, ACROSS>(A, stream);
 }
 
 }  // namespace

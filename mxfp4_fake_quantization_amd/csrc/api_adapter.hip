@@ -90,8 +90,14 @@ extern "C" {
 
 int64_t mxfp4_adapter_workspace(const mxfp4_adapter_t *desc) {
   if (check_adapter(desc) != MXFP4_OK) return -1;
-  return 4 * mxfp4::adapter_workspace(desc->tokens, desc->in_features, desc->out_features, desc->rank, desc->adapters,
-                                      desc->dtype);
+  mxfp4::AdapterLaunch L{};
+  L.dtype = desc->dtype;
+  L.rank = desc->rank;
+  L.adapters = desc->adapters;
+  L.tokens = desc->tokens;
+  L.in = desc->in_features;
+  L.out = desc->out_features;
+  return 4 * mxfp4::adapter_workspace(L);
 }
 
 mxfp4_status_t mxfp4_adapter_fwd(const mxfp4_adapter_t *desc, const void *x, int64_t ldx, const void *a, const void *b,

@@ -123,11 +123,13 @@ def test_abi_descriptors(lib, bad, status):
 
 def test_abi_forward(lib):
     assert fwd(lib, desc(tokens=0), x=None, a=None, b=None, y=None, ws=None, nbytes=0) == OK
-    for k in ("x", "a", "b", "y", "ws"):
+    for k in ("x", "a", "b", "y"):
         assert fwd(lib, desc(), **{k: None}) == EINVAL, k
+    many = desc(tokens=4000)                                      # few rows need no workspace
+    assert fwd(lib, many, ws=None) == EINVAL
     assert fwd(lib, desc(), x=A[0] + 1) == EINVAL
     assert fwd(lib, desc(dtype=F32), x=A[0] + 2) == EINVAL
-    assert fwd(lib, desc(), ws=A[4] + 8) == EINVAL
+    assert fwd(lib, many, ws=A[4] + 8) == EINVAL
     assert fwd(lib, desc(), ldx=63) == EINVAL
     assert fwd(lib, desc(), ldy=95) == EINVAL
     assert fwd(lib, desc(), base=A[5], ldb=95) == EINVAL
@@ -135,9 +137,9 @@ def test_abi_forward(lib):
     assert fwd(lib, desc(), ids=A[5] + 2) == EINVAL
     assert fwd(lib, desc(), u=A[5] + 2) == EINVAL
     assert fwd(lib, desc(), scale=A[5] + 2) == EINVAL
-    need = lib.mxfp4_adapter_workspace(desc())
-    assert need >= 4 * 4 * 8
-    assert fwd(lib, desc(), nbytes=need - 1) == EINVAL
+    need = lib.mxfp4_adapter_workspace(many)
+    assert need >= 4 * 4000 * 8
+    assert fwd(lib, many, nbytes=need - 1) == EINVAL
     for k in ("x", "a", "b"):                                     # y over an input
         assert fwd(lib, desc(), **{k: A[3]}) == EINVAL, k
     assert fwd(lib, desc(), u=A[4]) == EINVAL                     # u over the workspace
