@@ -291,6 +291,7 @@ hipError_t backward(const AdapterBwdLaunch &L, hipStream_t stream) {
     P.first = reinterpret_cast<int32_t *>(ws + S.first);
     P.pieces = reinterpret_cast<int4 *>(ws + S.pieces);
     P.rows = S.rows;
+    P.blocks = plan_blocks(L.tokens);
     while ((1 << P.bits) < L.adapters) ++P.bits;
   }
   const int64_t part = L.tokens * L.rank;

@@ -36,52 +36,83 @@ struct ExpandArgs {
 //
 // The weight gradients sum over an adapter's rows, wherever they are: a stable
 // counting sort of the tokens by adapter, cut into pieces of at most `rows` rows
-// of one adapter.  One workgroup does it while the others of the same launch
-// compute du.
+// of one adapter.  It runs in workgroups of its own beside those that compute du, each
+// of which counts all tokens and places a part of them (one workgroup for all took 34 us
+// for 16384 tokens, longer than du).
 
 struct PlanArgs {
   int32_t *order;   // [tokens] rows, sorted by adapter
   int32_t *first;   // [adapters + 1] each adapter's first piece, and their number
   int4 *pieces;     // adapter, first place in order, rows
   int rows, bits;   // bits of an adapter's number
+  int blocks;       // workgroups
 };
 
+constexpr int kPlanStep = 256;  // tokens of a wave's step: four a lane
+
+inline int plan_blocks(int64_t tokens) {
+  const int64_t b = (tokens + 1023) / 1024;
+  return b > 64 ? 64 : b < 1 ? 1 : (int)b;
+}
+
+// lds: (WAVES + 2) * adapters numbers.
 template <int WAVES>
-__device__ void plan_rows(const PlanArgs &P, const int32_t *ids, int64_t tokens, int adapters, int32_t *cnt) {
+__device__ void plan_rows(const PlanArgs &P, const int32_t *ids, int64_t tokens, int adapters, int32_t *lds, int block) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e < WAVES * adapters; e += 64 * WAVES) cnt[e] = 0;
+  int32_t *total = lds, *before = lds + adapters, *cnt = lds + 2 * adapters;
+  for (int e = tid; e < (WAVES + 2) * adapters; e += 64 * WAVES) lds[e] = 0;
   __syncthreads();
-  const int64_t part = (tokens + 64 * WAVES - 1) / (64 * WAVES) * 64;
-  const int64_t lo = wave * part, hi = lo + part < tokens ? lo + part : tokens;
-  int32_t *mine = cnt + wave * adapters;
-  // (32 steps' ids are loaded at once: one at a time, a wave waits for memory at every step
-  // and 16384 tokens took 44 us, longer than the products beside it)
-  constexpr int AHEAD = 32;
-  auto load_ids = [&](int64_t base, int(&id)[AHEAD]) {
-#pragma unroll
-    for (int s = 0; s < AHEAD; ++s) {
-      const int64_t i = base + 64 * s + lane;
-      const int v = ids ? ids[i < hi ? i : hi - 1] : 0;
-      id[s] = i < hi && v >= 0 && v < adapters ? v : -1;
-    }
-  };
-  for (int64_t base = lo; base < hi; base += 64 * AHEAD) {
-    int id[AHEAD];
-    load_ids(base, id);
+  const int64_t chunk = (tokens + (int64_t)P.blocks * kPlanStep - 1) / ((int64_t)P.blocks * kPlanStep) * kPlanStep;
+  const int64_t lo = block * chunk < tokens ? block * chunk : tokens, hi = lo + chunk < tokens ? lo + chunk : tokens;
+  // All tokens, a step of 256 a wave, two steps' loads at a time; a step of one adapter, as
+  // most are, is one addition.  (Integer sums: any order.)
+  constexpr int AHEAD = 2;
+  for (int64_t base = wave * kPlanStep; base < tokens; base += AHEAD * WAVES * kPlanStep) {
+    int32_t id[AHEAD][4];
 #pragma unroll
     for (int s = 0; s < AHEAD; ++s)
-      if (id[s] >= 0) atomicAdd(&mine[id[s]], 1);  // a count: the order of the additions does not matter
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t i = base + s * WAVES * kPlanStep + 4 * lane + e;
+        const int v = ids ? ids[i < tokens ? i : tokens - 1] : 0;
+        id[s][e] = i < tokens && v >= 0 && v < adapters ? v : -1;
+      }
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s) {
+      const bool early = base + s * WAVES * kPlanStep < lo;  // (lo is a multiple of the step)
+      const int one = __builtin_amdgcn_readfirstlane(id[s][0]);
+      const bool alike = id[s][0] == one && id[s][1] == one && id[s][2] == one && id[s][3] == one;
+      if (__ballot(alike) == ~0ull) {
+        if (lane == 0 && one >= 0) {
+          atomicAdd(&total[one], kPlanStep);
+          if (early) atomicAdd(&before[one], kPlanStep);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (id[s][e] >= 0) {
+            atomicAdd(&total[id[s][e]], 1);
+            if (early) atomicAdd(&before[id[s][e]], 1);
+          }
+      }
+    }
+  }
+  // this workgroup's tokens by wave
+  const int64_t part = chunk / WAVES, wlo = lo + wave * part < hi ? lo + wave * part : hi;
+  const int64_t whi = wlo + part < hi ? wlo + part : hi;
+  int32_t *mine = cnt + wave * adapters;
+  for (int64_t i = wlo + lane; i < whi; i += 64) {
+    const int id = row_adapter(ids, i, adapters);
+    if (id >= 0) atomicAdd(&mine[id], 1);
   }
   __syncthreads();
   if (wave == 0) {  // first places and pieces, 64 adapters at a time
     int32_t at = 0, piece = 0;
     for (int e0 = 0; e0 < adapters; e0 += 64) {
       const int e = e0 + lane;
-      int32_t total = 0;
-      if (e < adapters)
-        for (int w = 0; w < WAVES; ++w) total += cnt[w * adapters + e];
-      const int32_t np = (total + P.rows - 1) / P.rows;
-      int32_t st = total, sp = np;
+      const int32_t n = e < adapters ? total[e] : 0;
+      const int32_t np = (n + P.rows - 1) / P.rows;
+      int32_t st = n, sp = np;
       for (int d = 1; d < 64; d <<= 1) {
         const int32_t ot = __shfl_up(st, d), op = __shfl_up(sp, d);
         if (lane >= d) {
@@ -89,48 +120,46 @@ __device__ void plan_rows(const PlanArgs &P, const int32_t *ids, int64_t tokens,
           sp += op;
         }
       }
-      int32_t start = at + st - total;
-      const int32_t fp = piece + sp - np;
+      const int32_t start = at + st - n, fp = piece + sp - np;
       at += __shfl(st, 63);
       piece += __shfl(sp, 63);
       if (e < adapters) {
-        P.first[e] = fp;
-        for (int p = 0; p < np; ++p) {
-          const int32_t left = total - p * P.rows;
-          P.pieces[fp + p] = make_int4(e, start + p * P.rows, left < P.rows ? left : P.rows, 0);
+        if (block == 0) {
+          P.first[e] = fp;
+          for (int p = 0; p < np; ++p) {
+            const int32_t left = n - p * P.rows;
+            P.pieces[fp + p] = make_int4(e, start + p * P.rows, left < P.rows ? left : P.rows, 0);
+          }
         }
+        int32_t here = start + before[e];
         for (int w = 0; w < WAVES; ++w) {
           const int32_t c = cnt[w * adapters + e];
-          cnt[w * adapters + e] = start;
-          start += c;
+          cnt[w * adapters + e] = here;
+          here += c;
         }
       }
     }
-    if (lane == 0) P.first[adapters] = piece;
+    if (lane == 0 && block == 0) P.first[adapters] = piece;
   }
   __syncthreads();
   // Every lane of a wave takes part in the ballots: the loop count is the wave's.
-  for (int64_t base = lo; base < hi; base += 64 * AHEAD) {
-    int id[AHEAD];
-    load_ids(base, id);
-#pragma unroll
-    for (int s = 0; s < AHEAD; ++s) {
-      if (base + 64 * s >= hi) break;
-      uint64_t same = __ballot(id[s] >= 0);
-      for (int b = 0; b < P.bits; ++b) {
-        const uint64_t on = __ballot((id[s] >> b) & 1);
-        same &= (id[s] >> b) & 1 ? on : ~on;
-      }
-      if (id[s] >= 0) {
-        const int32_t at = mine[id[s]];
-        P.order[at + __popcll(same & ((1ull << lane) - 1))] = (int32_t)(base + 64 * s + lane);
-        // the group's last lane moves the count on (a wave's LDS operations keep
-        // their order: the reads above come first)
-        if ((same >> lane) == 1ull) mine[id[s]] = at + (int32_t)__popcll(same);
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+  for (int64_t base = wlo; base < whi; base += 64) {
+    const int64_t i = base + lane;
+    const int id = i < whi ? row_adapter(ids, i, adapters) : -1;
+    uint64_t same = __ballot(id >= 0);
+    for (int b = 0; b < P.bits; ++b) {
+      const uint64_t on = __ballot((id >> b) & 1);
+      same &= (id >> b) & 1 ? on : ~on;
     }
+    if (id >= 0) {
+      const int32_t at = mine[id];
+      P.order[at + __popcll(same & ((1ull << lane) - 1))] = (int32_t)i;
+      // the group's last lane moves the count on (a wave's LDS operations keep
+      // their order: the reads above come first)
+      if ((same >> lane) == 1ull) mine[id] = at + (int32_t)__popcll(same);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -172,9 +201,10 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink_kernel(ShrinkAr
   int64_t block = blockIdx.x;
   if constexpr (ACROSS) {  // the backward pass
     if (P.order) {
-      static_assert(sizeof xs >= sizeof(int32_t) * kShrinkWaves * kAdapterMaxTrained, "the plan's counts");
-      if (block == 0) plan_rows<kShrinkWaves>(P, A.ids, A.tokens, A.adapters, reinterpret_cast<int32_t *>(xs));
-      block -= 8;  // (the others keep their XCDs)
+      static_assert(sizeof xs >= sizeof(int32_t) * (kShrinkWaves + 2) * kAdapterMaxTrained, "the plan's counts");
+      if (block < P.blocks)
+        plan_rows<kShrinkWaves>(P, A.ids, A.tokens, A.adapters, reinterpret_cast<int32_t *>(xs), (int)block);
+      block -= (P.blocks + 7) / 8 * 8;  // (the others keep their XCDs)
       if (block < 0) return;
     }
   }
@@ -547,7 +577,7 @@ void by_rank_and_mode(int rank, int mode, F f) {
 template <int DT, bool ACROSS>
 hipError_t launch_shrink(const ShrinkArgs &A, const PlanArgs &P, int mode, hipStream_t stream) {
   const int64_t pairs = (int64_t)A.windows * A.splits;
-  const dim3 grid((unsigned)((pairs + 7) / 8 * 8 * A.slots + (P.order ? 8 : 0)));
+  const dim3 grid((unsigned)((pairs + 7) / 8 * 8 * A.slots + (P.order ? (P.blocks + 7) / 8 * 8 : 0)));
   by_rank_and_mode(A.rank, mode, [&](auto rt, auto m) {
     adapter_shrink_kernel<DT, decltype(rt)::value, ACROSS, decltype(m)::value><<<grid, kShrinkThreads, 0, stream>>>(A, P);
   });
