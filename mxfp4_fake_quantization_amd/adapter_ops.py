@@ -22,7 +22,6 @@ from __future__ import annotations
 
 import math
 import struct
-from operator import attrgetter
 
 import torch
 
@@ -199,33 +198,22 @@ def mxfp4_adapter_bwd(grad_y, a, b, x=None, u=None, ids=None, scale=None, grad_x
 
 # ---- the gradient norm ----------------------------------------------------------
 
-_data_ptr, _numel, _contiguous = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
-_get_device, _get_dtype = torch.Tensor.get_device, attrgetter("dtype")
+_pack = None
 
 
-def _tensors(ts, what):
-    """Addresses, sizes and types of a list of tensors: a few C-level passes over
-    it, since a model has hundreds."""
-    if isinstance(ts, torch.Tensor):
-        raise TypeError(f"{what} is a list of tensors")
-    dtypes = list(map(_get_dtype, ts))
-    for dt in set(dtypes):
-        if dt not in _CODES:
-            raise ValueError(f"{what} must be bfloat16 or float32 tensors, got {dt}")
-    if not all(map(_contiguous, ts)):
-        raise ValueError("tensors must be contiguous")
-    return list(map(_data_ptr, ts)), list(map(_numel, ts)), dtypes
-
-
-def _devices(norm, *lists):
-    at = set()
-    for ts in lists:
-        at.update(map(_get_device, ts))
-    at.add(norm.get_device())
-    if -1 in at:
-        raise ValueError("tensors must live on the GPU (no CPU path)")
-    if at != {torch.cuda.current_device()}:
-        raise ValueError("tensors must live on the current GPU")
+def _items(grads, outs, write):
+    """mxfp4_grad_item_t of every tensor, checked, and the number of elements."""
+    global _pack
+    if _pack is None:
+        try:
+            from ._tensor_list import pack
+        except ImportError as e:
+            raise RuntimeError("_tensor_list is not built; build it with "
+                               "`python -m mxfp4_fake_quantization_amd.build`") from e
+        _pack = pack
+    if isinstance(grads, torch.Tensor) or isinstance(outs, torch.Tensor):
+        raise TypeError("grads and outs are lists of tensors")
+    return _pack(grads, outs, torch.cuda.current_device() if torch.cuda.is_available() else -1, write)
 
 
 def _norm_type(p) -> int:
@@ -249,24 +237,18 @@ def mxfp4_grad_norm_workspace(tensors: int, elements: int) -> int:
     return n
 
 
-def _items(ptrs, outs, counts, dtypes):
-    code = _CODES
-    pack = _ITEM.pack
-    return b"".join([pack(p, o, n, code[t], 0) for p, o, n, t in zip(ptrs, outs, counts, dtypes)])
-
-
 def mxfp4_grad_norm(grads, norm, norm_type=2.0, workspace=None):
     """norm (one float32 element) = the 1-, 2- or inf-norm over all elements of a
     list of gradients, summed in 64 bits.  workspace: a uint8 tensor of
     mxfp4_grad_norm_workspace bytes; allocated from torch when None."""
     order, pn = _norm_type(norm_type), _norm_out(norm)
-    ptrs, counts, dtypes = _tensors(grads, "grads")
-    _devices(norm, grads)
-    lib, n = _lib(), len(ptrs)
-    need = int(lib.mxfp4_grad_norm_workspace(n, sum(counts)))
+    items, elements = _items(grads, None, False)
+    _here(norm, workspace)
+    lib, n = _lib(), len(items) // _ITEM.size
+    need = int(lib.mxfp4_grad_norm_workspace(n, elements))
     workspace = _space(workspace, need, norm.device, "mxfp4_grad_norm")
-    _check(lib.mxfp4_grad_norm(order, n, _items(ptrs, [0] * n, counts, dtypes), pn,
-                               _ptr(workspace, "u8") if need else None, need, _stream()), "mxfp4_grad_norm")
+    _check(lib.mxfp4_grad_norm(order, n, items, pn, _ptr(workspace, "u8") if need else None, need, _stream()),
+           "mxfp4_grad_norm")
 
 
 def mxfp4_grad_clip(grads, max_norm, norm, outs=None, norm_type=2.0, compute_norm=True, workspace=None):
@@ -274,17 +256,10 @@ def mxfp4_grad_clip(grads, max_norm, norm, outs=None, norm_type=2.0, compute_nor
     ``outs``.  norm (one float32 element) receives the norm of ``grads``; without
     ``compute_norm`` it is read instead (a norm over several processes)."""
     order, pn = _norm_type(norm_type), _norm_out(norm)
-    ptrs, counts, dtypes = _tensors(grads, "grads")
-    if outs is None:
-        to = ptrs
-        _devices(norm, grads)
-    else:
-        to, sizes, types = _tensors(outs, "outs")
-        if sizes != counts or types != dtypes:
-            raise ValueError("outs must have the types and sizes of grads")
-        _devices(norm, grads, outs)
-    lib, n = _lib(), len(ptrs)
-    need = int(lib.mxfp4_grad_norm_workspace(n, sum(counts))) if compute_norm else 0
+    items, elements = _items(grads, outs, True)
+    _here(norm, workspace)
+    lib, n = _lib(), len(items) // _ITEM.size
+    need = int(lib.mxfp4_grad_norm_workspace(n, elements)) if compute_norm else 0
     workspace = _space(workspace, need, norm.device, "mxfp4_grad_clip")
-    _check(lib.mxfp4_grad_clip(order, n, _items(ptrs, to, counts, dtypes), float(max_norm), 1 if compute_norm else 0,
-                               pn, _ptr(workspace, "u8") if need else None, need, _stream()), "mxfp4_grad_clip")
+    _check(lib.mxfp4_grad_clip(order, n, items, float(max_norm), 1 if compute_norm else 0, pn,
+                               _ptr(workspace, "u8") if need else None, need, _stream()), "mxfp4_grad_clip")

@@ -6,12 +6,14 @@ Each .hip file of the library under csrc/ is compiled by hipcc for gfx950
 into _build/, then linked into mxfp4_fake_quantization_amd/libmxfp4.so.
 csrc/probe_kernels.hip (streaming probes the benchmark times next to the
 kernels; not part of the C ABI) becomes libmxfp4_probe.so.  Packed-FP32 VALU
-instructions are disabled (-packed-fp32-ops); no fast-math.
+instructions are disabled (-packed-fp32-ops); no fast-math.  csrc/tensor_list.cpp
+(host code of the binding, against torch's headers) becomes _tensor_list.so.
 """
 import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -19,6 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxfp4.so")
 PROBE_LIB = os.path.join(HERE, "libmxfp4_probe.so")
 PROBE_SOURCES = ["probe_kernels.hip"]
+LIST_SOURCE = "tensor_list.cpp"
+LIST_LIB = os.path.join(HERE, "_tensor_list.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 SOURCES = ["api.hip", "row_kernels.hip", "col_kernels.hip", "ste_kernels.hip",
@@ -39,10 +43,31 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_list() -> str:
+    """The binding's helper module: a CPython extension on torch's libraries."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = LIST_LIB + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, LIST_SOURCE), "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           f"-Wl,-rpath,{os.path.join(root, 'lib')}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {LIST_SOURCE} failed:\n{r.stderr}")
+    os.replace(tmp, LIST_LIB)
+    return LIST_LIB
+
+
 def build() -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + len(PROBE_SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + len(PROBE_SOURCES) + 1) as ex:
+        helper = ex.submit(_build_list)
         objs = list(ex.map(_compile, SOURCES + PROBE_SOURCES))
+        helper.result()
     _link(objs[len(SOURCES):], PROBE_LIB)
     return _link(objs[:len(SOURCES)], LIB)
 

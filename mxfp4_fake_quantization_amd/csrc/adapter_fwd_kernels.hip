@@ -52,16 +52,14 @@ struct FewRows {
   }
 };
 
-template <int DT, int RT, int MODE>
-__global__ __launch_bounds__(64 * kFewWaves) void adapter_few_u_kernel(FewArgs A) {
+// The rows' tiles of 16 are taken together (NT: one, or up to four), so that the weights
+// are loaded once for all of them.
+template <int DT, int RT, int MODE, int NT>
+__device__ __forceinline__ void few_u(const FewArgs &A, const FewRows &R, f32x4 (*part)[RT][64], int lane, int wave) {
   using T = Tile<DT>;
-  constexpr int U = RT <= 1 ? 8 : RT <= 4 ? 4 : 2;  // fragments of a turn, as the registers allow
-  __shared__ f32x4 part[kFewWaves][RT][64];
-  const int m = blockIdx.x;
-  if (m >= A.tokens) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
-  const FewRows R(A, m, lane);
-  if (!R.mine || R.own < 0) return;
+  // fragments of a turn, as the registers allow
+  constexpr int U = NT == 1 ? (RT <= 1 ? 8 : RT <= 4 ? 4 : 2) : RT <= 1 ? 4 : RT <= 4 ? 2 : 1;
+  const int i = lane & 15, q = lane >> 4;
   float *u = A.u + blockIdx.y * A.part;
   const uint8_t *wa = A.a + (int64_t)R.own * A.rank * A.in * T::ES;
   uint32_t at_w[RT];  // the lane's row of each 16 ranks, from the first (few_rows() bounds it)
@@ -69,53 +67,81 @@ __global__ __launch_bounds__(64 * kFewWaves) void adapter_few_u_kernel(FewArgs A
   for (int r = 0; r < RT; ++r) at_w[r] = ((16 * r + i < A.rank ? 16 * r + i : A.rank - 1) * (uint32_t)A.in + T::PE * q) * T::ES;
   const int64_t turns = A.in / (U * T::KF);
   const int first = blockIdx.y * kFewWaves + wave, step = kFewWaves * A.splits;
-  for (int t = 0; 16 * t < R.n; ++t) {
-    const int at = 16 * t + i;
-    const int64_t row_x = R.row(at);
-    const uint8_t *xp = A.x + row_x * A.ldx * T::ES;
-    f32x4 acc[RT];
+  int64_t row[NT];
+  const uint8_t *xp[NT];
+  f32x4 acc[NT][RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
-    for (int64_t turn = first; turn < turns; turn += step) {
-      u32x4 xf[U], wf[U][RT];
+  for (int t = 0; t < NT; ++t) {
+    row[t] = R.row(16 * t + i);
+    xp[t] = A.x + row[t] * A.ldx * T::ES;
 #pragma unroll
-      for (int c = 0; c < U; ++c)
+    for (int r = 0; r < RT; ++r) acc[t][r] = f32x4{0, 0, 0, 0};
+  }
+  for (int64_t turn = first; turn < turns; turn += step) {
+    u32x4 xf[NT][U], wf[U][RT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) wf[c][r] = ld_frag(wa + (turn * U + c) * T::KF * T::ES + at_w[r]);
+    for (int c = 0; c < U; ++c)
 #pragma unroll
-      for (int c = 0; c < U; ++c) xf[c] = u32x4{0, 0, 0, 0};
-      if (at < R.n) {  // (lanes without a row would cost the L1 a cycle for each 64 bytes)
+      for (int r = 0; r < RT; ++r) wf[c][r] = ld_frag(wa + (turn * U + c) * T::KF * T::ES + at_w[r]);
 #pragma unroll
-        for (int c = 0; c < U; ++c) xf[c] = ld_frag(xp + ((turn * U + c) * T::KF + T::PE * q) * T::ES);
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int c = 0; c < U; ++c) xf[t][c] = u32x4{0, 0, 0, 0};
+      if (16 * t + i < R.n) {  // (lanes without a row would cost the L1 a cycle for each 64 bytes)
+#pragma unroll
+        for (int c = 0; c < U; ++c) xf[t][c] = ld_frag(xp[t] + ((turn * U + c) * T::KF + T::PE * q) * T::ES);
       }
-#pragma unroll
-      for (int c = 0; c < U; ++c)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[r] = mma<DT>(wf[c][r], xf[c], acc[r]);
     }
-    // the rest of the row, fragment by fragment
-    for (int64_t k0 = (turns * U + first) * T::KF; k0 < A.in; k0 += step * T::KF) {
-      const RowPiece<DT, MODE> piece(k0 + T::PE * q, A.in);
-      const u32x4 xf = piece.load(xp);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) acc[r] = mma<DT>(piece.load(wa + at_w[r] - T::PE * q * T::ES), xf, acc[r]);
+    for (int c = 0; c < U; ++c)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[t][r] = mma<DT>(wf[c][r], xf[t][c], acc[t][r]);
+  }
+  // the rest of the row, fragment by fragment
+  for (int64_t k0 = (turns * U + first) * T::KF; k0 < A.in; k0 += step * T::KF) {
+    const RowPiece<DT, MODE> piece(k0 + T::PE * q, A.in);
+    u32x4 xf[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xf[t] = piece.load(xp[t]);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const u32x4 wf = piece.load(wa + at_w[r] - T::PE * q * T::ES);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t][r] = mma<DT>(wf, xf[t], acc[t][r]);
     }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
     __syncthreads();  // the tile before has been read
 #pragma unroll
-    for (int r = 0; r < RT; ++r) part[wave][r][lane] = acc[r];
+    for (int r = 0; r < RT; ++r) part[wave][r][lane] = acc[t][r];
     __syncthreads();
     for (int r = wave; r < RT; r += kFewWaves) {
       f32x4 sum = part[0][r][lane];
 #pragma unroll
       for (int w = 1; w < kFewWaves; ++w) sum += part[w][r][lane];
       const int r0 = 16 * r + 4 * q;
-      if (at < R.n) {
+      if (16 * t + i < R.n) {
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          if (r0 + v < A.rank) u[row_x * A.rank + r0 + v] = sum[v];
+          if (r0 + v < A.rank) u[row[t] * A.rank + r0 + v] = sum[v];
       }
     }
   }
+}
+
+template <int DT, int RT, int MODE>
+__global__ __launch_bounds__(64 * kFewWaves) void adapter_few_u_kernel(FewArgs A) {
+  __shared__ f32x4 part[kFewWaves][RT][64];
+  const int m = blockIdx.x;
+  if (m >= A.tokens) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const FewRows R(A, m, lane);
+  if (!R.mine || R.own < 0) return;
+  if (R.n <= 16) few_u<DT, RT, MODE, 1>(A, R, part, lane, wave);
+  else few_u<DT, RT, MODE, kWindow / 16>(A, R, part, lane, wave);
 }
 
 // Columns are the rows of the first operand here: tile j of a run has columns 16 j to
@@ -175,22 +201,16 @@ struct Quad {  // four consecutive elements of a row
 constexpr int few_tiles(int rt) { return rt <= 2 ? 8 : 4; }  // of a run, as the registers allow
 
 template <int DT, int RT, int MODE>
-__global__ __launch_bounds__(64 * kFewWaves) void adapter_few_y_kernel(FewArgs A) {
+__device__ __forceinline__ void few_y(const FewArgs &A, const FewRows &R,
+                                      u32x4 (*us)[Expand<DT, frag_count<DT>(RT), false, MODE>::UF][64], int lane, int wave) {
   using T = Tile<DT>;
   using X = Expand<DT, frag_count<DT>(RT), false, MODE>;
   constexpr int F = X::F, TILES = few_tiles(RT), COLS = 16 * TILES;
-  const int m = blockIdx.x;
-  if (m >= A.tokens) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
-  const FewRows R(A, m, lane);
-  if (!R.mine) return;
-  const int own = R.own, n = R.n;
-  const bool out_u = A.u_out && blockIdx.y == 0;
+  const int i = lane & 15, q = lane >> 4, own = R.own, n = R.n;
   const int64_t runs = (A.out + COLS - 1) / COLS;
   const int64_t first = blockIdx.y * kFewWaves + wave, step = kFewWaves * A.parts;
   const uint8_t *wb = A.b + (int64_t)(own < 0 ? 0 : own) * A.out * A.rank * T::ES;
   const uint8_t *w_last = wb + A.out * A.rank * T::ES - 16;
-  const float s = own >= 0 && A.scale ? A.scale[own] : 1.0f;
   // The lane's pieces of a run's weights lie at one distance each from the run's first
   // row, which is the wave's: loads take no arithmetic (it was what bound this kernel).
   uint32_t at_w[F];
@@ -201,74 +221,90 @@ __global__ __launch_bounds__(64 * kFewWaves) void adapter_few_y_kernel(FewArgs A
   }
   const uint32_t tile_bytes = 16 * A.rank * T::ES;
   const bool full = MODE == kExact && A.rank == 16 * RT;  // no fragment holds a rank past the last
-  for (int t = 0; 16 * t < n; ++t) {
-    const int64_t row = R.row(16 * t + i);
-    const bool wanted = 16 * t + i < n;
-    u32x4 uf[X::UF];
-    bool have_u = false;
-    const uint8_t *base_row = A.base + (row * A.ld_base + 4 * q) * T::ES;
-    uint8_t *y_row = A.y + (row * A.ldy + 4 * q) * T::ES;
-    for (int64_t run = first; run < runs; run += step) {
-      const int64_t n0 = run * COLS, left = A.out - n0 - 4 * q;
-      // (rows shorter than a piece end in the last 16 bytes: one run more is met with care)
-      const bool inside = n0 + COLS + (MODE == kCut ? T::PE : 0) <= A.out;
-      u32x4 w[F][TILES];
-      if (own >= 0) {
-        const uint8_t *from = wb + n0 * A.rank * T::ES;
-        if (inside && MODE != kSingle) {
+  // (rows shorter than a piece end in the last 16 bytes: one run more is met with care)
+  auto inside = [&](int64_t n0) { return MODE != kSingle && n0 + COLS + (MODE == kCut ? T::PE : 0) <= A.out; };
+  u32x4 w[F][TILES];
+  auto load = [&](int64_t n0) {
+    if (inside(n0)) {
+      const uint8_t *from = wb + n0 * A.rank * T::ES;
 #pragma unroll
-          for (int f = 0; f < F; ++f)
+      for (int f = 0; f < F; ++f)
 #pragma unroll
-            for (int j = 0; j < TILES; ++j) w[f][j] = ld_frag(from + j * tile_bytes + at_w[f]);
-        } else {
+        for (int j = 0; j < TILES; ++j) w[f][j] = ld_frag(from + j * tile_bytes + at_w[f]);
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < TILES; ++j) {
 #pragma unroll
-          for (int f = 0; f < F; ++f)
+        for (int f = 0; f < F; ++f) {
+          const int64_t col = n0 + 16 * j + i;
+          const int r0 = X::rank0(f, q);
+          const uint8_t *p = wb + ((col < A.out ? col : A.out - 1) * A.rank + (r0 < A.rank ? r0 : 0)) * T::ES;
+          const u32x4 v = settle_inside<DT, MODE>(ld_inside<DT, MODE>(p, w_last, A.rank - r0), p, w_last, A.rank - r0);
 #pragma unroll
-            for (int j = 0; j < TILES; ++j) {
-              const int64_t col = n0 + 16 * j + i;
-              const int r0 = X::rank0(f, q);
-              const uint8_t *p = wb + ((col < A.out ? col : A.out - 1) * A.rank + (r0 < A.rank ? r0 : 0)) * T::ES;
-              w[f][j] = settle_inside<DT, MODE>(ld_inside<DT, MODE>(p, w_last, A.rank - r0), p, w_last, A.rank - r0);
-            }
+          for (int k = 0; k < TILES; ++k)
+            if (k == j) w[f][k] = v;
         }
       }
+    }
+  };
+  if (own >= 0) {
+    if (first < runs) load(first * COLS);
+    if (16 * wave < n) {  // u's fragments, wave w those of tile w
+      const float s = A.scale ? A.scale[own] : 1.0f;
+      const float *up = A.u + R.row(16 * wave + i) * A.rank;
+      const uint8_t *u_last = reinterpret_cast<const uint8_t *>(A.u + A.tokens * A.rank - 4);
+      u32x4 uf[X::UF];
+      X::u_frags(uf, A.rank, q, [&](float(&v)[T::PE], int r, int rest) {
+#pragma unroll
+        for (int e = 0; e < T::PE; ++e) v[e] = 0.0f;
+#pragma unroll 2
+        for (int k = 0; k < A.splits; ++k) {
+#pragma unroll
+          for (int h = 0; h < T::PE; h += 4) {
+            const uint8_t *p = reinterpret_cast<const uint8_t *>(up + k * A.part + (rest > h ? r + h : 0));
+            const uint8_t *end = u_last + k * A.part * 4;
+            const u32x4 g = settle_inside<kF32, MODE>(ld_inside<kF32, MODE>(p, end, rest - h), p, end, rest - h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[h + e] += bits_f32(g[e]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < T::PE; ++e) v[e] *= s;
+      });
+#pragma unroll
+      for (int f = 0; f < X::UF; ++f) us[wave][f][lane] = uf[f];
+    }
+  }
+  static_assert(kFewWaves >= kWindow / 16, "a wave for every tile's fragments");
+  __syncthreads();
+  for (int64_t run = first; run < runs; run += step) {
+    const int64_t n0 = run * COLS, left = A.out - n0 - 4 * q;
+    const bool in = n0 + COLS <= A.out;
+    if (own >= 0 && run > first) load(n0);
+    bool settled = full || !inside(n0);
+#pragma unroll 1
+    for (int t = 0; 16 * t < n; ++t) {  // (the weights stay for all tiles of rows)
+      const int64_t row = R.row(16 * t + i);
+      const bool wanted = 16 * t + i < n;
       Quad<DT> out[TILES];
 #pragma unroll
       for (int j = 0; j < TILES; ++j) out[j] = Quad<DT>{};
       if (A.base && wanted) {
-        const uint8_t *from = base_row + n0 * T::ES;
+        const uint8_t *from = A.base + (row * A.ld_base + 4 * q + n0) * T::ES;
 #pragma unroll
-        for (int j = 0; j < TILES; ++j) out[j].load(from + 16 * j * T::ES, left - 16 * j, inside);
+        for (int j = 0; j < TILES; ++j) out[j].load(from + 16 * j * T::ES, left - 16 * j, in);
       }
       if (own >= 0) {
-        if (!have_u) {  // (once, when the first weights are under way)
-          const uint8_t *u_last = reinterpret_cast<const uint8_t *>(A.u + A.tokens * A.rank - 4);
-          const float *up = A.u + row * A.rank;
-          X::u_frags(uf, A.rank, q, [&](float(&v)[T::PE], int r, int rest) {
-#pragma unroll
-            for (int e = 0; e < T::PE; ++e) v[e] = 0.0f;
-#pragma unroll 2
-            for (int k = 0; k < A.splits; ++k) {
-#pragma unroll
-              for (int h = 0; h < T::PE; h += 4) {
-                const uint8_t *p = reinterpret_cast<const uint8_t *>(up + k * A.part + (rest > h ? r + h : 0));
-                const uint8_t *end = u_last + k * A.part * 4;
-                const u32x4 g = settle_inside<kF32, MODE>(ld_inside<kF32, MODE>(p, end, rest - h), p, end, rest - h);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[h + e] += bits_f32(g[e]);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < T::PE; ++e) v[e] *= s;
-          });
-          have_u = true;
-        }
-        if (!full && inside && MODE != kSingle) {
+        if (!settled) {
 #pragma unroll
           for (int f = 0; f < F; ++f)
 #pragma unroll
             for (int j = 0; j < TILES; ++j) w[f][j] = only<DT>(w[f][j], A.rank - X::rank0(f, q));
+          settled = true;
         }
+        u32x4 uf[X::UF];
+#pragma unroll
+        for (int f = 0; f < X::UF; ++f) uf[f] = us[t][f][lane];
 #pragma unroll
         for (int j = 0; j < TILES; ++j) {
           f32x4 acc = {0, 0, 0, 0};
@@ -278,28 +314,46 @@ __global__ __launch_bounds__(64 * kFewWaves) void adapter_few_y_kernel(FewArgs A
         }
       }
       if (wanted && (own >= 0 || A.base != A.y)) {
-        uint8_t *to = y_row + n0 * T::ES;
+        uint8_t *to = A.y + (row * A.ldy + 4 * q + n0) * T::ES;
 #pragma unroll
-        for (int j = 0; j < TILES; ++j) out[j].store(to + 16 * j * T::ES, left - 16 * j, inside);
+        for (int j = 0; j < TILES; ++j) out[j].store(to + 16 * j * T::ES, left - 16 * j, in);
       }
     }
-    if (out_u && wanted)
-      for (int r = wave * 4 + q; r < A.rank; r += 4 * kFewWaves)
-        A.u_out[row * A.rank + r] = own >= 0 ? parts_sum(A.u + row * A.rank + r, A.part, A.splits) : 0.0f;
   }
+  if (A.u_out && blockIdx.y == 0) {
+    const int count = n * A.rank;
+    for (int e0 = 0; e0 < count; e0 += 64 * kFewWaves) {
+      const int e = e0 + threadIdx.x, t = e / A.rank;
+      const int64_t at = R.row(t) * A.rank + (e - t * A.rank);  // (every lane takes part)
+      if (e < count) A.u_out[at] = own >= 0 ? parts_sum(A.u + at, A.part, A.splits) : 0.0f;
+    }
+  }
+}
+
+template <int DT, int RT, int MODE>
+__global__ __launch_bounds__(64 * kFewWaves) void adapter_few_y_kernel(FewArgs A) {
+  __shared__ u32x4 us[kWindow / 16][Expand<DT, frag_count<DT>(RT), false, MODE>::UF][64];
+  const int m = blockIdx.x;
+  if (m >= A.tokens) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const FewRows R(A, m, lane);
+  if (!R.mine) return;
+  few_y<DT, RT, MODE>(A, R, us, lane, wave);
 }
 
 // Few rows: the weights' reading is all there is.
 // (A's rows are reached by 32-bit distances.)
 bool few_rows(const AdapterLaunch &L) { return L.tokens <= 256 && L.rank * L.in < (int64_t)1 << 29; }
 
-// Parts of the long dimension, for about 768 workgroups, each wave with 512 bytes or more of a row.
+// Parts of the long dimension, for about 512 workgroups, each wave with 8 KB or more of an
+// adapter's weights.
 int few_splits(const AdapterLaunch &L) {
   const int64_t most = L.adapters < L.tokens ? L.adapters : L.tokens;
-  const int64_t useful = (L.in * (L.dtype == kBF16 ? 2 : 4) + 512 * kFewWaves - 1) / (512 * kFewWaves);
+  const int64_t useful = (L.in * L.rank * (L.dtype == kBF16 ? 2 : 4) + 8192 * kFewWaves - 1) / (8192 * kFewWaves);
   int64_t s = most > 0 ? 512 / most : 1;
   if (s > useful) s = useful;
-  if (s > 4) s = 4;
+  const int cap = L.rank <= 32 ? 4 : 12;  // (y's kernel adds the parts up)
+  if (s > cap) s = cap;
   return s < 1 ? 1 : (int)s;
 }
 

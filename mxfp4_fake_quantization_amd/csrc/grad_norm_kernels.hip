@@ -9,8 +9,8 @@
 // loads.  A workgroup sums a contiguous run of chunks and writes one partial sum;
 // the partial sums are added in a fixed order: no atomics, the same bits each time.
 //
-// Tensors come as kernel arguments, kBatch a launch: nothing is copied to the device,
-// and the call can be captured.
+// Tensors come as kernel arguments, up to 4 KB of them a launch: nothing is copied to the
+// device, and the call can be captured.
 #include "grad_norm_kernels.h"
 #include "mxfp4_device.h"
 #include "mxfp4_kernels.h"
@@ -19,20 +19,23 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kNormThreads = 256, kLoads = 4;          // 16-byte loads of a thread and chunk
+constexpr int kNormThreads = 256, kLoads = 8;          // 16-byte loads of a thread and chunk
 constexpr int kChunkBytes = kNormThreads * 16 * kLoads;
-constexpr int kBatch = 128;                            // tensors of a launch (4 KB of arguments)
 constexpr int kMostGroups = 2048;                      // workgroups of a launch
 
+// The tensors of a launch, as many as 4000 bytes of arguments hold.  OUT: with outputs apart from
+// the gradients.
+template <bool OUT>
 struct Batch {
-  const uint8_t *grad[kBatch];
-  uint8_t *out[kBatch];
-  int64_t count[kBatch];    // elements * 2, + 1 for fp32
-  uint32_t end[kBatch];     // chunks up to and with the tensor's
+  static constexpr int N = OUT ? 180 : 284;
+  const uint8_t *grad[N];
+  uint8_t *out[OUT ? N : 1];
+  uint32_t end[N];          // chunks up to and with the tensor's
+  uint16_t tail[N];         // elements of its last chunk * 2, + 1 for fp32
   int n;
   uint32_t chunks;
 };
-static_assert(sizeof(Batch) <= 4000, "kernel arguments stay below 4 KB");
+static_assert(sizeof(Batch<true>) <= 4000 && sizeof(Batch<false>) <= 4000, "kernel arguments stay below 4 KB");
 
 // Sum or maximum of |g|^p over a chunk, per thread.
 template <int P>
@@ -71,18 +74,21 @@ __device__ __forceinline__ float norm_of(double v) {
   return (float)(P == 2 ? __builtin_sqrt(v) : v);
 }
 
-// A chunk's place: the thread's first element and how many its tensor has from there.
+// A chunk's place: the thread's first element and how many the chunk has from there.
 struct Place {
   const uint8_t *p;
   uint8_t *out;
-  int64_t left;  // elements from the thread's first on
+  int left;
   bool f32;
 };
-__device__ __forceinline__ Place place(const Batch &B, uint32_t chunk, int item) {
-  const int64_t c = B.count[item];
-  const bool f32 = c & 1;
+template <bool OUT>
+__device__ __forceinline__ Place place(const Batch<OUT> &B, uint32_t chunk, int item) {
+  const int t = B.tail[item];
+  const bool f32 = t & 1;
   const int64_t first = (int64_t)(chunk - (item ? B.end[item - 1] : 0)) * kChunkBytes + threadIdx.x * 16;
-  return {B.grad[item] + first, B.out[item] + first, (c >> 1) - (first >> (f32 ? 2 : 1)), f32};
+  const int count = chunk + 1 == B.end[item] ? t >> 1 : kChunkBytes / (f32 ? 4 : 2);
+  const uint8_t *p = B.grad[item] + first;
+  return {p, OUT ? B.out[item] + first : const_cast<uint8_t *>(p), count - (int)threadIdx.x * (f32 ? 4 : 8), f32};
 }
 // Elements between a thread's loads of a chunk.
 __device__ __forceinline__ int step_of(bool f32) { return kNormThreads * (f32 ? 4 : 8); }
@@ -97,7 +103,7 @@ __device__ __forceinline__ void load_chunk(u32x4 (&w)[kLoads], const Place &at) 
   }
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int64_t n = at.left - i * step;
+    const int n = at.left - i * step;
     const uint8_t *p = at.p + i * (kNormThreads * 16);
     w[i] = u32x4{0, 0, 0, 0};
     if (n >= per) {
@@ -114,7 +120,8 @@ __device__ __forceinline__ void load_chunk(u32x4 (&w)[kLoads], const Place &at) 
   }
 }
 
-__device__ __forceinline__ int item_of(const Batch &B, uint32_t chunk) {
+template <bool OUT>
+__device__ __forceinline__ int item_of(const Batch<OUT> &B, uint32_t chunk) {
   int lo = 0, hi = B.n - 1;  // the first item whose end is past the chunk
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -126,7 +133,7 @@ __device__ __forceinline__ int item_of(const Batch &B, uint32_t chunk) {
 
 // partial: one double a workgroup; or, ALONE, the norm itself.
 template <int P>
-__global__ __launch_bounds__(kNormThreads) void grad_norm_kernel(Batch B, double *partial, float *norm) {
+__global__ __launch_bounds__(kNormThreads) void grad_norm_kernel(Batch<false> B, double *partial, float *norm) {
   __shared__ double lds[kNormThreads / 64];
   const uint32_t lo = (uint32_t)((uint64_t)B.chunks * blockIdx.x / gridDim.x);
   const uint32_t hi = (uint32_t)((uint64_t)B.chunks * (blockIdx.x + 1) / gridDim.x);
@@ -167,7 +174,7 @@ __device__ __forceinline__ double all_partials(const double *partial, int n, dou
   return group_joined<P, THREADS / 64>(v, lds);
 }
 
-constexpr int kFinalThreads = 1024;
+constexpr int kFinalThreads = 256;
 template <int P>
 __global__ __launch_bounds__(kFinalThreads) void grad_norm_final_kernel(const double *partial, int n, float *norm) {
   __shared__ double lds[kFinalThreads / 64];
@@ -178,8 +185,8 @@ __global__ __launch_bounds__(kFinalThreads) void grad_norm_final_kernel(const do
 // partial NULL: the norm is given.  Every workgroup joins the partial sums (they stay
 // in the cache); the first one of a launch with `write` stores the norm.  The chunks
 // are taken in the opposite order, the last read first: they are still in the cache.
-template <int P>
-__global__ __launch_bounds__(kNormThreads) void grad_clip_kernel(Batch B, const double *partial, int n, float *norm,
+template <int P, bool OUT>
+__global__ __launch_bounds__(kNormThreads) void grad_clip_kernel(Batch<OUT> B, const double *partial, int n, float *norm,
                                                                  float max_norm, bool write) {
   __shared__ double lds[kNormThreads / 64];
   float v;
@@ -214,7 +221,7 @@ __global__ __launch_bounds__(kNormThreads) void grad_clip_kernel(Batch B, const 
         for (int j = 0; j < 4; ++j)
           w[i][j] = pack_bf16(bits_f32(w[i][j] << 16) * coef, bits_f32(w[i][j] & 0xFFFF0000u) * coef);
       }
-      const int64_t left = at.left - i * step;
+      const int left = at.left - i * step;
       uint8_t *p = at.out + i * (kNormThreads * 16);
       if (left >= per) {
         *reinterpret_cast<u32x4_a2 *>(p) = w[i];
@@ -240,24 +247,26 @@ uint32_t chunks_of(const GradTensor &t) {
 
 // Tensors that follow one another in memory (and whose outputs do) are one to the
 // kernels: the gradients of a flat bucket take one launch, however many they are.
-bool follows(const GradTensor &a, const GradTensor &b) {
+bool follows(const GradTensor &a, const GradTensor &b, bool outs) {
   const int64_t bytes = a.count * (a.dtype == kF32 ? 4 : 2);
   return a.dtype == b.dtype && static_cast<const uint8_t *>(a.grad) + bytes == b.grad &&
-         (a.out == nullptr) == (b.out == nullptr) && (!a.out || static_cast<uint8_t *>(a.out) + bytes == b.out);
+         (!outs || static_cast<uint8_t *>(a.out) + bytes == b.out);
 }
 
 constexpr uint32_t kMostChunks = 1u << 30;  // of a launch
 
 // Calls f(batch, first partial, workgroups) for each launch.
-template <typename F>
+template <bool OUT, typename F>
 hipError_t each_batch(const GradNormLaunch &L, F f) {
-  Batch B;
+  Batch<OUT> B;
   B.n = 0;
   B.chunks = 0;
   int at = 0;
   auto send = [&]() {
     if (!B.n) return hipSuccess;
-    const int groups = B.chunks < (uint32_t)kMostGroups ? (int)B.chunks : kMostGroups;
+    // as many chunks for each workgroup, but for one
+    const uint32_t each = (B.chunks + kMostGroups - 1) / kMostGroups;
+    const int groups = (int)((B.chunks + each - 1) / each);
     const hipError_t e = f(B, at, groups);
     at += groups;
     B.n = 0;
@@ -267,31 +276,31 @@ hipError_t each_batch(const GradNormLaunch &L, F f) {
   for (int i = 0; i < L.n;) {
     GradTensor t = L.tensors[i++];
     if (!t.count) continue;
-    while (i < L.n && follows(t, L.tensors[i])) t.count += L.tensors[i++].count;
+    while (i < L.n && follows(t, L.tensors[i], OUT)) t.count += L.tensors[i++].count;
     const int64_t es = t.dtype == kF32 ? 4 : 2, most = (int64_t)(kMostChunks / 2) * (kChunkBytes / es);
     while (t.count > 0) {  // (a tensor of more chunks than a launch takes goes in parts)
       GradTensor part = t;
       if (part.count > most) part.count = most;
       const uint32_t c = chunks_of(part);
-      if (B.n == kBatch || B.chunks + c > kMostChunks) {
+      if (B.n == Batch<OUT>::N || B.chunks + c > kMostChunks) {
         const hipError_t e = send();
         if (e != hipSuccess) return e;
       }
       B.grad[B.n] = static_cast<const uint8_t *>(part.grad);
-      B.out[B.n] = static_cast<uint8_t *>(part.out);
-      B.count[B.n] = 2 * part.count + (part.dtype == kF32);
+      if (OUT) B.out[B.n] = static_cast<uint8_t *>(part.out);
+      B.tail[B.n] = (uint16_t)(2 * (part.count - (c - 1) * (kChunkBytes / es)) + (part.dtype == kF32));
       B.chunks += c;
       B.end[B.n++] = B.chunks;
       t.count -= part.count;
       t.grad = static_cast<const uint8_t *>(t.grad) + part.count * es;
-      if (t.out) t.out = static_cast<uint8_t *>(t.out) + part.count * es;
+      if (OUT) t.out = static_cast<uint8_t *>(t.out) + part.count * es;
     }
   }
   return send();
 }
 
 // One workgroup does it all: a handful of chunks cost less than a second launch.
-constexpr uint32_t kAlone = 8;
+constexpr uint32_t kAlone = 6;
 
 template <int P>
 hipError_t norm_and_clip(const GradNormLaunch &L, hipStream_t stream) {
@@ -300,8 +309,8 @@ hipError_t norm_and_clip(const GradNormLaunch &L, hipStream_t stream) {
   if (!L.given) {
     uint64_t chunks = 0;
     for (int i = 0; i < L.n; ++i) chunks += chunks_of(L.tensors[i]);
-    const bool alone = !L.clip && chunks <= kAlone && chunks > 0 && L.n <= kBatch;
-    const hipError_t e = each_batch(L, [&](const Batch &B, int at, int groups) {
+    const bool alone = !L.clip && chunks <= kAlone && chunks > 0 && L.n <= Batch<false>::N;
+    const hipError_t e = each_batch<false>(L, [&](const Batch<false> &B, int at, int groups) {
       grad_norm_kernel<P><<<alone ? 1 : groups, kNormThreads, 0, stream>>>(B, alone ? nullptr : L.workspace + at, L.norm);
       n = at + groups;
       return hipGetLastError();
@@ -313,17 +322,21 @@ hipError_t norm_and_clip(const GradNormLaunch &L, hipStream_t stream) {
     }
   }
   if (!L.clip) return hipSuccess;
-  return each_batch(L, [&](const Batch &B, int at, int groups) {
-    grad_clip_kernel<P><<<groups, kNormThreads, 0, stream>>>(B, partial, n, L.norm, L.max_norm, at == 0);
+  bool in_place = true;
+  for (int i = 0; i < L.n; ++i) in_place = in_place && (L.tensors[i].count == 0 || L.tensors[i].grad == L.tensors[i].out);
+  auto launch = [&](const auto &B, int at, int groups) {
+    constexpr bool OUT = sizeof(B.out) > sizeof(void *);
+    grad_clip_kernel<P, OUT><<<groups, kNormThreads, 0, stream>>>(B, partial, n, L.norm, L.max_norm, at == 0);
     return hipGetLastError();
-  });
+  };
+  return in_place ? each_batch<false>(L, launch) : each_batch<true>(L, launch);
 }
 
 }  // namespace
 
 int64_t grad_norm_workspace(int64_t n, int64_t elements) {
-  // a launch takes kBatch tensors, a part of one, or kMostChunks chunks
-  const int64_t chunks = elements * 4 / kChunkBytes + n, launches = n / kBatch + 1 + 4 * (chunks / kMostChunks + 1);
+  // a launch takes Batch::N tensors, a part of one, or kMostChunks chunks
+  const int64_t chunks = elements * 4 / kChunkBytes + n, launches = n / Batch<false>::N + 1 + 4 * (chunks / kMostChunks + 1);
   const int64_t most = launches * kMostGroups;
   return chunks < most ? chunks : most;
 }
