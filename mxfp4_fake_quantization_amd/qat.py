@@ -17,6 +17,9 @@ twice changes nothing).  Here every step runs in libmxfp4's HIP kernels:
   its Parameter objects.
 - ``quantize_model``: swaps every Linear of a model (outside the excluded
   paths) for a QATLinear.
+- ``clip_grad_norm_``: the norm over all gradients of a training step, and clipping,
+  with torch.nn.utils.clip_grad_norm_'s arguments (two launches for a model's hundreds
+  of tensors, sums in 64 bits).
 
 The names of the PR's interface (``mxfp4_fake_quant``, ``MXFP4FakeQuantizer``,
 ``MXFP4QATConfig``, ``MXFP4QATLinear``, ``convert_to_mxfp4_qat``) are kept as
@@ -35,9 +38,10 @@ import torch
 import torch.nn.functional as F
 from torch import nn
 
-from . import ROW, mxfp4_qdq_fwd, mxfp4_qdq_fwd_rows_batch, mxfp4_ste_bwd, mxfp4_ste_bwd_rows_batch
+from . import (ROW, mxfp4_grad_clip, mxfp4_grad_norm, mxfp4_qdq_fwd, mxfp4_qdq_fwd_rows_batch, mxfp4_ste_bwd,
+               mxfp4_ste_bwd_rows_batch)
 
-__all__ = ["MXFP4Spec", "QATPolicy", "QATLinear", "FakeQuant", "fake_quant", "quantize_model",
+__all__ = ["MXFP4Spec", "QATPolicy", "QATLinear", "FakeQuant", "fake_quant", "quantize_model", "clip_grad_norm_",
            "mxfp4_fake_quant", "MXFP4FakeQuantizer", "MXFP4QATConfig", "MXFP4QATLinear",
            "convert_to_mxfp4_qat"]
 
@@ -252,6 +256,29 @@ def quantize_model(model: nn.Module, policy: Optional[QATPolicy] = None,
         setattr(parent, leaf, done[id(mod)])
         replaced.append(path)
     return model
+
+
+@torch.no_grad()
+def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0,
+                    error_if_nonfinite: bool = False) -> torch.Tensor:
+    """Scale the gradients of ``parameters`` (tensors, or one) in place by min(1,
+    max_norm / (norm + 1e-6)), norm being the 1-, 2- or inf-norm over all of them
+    together; returns the norm (float32, on the GPU).  Gradients are contiguous
+    bfloat16 or float32 tensors on one GPU.  With ``error_if_nonfinite`` a norm that
+    is no finite number raises before anything is scaled (and the host waits for it)."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = [p.grad for p in parameters if p.grad is not None]
+    if not grads:
+        return torch.tensor(0.0)
+    norm = torch.empty((), device=grads[0].device)
+    if error_if_nonfinite:
+        mxfp4_grad_norm(grads, norm, norm_type=norm_type)
+        if not bool(torch.isfinite(norm)):
+            raise RuntimeError(f"the {norm_type}-norm of the gradients is not finite: {float(norm)}")
+    mxfp4_grad_clip(grads, max_norm, norm, norm_type=norm_type, compute_norm=not error_if_nonfinite)
+    torch.autograd.graph.increment_version(grads)  # written behind autograd's back
+    return norm
 
 
 # ---------------------------------------------------------------------------
