@@ -384,23 +384,27 @@ __device__ __forceinline__ float parts_sum(const float *u, int64_t part, int spl
 // (the wave's 16 KB) and u, of which wave w makes the fragments of rows 16 w to 16 w +
 // 15 for all.  Then the adapters of the window pass one after the other; a row takes
 // the result of its own one, so that no other adapter's values (an infinity, say) reach it.
-constexpr int kExpandTiles = 4, kExpandRows = 16 * kExpandTiles;
+// Rows of a workgroup: 64, with the 16-byte pieces of 128 columns a row; 32 in fp32, whose registers
+// then leave room for a wave more (4096 rows, 4096 columns, rank 8: 28.8 us, with 64 rows 31.2;
+// bf16, 8192 rows, 7168 columns, rank 32: 59.4 with 32 rows, 55.2 with 64).
+template <int DT>
+constexpr int kExpandRows = DT == kBF16 ? 64 : 32;
 
 template <int DT, int NF, bool ACROSS, int MODE>
-__global__ __launch_bounds__(64 * kExpandWaves, NF <= 1 ? 3 : 2) void adapter_expand_kernel(ExpandArgs A, int chunks) {
+__global__ __launch_bounds__(64 * kExpandWaves, NF <= 1 ? (DT == kBF16 ? 3 : 4) : 2) void adapter_expand_kernel(ExpandArgs A, int chunks) {
   using T = Tile<DT>;
   using X = Expand<DT, NF, ACROSS, MODE>;
-  constexpr int TILES = kExpandTiles;
+  constexpr int ROWS = kExpandRows<DT>, TILES = ROWS / 16;
   __shared__ u32x4 us[TILES][X::UF][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
   const int64_t tile = xcd_share(blockIdx.x, gridDim.x);
-  const int64_t row0 = tile / chunks * kExpandRows;
+  const int64_t row0 = tile / chunks * ROWS;
   const int chunk = (int)(tile % chunks);
   const int64_t n0 = ((int64_t)chunk * kExpandWaves + wave) * X::COLS;
-  const int rows = A.tokens - row0 < kExpandRows ? (int)(A.tokens - row0) : kExpandRows;
+  const int rows = A.tokens - row0 < ROWS ? (int)(A.tokens - row0) : ROWS;
   const int id = lane < rows ? row_adapter(A.ids, row0 + lane, A.adapters) : -2;
   const bool mine = n0 < A.N;  // (a wave past the columns still makes fragments)
-  const bool inside = (int64_t)(chunk + 1) * kExpandWaves * X::COLS <= A.N && rows == kExpandRows;
+  const bool inside = (int64_t)(chunk + 1) * kExpandWaves * X::COLS <= A.N && rows == ROWS;
   const int64_t col = n0 + T::PE * i;
   // out[j][v]: row 16 j + 4 q + v; base at first
   u32x4 out[TILES][4];
@@ -531,11 +535,14 @@ __global__ __launch_bounds__(64 * kExpandWaves, NF <= 1 ? 3 : 2) void adapter_ex
 
 inline int window_count(int64_t tokens) { return (int)((tokens + kWindow - 1) / kWindow); }
 
-// Parts of the long dimension: as many as put two workgroups on each of the 256 CUs.
+// Parts of the long dimension: as many as put a workgroup on each of the 256 CUs. The second kernel
+// adds the parts up once a tile of columns, so fewer are better there (8192 tokens, 7168 columns,
+// rank 64, both kernels of the backward: 23 + 61 us; with two workgroups a CU 31 + 70, and with half a
+// workgroup 24 + 54; but 4096 tokens of fp32, rank 8: 14.4 + 28, two 15.2 + 28.8, half 21.7 + 27.2).
 inline int shrink_splits(int64_t tokens, int64_t K) {
   const int64_t windows = window_count(tokens);
   const int64_t most = (K + 511) / 512;
-  int64_t s = 512 / (windows > 0 ? windows : 1);
+  int64_t s = 256 / (windows > 0 ? windows : 1);
   if (s > most) s = most;
   if (s > 16) s = 16;
   return s < 1 ? 1 : (int)s;
@@ -586,7 +593,7 @@ hipError_t launch_shrink(const ShrinkArgs &A, const PlanArgs &P, int mode, hipSt
 
 template <int DT, bool ACROSS>
 hipError_t launch_expand(const ExpandArgs &A, int mode, hipStream_t stream) {
-  const int64_t windows = (A.tokens + kExpandRows - 1) / kExpandRows;
+  const int64_t windows = (A.tokens + kExpandRows<DT> - 1) / kExpandRows<DT>;
   const int64_t cols = kExpandWaves * 16 * Tile<DT>::PE;
   const int chunks = (int)((A.N + cols - 1) / cols);
   const dim3 grid((unsigned)(windows * chunks));
