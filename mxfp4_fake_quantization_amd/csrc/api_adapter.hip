@@ -51,14 +51,15 @@ mxfp4_status_t check_space(const void *workspace, int64_t have, int64_t need) {
   return MXFP4_OK;
 }
 
-// Workgroups of the weight gradients' launches, 256 threads each.
+// Workgroups of the weight gradients' launches, 256 threads each: pieces by columns, and 256 elements of
+// the summed gradients; a launch has below 2^32 threads.
 mxfp4_status_t check_trained(const mxfp4_adapter_t *d) {
   if (d->adapters > mxfp4::kAdapterMaxTrained)
     return fail(MXFP4_EUNSUPPORTED, "the backward pass takes up to %d adapters, got %d", mxfp4::kAdapterMaxTrained,
                 d->adapters);
   const int64_t sum = d->in_features + d->out_features;
   const int64_t pieces = d->tokens / 128 + (d->adapters < d->tokens ? d->adapters : d->tokens);
-  if (pieces * (sum / 64 + 2) >= (int64_t)1 << 24 || d->adapters * (d->rank * sum / 1024 + 2) >= (int64_t)1 << 24)
+  if (pieces * (sum / 64 + 2) >= (int64_t)1 << 24 || d->adapters * (d->rank * sum / 256 + 2) >= (int64_t)1 << 24)
     return fail(MXFP4_EUNSUPPORTED, "%d adapters of %lld features and %lld tokens are more than one call takes",
                 d->adapters, (long long)sum, (long long)d->tokens);
   return MXFP4_OK;

@@ -168,6 +168,9 @@ def test_abi_backward(lib):
     assert bwd(lib, desc(), ga=A[6]) == EINVAL                    # over the workspace
     assert bwd(lib, desc(adapters=1025), **full) == EUNSUP
     assert lib.mxfp4_adapter_bwd_workspace(desc(adapters=1025), 1, 1) == -1
+    big = dict(adapters=1024, rank=128, n_in=1 << 14)             # the summed gradients fill 2^32 threads
+    assert lib.mxfp4_adapter_bwd_workspace(desc(**big, n_out=1 << 14), 1, 1) == -1
+    assert lib.mxfp4_adapter_bwd_workspace(desc(**big, n_out=1 << 13), 1, 1) > 0
     need = lib.mxfp4_adapter_bwd_workspace(desc(), 1, 1)
     assert lib.mxfp4_adapter_bwd_workspace(desc(), 0, 0) < need
     assert bwd(lib, desc(), **full, nbytes=need - 1) == EINVAL
