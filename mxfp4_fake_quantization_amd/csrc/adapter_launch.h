@@ -318,7 +318,7 @@ __global__ __launch_bounds__(kShrinkThreads) void adapter_shrink_kernel(ShrinkAr
     using Yes = std::integral_constant<bool, true>;
     using No = std::integral_constant<bool, false>;
     // blocks inside the rows; (ACROSS) and whose pieces of short rows end inside W
-    const int64_t inside = (A.K - (ACROSS && MODE == kCut ? T::PE : 0)) / BK;
+    const int64_t inside = (A.K - (ACROSS && MODE != kExact ? T::PE : 0)) / BK;
     const int64_t full = hi <= inside ? hi : inside > lo ? inside : lo;
     const int64_t count = full - lo;
     if (count > 0) {

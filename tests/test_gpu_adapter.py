@@ -172,6 +172,25 @@ def test_backward(size, pattern, dt):
         assert torch.equal(alone, out[k])
 
 
+# rows of x, W or u shorter than 16 bytes, the other dimension whole blocks of the kernels
+SHORT = [(200, 4, 128, 2, 3), (300, 6, 512, 3, 2), (70, 3, 64, 1, 2), (40, 512, 3, 5, 2), (500, 1, 1, 7, 3), (1, 2, 256, 1, 1)]
+
+
+@pytest.mark.parametrize("dt", [bf16, f32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("size", SHORT, ids=str)
+def test_short_rows(size, dt):
+    p = Problem(*size, "mixed" if size[0] > 1 else "null", dt)
+    y, u = torch.empty_like(p.base), torch.empty(size[0], size[3], device="cuda")
+    M.mxfp4_adapter_fwd(p.x, p.a, p.b, y, ids=p.ids, scale=p.scale, base=p.base, u=u)
+    wy, ey, wu, eu = p.forward64(True, True)
+    within(y, wy, ey)
+    within(u, wu, eu)
+    out = {"grad_x": torch.empty_like(p.x), "grad_a": torch.empty_like(p.a), "grad_b": torch.empty_like(p.b)}
+    M.mxfp4_adapter_bwd(p.gy, p.a, p.b, x=p.x, u=u, ids=p.ids, scale=p.scale, base=p.gbase, **out)
+    for k, (want, bound) in p.backward64(u, True, True).items():
+        within(out[k], want, bound)
+
+
 @pytest.mark.parametrize("dt", [bf16, f32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("pattern", ["null", "none", "last"])
 @pytest.mark.parametrize("size", [(5, 200, 70, 8, 3), (150, 384, 520, 20, 3)], ids=str)
@@ -352,6 +371,42 @@ def test_long_training_batch():
         again = {k: torch.empty_like(t) for k, t in out.items()}
         M.mxfp4_adapter_bwd(p.gy, p.a, p.b, x=p.x, u=u, ids=p.ids, scale=p.scale, base=p.gbase, **again)
         assert all(torch.equal(out[k], again[k]) for k in out)
+
+
+@pytest.mark.parametrize("tokens,ld", [(70, 1 << 25), (300, 1 << 23)])
+def test_rows_far_apart(tokens, ld):
+    """Columns of matrices whose rows lie more than 2^32 bytes from the first: the bits of the same rows together."""
+    p = Problem(tokens, 64, 96, 8, 3, "mixed", bf16)
+    far = torch.empty(tokens, ld, dtype=bf16, device="cuda")
+    x, y, gy, gx = (far[:, 128 * k:128 * k + n] for k, n in enumerate((64, 96, 96, 64)))
+    x.copy_(p.x)
+    gy.copy_(p.gy)
+    want, u = torch.empty_like(p.base), torch.empty(tokens, 8, device="cuda")
+    wx, wa, wb = torch.empty_like(p.x), torch.empty_like(p.a), torch.empty_like(p.b)
+    M.mxfp4_adapter_fwd(p.x, p.a, p.b, want, ids=p.ids, base=p.base, u=u)
+    M.mxfp4_adapter_bwd(p.gy, p.a, p.b, x=p.x, u=u, ids=p.ids, grad_x=wx, grad_a=wa, grad_b=wb)
+    v, ga, gb = torch.empty_like(u), torch.empty_like(p.a), torch.empty_like(p.b)
+    M.mxfp4_adapter_fwd(x, p.a, p.b, y, ids=p.ids, base=p.base, u=v)
+    M.mxfp4_adapter_bwd(gy, p.a, p.b, x=x, u=u, ids=p.ids, grad_x=gx, grad_a=ga, grad_b=gb)
+    for a, b in ((y, want), (v, u), (gx, wx), (ga, wa), (gb, wb)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("tokens", [3, 300])
+def test_weights_past_32_bits(tokens):
+    """The last of adapters that together hold more than 2^32 bytes."""
+    p = Problem(tokens, 8192, 1024, 128, 2, "mixed", bf16)
+    a = torch.empty(2100, 128, 8192, dtype=bf16, device="cuda")
+    b = torch.empty(2100, 1024, 128, dtype=bf16, device="cuda")
+    a[[0, 2099]] = p.a
+    b[[0, 2099]] = p.b
+    ids = torch.where(p.ids == 1, 2099, torch.where(p.ids == 0, 0, -1)).to(torch.int32)
+    want, y = torch.empty_like(p.base), torch.empty_like(p.base)
+    M.mxfp4_adapter_fwd(p.x, p.a, p.b, want, ids=p.ids, base=p.base)
+    M.mxfp4_adapter_fwd(p.x, a, b, y, ids=ids, base=p.base)
+    # (how the long dimension is cut hangs on the number of adapters: two sums in fp32, rounded once each)
+    bound = p.forward64(False, True)[1]
+    within(y, want.double(), 2 * bound)
 
 
 @pytest.mark.parametrize("tokens,adapters", [(4, 3), (300, 5)])

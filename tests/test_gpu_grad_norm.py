@@ -167,6 +167,19 @@ def test_bucket(dt):
             assert torch.equal(norm, one)
 
 
+def test_past_32_bits():
+    """A tensor of more than 2^32 bytes, whose last elements are what there is."""
+    t = torch.zeros((1 << 31) + 77, dtype=bf16, device="cuda")
+    t[-3:] = torch.tensor([3.0, -4.0, 12.0])
+    t[5] = 84.0
+    norm = torch.empty(1, device="cuda")
+    M.mxfp4_grad_norm([t], norm)
+    assert float(norm) == 85.0
+    M.mxfp4_grad_clip([t], 42.5, norm)
+    assert float(norm) == 85.0 and t[-3:].tolist() == [1.5, -2.0, 6.0] and float(t[5]) == 42.0
+    assert int(t.count_nonzero()) == 4
+
+
 def test_streams_and_graphs():
     grads = grads_of([3000, 70000, 5, 20000], [bf16, f32])
     outs = [torch.empty_like(t) for t in grads]
