@@ -616,7 +616,8 @@ mxfp4_status_t mxfp4_grad_norm(int32_t norm_type, int32_t n, const mxfp4_grad_it
  * the same tensors (compute_norm 1: computed and written to norm) or one that
  * the caller holds (0: norm is read, for instance a norm over several processes;
  * workspace may be NULL).  An infinite norm gives 0 (NaN for infinite elements), a
- * NaN norm NaN.  Each element is rounded once.  out is grad, or overlaps no tensor.
+ * NaN norm NaN.  Each element is rounded once.  out is grad, or overlaps no tensor;
+ * no tensor is given twice (MXFP4_EINVAL).
  */
 mxfp4_status_t mxfp4_grad_clip(int32_t norm_type, int32_t n, const mxfp4_grad_item_t *items, float max_norm,
                                int32_t compute_norm, float *norm, void *workspace, int64_t workspace_bytes,

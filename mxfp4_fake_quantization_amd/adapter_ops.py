@@ -254,7 +254,8 @@ def mxfp4_grad_norm(grads, norm, norm_type=2.0, workspace=None):
 def mxfp4_grad_clip(grads, max_norm, norm, outs=None, norm_type=2.0, compute_norm=True, workspace=None):
     """Every gradient times min(1, max_norm / (norm + 1e-6)), in place or into
     ``outs``.  norm (one float32 element) receives the norm of ``grads``; without
-    ``compute_norm`` it is read instead (a norm over several processes)."""
+    ``compute_norm`` it is read instead (a norm over several processes).  What is
+    written may overlap nothing else: a tensor given twice is refused."""
     order, pn = _norm_type(norm_type), _norm_out(norm)
     items, elements = _items(grads, outs, True)
     _here(norm, workspace)

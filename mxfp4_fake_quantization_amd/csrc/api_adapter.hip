@@ -7,6 +7,10 @@
 #include "grad_norm_kernels.h"
 #include "mxfp4_kernels.h"
 
+#include <algorithm>
+#include <new>
+#include <vector>
+
 using namespace mxfp4_api;
 
 namespace {
@@ -62,6 +66,50 @@ mxfp4_status_t check_trained(const mxfp4_adapter_t *d) {
   if (pieces * (sum / 64 + 2) >= (int64_t)1 << 24 || d->adapters * (d->rank * sum / 256 + 2) >= (int64_t)1 << 24)
     return fail(MXFP4_EUNSUPPORTED, "%d adapters of %lld features and %lld tokens are more than one call takes",
                 d->adapters, (long long)sum, (long long)d->tokens);
+  return MXFP4_OK;
+}
+
+// What clipping writes must not meet: a tensor given twice would be scaled twice, in an order that
+// hangs on the workgroups.  (The sort of 448 tensors in no order takes 14 us of the host's time.)
+struct Span {
+  uintptr_t lo, hi;
+  bool read;  // a gradient with its output elsewhere: may meet another one
+};
+bool meets(const std::vector<Span> &spans) {
+  uintptr_t any = 0, written = 0;
+  for (const Span &s : spans) {
+    if (s.lo < (s.read ? written : any)) return true;
+    any = std::max(any, s.hi);
+    if (!s.read) written = std::max(written, s.hi);
+  }
+  return false;
+}
+mxfp4_status_t check_clip_spans(int32_t n, const mxfp4_grad_item_t *items, const float *norm, const void *workspace,
+                                int64_t workspace_bytes) {
+  try {
+    std::vector<Span> spans;
+    spans.reserve(2 * (size_t)n);
+    const uintptr_t nlo = reinterpret_cast<uintptr_t>(norm), nhi = nlo + 4;
+    const uintptr_t wlo = reinterpret_cast<uintptr_t>(workspace), whi = wlo + (uintptr_t)workspace_bytes;
+    bool good = true;
+    auto add = [&](const void *p, int64_t bytes, bool read) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      if (bytes == 0) return;
+      const Span s{at, at + (uintptr_t)bytes, read};
+      good = good && (s.hi <= nlo || s.lo >= nhi) && (s.hi <= wlo || s.lo >= whi);
+      spans.push_back(s);
+    };
+    for (int32_t i = 0; i < n; ++i) {
+      const int64_t bytes = items[i].count * (items[i].dtype == MXFP4_F32 ? 4 : 2);
+      add(items[i].out, bytes, false);
+      if (items[i].grad != items[i].out) add(items[i].grad, bytes, true);
+    }
+    auto before = [](const Span &a, const Span &b) { return a.lo < b.lo; };
+    if (!std::is_sorted(spans.begin(), spans.end(), before)) std::sort(spans.begin(), spans.end(), before);
+    if (!good || meets(spans)) return fail(MXFP4_EINVAL, "a clipped tensor overlaps another tensor, the norm or the workspace");
+  } catch (const std::bad_alloc &) {
+    return fail(MXFP4_EUNSUPPORTED, "no host memory to check %d tensors", n);
+  }
   return MXFP4_OK;
 }
 
@@ -194,7 +242,9 @@ mxfp4_status_t mxfp4_grad_clip(int32_t norm_type, int32_t n, const mxfp4_grad_it
   if (compute_norm != 0 && compute_norm != 1) return fail(MXFP4_EINVAL, "compute_norm must be 0 or 1 (got %d)", compute_norm);
   if (!(max_norm >= 0.0f)) return fail(MXFP4_EINVAL, "max_norm must be >= 0 (got %g)", (double)max_norm);
   MXFP4_TRY(check_ptr(norm, 4, "norm"));
-  if (compute_norm) MXFP4_TRY(check_space(workspace, workspace_bytes, mxfp4_grad_norm_workspace(n, elements)));
+  const int64_t need = compute_norm ? mxfp4_grad_norm_workspace(n, elements) : 0;
+  MXFP4_TRY(check_space(workspace, workspace_bytes, need));
+  MXFP4_TRY(check_clip_spans(n, items, norm, workspace, need));
   mxfp4::GradNormLaunch L{items, n, norm_type, static_cast<double *>(workspace), norm, true, !compute_norm, max_norm};
   return hip_status(mxfp4::launch_grad_norm(L, static_cast<hipStream_t>(stream)), "gradient clipping launch");
 }

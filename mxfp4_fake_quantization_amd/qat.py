@@ -264,7 +264,7 @@ def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0,
     """Scale the gradients of ``parameters`` (tensors, or one) in place by min(1,
     max_norm / (norm + 1e-6)), norm being the 1-, 2- or inf-norm over all of them
     together; returns the norm (float32, on the GPU).  Gradients are contiguous
-    bfloat16 or float32 tensors on one GPU.  With ``error_if_nonfinite`` a norm that
+    bfloat16 or float32 tensors on one GPU, each given once.  With ``error_if_nonfinite`` a norm that
     is no finite number raises before anything is scaled (and the host waits for it)."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]

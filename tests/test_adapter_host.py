@@ -205,6 +205,13 @@ def test_abi_norm(lib):
     assert clip([good], compute=2) == EINVAL
     assert clip([good], ws=None) == EINVAL
     assert clip([], compute=0, ws=None, nbytes=0) == OK           # nothing to do
+    # what is written overlaps nothing: the same tensor twice, a part of it, another's output or gradient, the norm
+    for other in (item(A[0], A[0], 100, BF16, 0), item(A[0] + 198, A[0] + 198, 100, BF16, 0),
+                  item(A[4], A[0] + 100, 7, F32, 0), item(A[0] + 4, A[4], 7, BF16, 0),
+                  item(A[1] - 4, A[1] - 4, 2, F32, 0), item(A[4], A[4] + 2, 5, BF16, 0), item(A[2], A[2], 4, F32, 0)):
+        for pair in ([item(A[0], A[0], 100, BF16, 0), other], [other, item(A[0], A[0], 100, BF16, 0)]):
+            assert clip(pair) == EINVAL
+            assert b"overlaps" in lib.mxfp4_last_error()
     assert lib.mxfp4_grad_norm_workspace(-1, 5) == -1 and lib.mxfp4_grad_norm_workspace(1, -5) == -1
 
 
