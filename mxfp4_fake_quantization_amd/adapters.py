@@ -73,12 +73,14 @@ def adapter_add(x, base, a, b, ids: Optional[torch.Tensor] = None, scale: Option
     """base + scale_i (x a_i^T) b_i^T with each token's adapter i = ids (int32,
     x's leading shape; None: adapter 0; outside [0, adapters): none).  base is
     [..., out] of x's type, a [adapters, rank, in], b [adapters, out, rank], scale
-    float32 [adapters].  Gradients reach x, base, a and b; second derivatives are
-    refused."""
+    float32 [adapters].  Gradients reach x, base, a and b (of up to 1024 adapters);
+    second derivatives, and a scale that wants a gradient, are refused."""
     if x.dim() < 1 or base.dim() != x.dim() or base.shape[:-1] != x.shape[:-1]:
         raise ValueError(f"base must have x's leading shape {list(x.shape[:-1])}, got {list(base.shape)}")
     if base.dtype != x.dtype:
         raise ValueError(f"base must have x's type {x.dtype}, got {base.dtype}")
+    if scale is not None and scale.requires_grad and torch.is_grad_enabled():
+        raise ValueError("scale gets no gradient: detach it")
     if ids is not None:
         if ids.shape != x.shape[:-1]:
             raise ValueError(f"ids must be {list(x.shape[:-1])}, got {list(ids.shape)}")

@@ -215,6 +215,13 @@ def test_abi_norm(lib):
     assert lib.mxfp4_grad_norm_workspace(-1, 5) == -1 and lib.mxfp4_grad_norm_workspace(1, -5) == -1
 
 
+def test_scale_wants_no_gradient():
+    from mxfp4_fake_quantization_amd.adapters import adapter_add
+    x, base, a, b = torch.zeros(2, 8), torch.zeros(2, 6), torch.zeros(1, 3, 8), torch.zeros(1, 6, 3)
+    with pytest.raises(ValueError, match="no gradient"):
+        adapter_add(x, base, a, b, scale=torch.ones(1, requires_grad=True))
+
+
 def test_abi_structs():
     """The packed structs have the sizes of the C ones."""
     assert adapter_ops._ADAPTER.size == 40 and adapter_ops._ITEM.size == 32
