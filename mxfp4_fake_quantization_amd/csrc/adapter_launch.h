@@ -389,9 +389,15 @@ __device__ __forceinline__ float parts_sum(const float *u, int64_t part, int spl
 // bf16, 8192 rows, 7168 columns, rank 32: 59.4 with 32 rows, 55.2 with 64).
 template <int DT>
 constexpr int kExpandRows = DT == kBF16 ? 64 : 32;
+// Waves a SIMD; what lets the weights stay in registers. (bf16 of rank 65 to 128, 1000 rows and columns:
+// 41 us with one wave, 46 with two and 124 registers spilled; fp32 is faster with two and 35 spilled, 4096
+// rows and columns 180 us, else 201.)
+template <int DT, int NF>
+constexpr int kExpandOccupancy = NF <= 1 ? (DT == kBF16 ? 3 : 4) : DT == kBF16 && NF >= 4 ? 1 : 2;
 
 template <int DT, int NF, bool ACROSS, int MODE>
-__global__ __launch_bounds__(64 * kExpandWaves, NF <= 1 ? (DT == kBF16 ? 3 : 4) : 2) void adapter_expand_kernel(ExpandArgs A, int chunks) {
+__global__ __launch_bounds__(64 * kExpandWaves, (kExpandOccupancy<DT, NF>)) void adapter_expand_kernel(ExpandArgs A,
+                                                                                                           int chunks) {
   using T = Tile<DT>;
   using X = Expand<DT, NF, ACROSS, MODE>;
   constexpr int ROWS = kExpandRows<DT>, TILES = ROWS / 16;
