@@ -247,8 +247,22 @@ __device__ __forceinline__ void few_y(const FewArgs &A, const FewRows &R,
       }
     }
   };
+  // base of tile t of the rows; the first one's is under way with the weights and u
+  Quad<DT> out[TILES];
+  auto fetch = [&](int64_t n0, int t) {
+    const int64_t left = A.out - n0 - 4 * q, row = R.row(16 * t + i);
+    const bool in = n0 + COLS <= A.out;
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) out[j] = Quad<DT>{};
+    if (A.base && 16 * t + i < n) {
+      const uint8_t *from = A.base + (row * A.ld_base + 4 * q + n0) * T::ES;
+#pragma unroll
+      for (int j = 0; j < TILES; ++j) out[j].load(from + 16 * j * T::ES, left - 16 * j, in);
+    }
+  };
+  if (own >= 0 && first < runs) load(first * COLS);
+  if (first < runs) fetch(first * COLS, 0);
   if (own >= 0) {
-    if (first < runs) load(first * COLS);
     if (16 * wave < n) {  // u's fragments, wave w those of tile w
       const float s = A.scale ? A.scale[own] : 1.0f;
       const float *up = A.u + R.row(16 * wave + i) * A.rank;
@@ -280,20 +294,16 @@ __device__ __forceinline__ void few_y(const FewArgs &A, const FewRows &R,
   for (int64_t run = first; run < runs; run += step) {
     const int64_t n0 = run * COLS, left = A.out - n0 - 4 * q;
     const bool in = n0 + COLS <= A.out;
-    if (own >= 0 && run > first) load(n0);
+    if (run > first) {
+      if (own >= 0) load(n0);
+      fetch(n0, 0);
+    }
     bool settled = full || !inside(n0);
 #pragma unroll 1
     for (int t = 0; 16 * t < n; ++t) {  // (the weights stay for all tiles of rows)
       const int64_t row = R.row(16 * t + i);
       const bool wanted = 16 * t + i < n;
-      Quad<DT> out[TILES];
-#pragma unroll
-      for (int j = 0; j < TILES; ++j) out[j] = Quad<DT>{};
-      if (A.base && wanted) {
-        const uint8_t *from = A.base + (row * A.ld_base + 4 * q + n0) * T::ES;
-#pragma unroll
-        for (int j = 0; j < TILES; ++j) out[j].load(from + 16 * j * T::ES, left - 16 * j, in);
-      }
+      if (t > 0) fetch(n0, t);
       if (own >= 0) {
         if (!settled) {
 #pragma unroll

@@ -420,7 +420,10 @@ __global__ __launch_bounds__(64 * kExpandWaves, (kExpandOccupancy<DT, NF>)) void
 #pragma unroll
     for (int j = 0; j < TILES; ++j)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) out[j][v] = ld_frag_nt(from + (16 * j + v) * A.ld_base * T::ES + mine_at);
+      for (int v = 0; v < 4; ++v) {  // (unaligned rows share cache lines between their pieces)
+        const uint8_t *p = from + (16 * j + v) * A.ld_base * T::ES + mine_at;
+        out[j][v] = MODE == kExact ? ld_frag_nt(p) : ld_frag(p);
+      }
   } else if (A.base && mine) {  // rows and columns past the last hold anything
     const RowPiece<DT, MODE> piece(col, A.N);
 #pragma unroll
