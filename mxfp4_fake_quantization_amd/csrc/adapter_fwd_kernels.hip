@@ -351,9 +351,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void adapter_few_y_kernel(FewArgs A
   few_y<DT, RT, MODE>(A, R, us, lane, wave);
 }
 
-// Few rows: the weights' reading is all there is.
-// (A's rows are reached by 32-bit distances.)
-bool few_rows(const AdapterLaunch &L) { return L.tokens <= 256 && L.rank * L.in < (int64_t)1 << 29; }
+// Few rows, and few of an adapter: up to 16 on average, one tile; the weights' reading is all there is.
+// (4096 -> 4096, rank 16, 48 adapters: 32 / 256 / 512 rows take 10 / 13.2 / 21.1 us, as many rows 42 /
+// 25.7 / 20.5; one adapter: 32 / 256 rows 14.3 / 24.9, as many 13.1 / 12.9; 4096 -> 14336, rank 64, 8
+// adapters: 128 / 256 rows 24 / 40.6, as many 27.1 / 24.  A's rows are reached by 32-bit distances.)
+bool few_rows(const AdapterLaunch &L) {
+  return L.tokens <= 256 && L.tokens <= 16 * (int64_t)L.adapters && L.rank * L.in < (int64_t)1 << 29;
+}
 
 // Parts of the long dimension, for about 512 workgroups, each wave with 8 KB or more of an
 // adapter's weights.
