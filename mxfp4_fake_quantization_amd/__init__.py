@@ -21,6 +21,9 @@ argument and enqueue on torch's current stream:
     mxfp4_dequant(codes, scales, y, block=32)
     mxfp8_quant(x, q, scales, fmt="e4m3")
 
+The mixture-of-experts calls are in moe_ops.py, those of the low-rank adapters and
+of the gradient norm in adapter_ops.py.
+
 Tensor conventions: x / y / grads are bfloat16 or float32, 2-D contiguous
 (higher ranks are viewed as rows x last-dim); bitmaps are int32 tensors (the
 uint32 bit patterns); scales and codes are uint8; group_list is int64 on the
