@@ -172,6 +172,22 @@ def test_backward(size, pattern, dt):
         assert torch.equal(alone, out[k])
 
 
+@pytest.mark.parametrize("dt", [bf16, f32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("pattern", ["null", "last", "runs"])
+@pytest.mark.parametrize("size", [(200, 256, 208, 8, 30), (256, 160, 96, 24, 16), (190, 129, 131, 50, 64), (61, 520, 72, 128, 5)],
+                         ids=str)
+def test_few_rows_of_one(size, pattern, dt):
+    """Few rows to many adapters, of which one has all or most of them: several tiles of rows a workgroup."""
+    p = Problem(*size, pattern, dt)
+    y, u = torch.empty_like(p.base), torch.empty(size[0], size[3], device="cuda")
+    M.mxfp4_adapter_fwd(p.x, p.a, p.b, y, ids=p.ids, scale=p.scale, base=p.base, u=u)
+    wy, ey, wu, eu = p.forward64(True, True)
+    within(y, wy, ey)
+    within(u, wu, eu)
+    M.mxfp4_adapter_fwd(p.x, p.a, p.b, p.base, ids=p.ids, scale=p.scale, base=p.base)
+    assert torch.equal(p.base, y)                     # in place
+
+
 # rows of x, W or u shorter than 16 bytes, the other dimension whole blocks of the kernels
 SHORT = [(200, 4, 128, 2, 3), (300, 6, 512, 3, 2), (70, 3, 64, 1, 2), (40, 512, 3, 5, 2), (500, 1, 1, 7, 3), (1, 2, 256, 1, 1)]
 
