@@ -16,7 +16,8 @@ namespace {
 // at once) and a part of the long dimension (u) or of the columns (y).
 // One launch that computed u again for every part of the columns read A once a part
 // through each CU's L1 at 64 bytes a clock: 64 tokens of 48 adapters, 8192 -> 28672, rank
-// 16 took 51 us, one token 4096 -> 4096 9.4.
+// 16 took 51 us (two launches 7 + 19, 46 MB of B at 2.5 TB/s), one token 4096 -> 4096 9.4
+// (3.6 + 4.8).
 
 struct FewArgs {
   const uint8_t *x, *a, *b;
@@ -198,14 +199,16 @@ struct Quad {  // four consecutive elements of a row
   }
 };
 
-constexpr int few_tiles(int rt) { return rt <= 2 ? 8 : 4; }  // of a run, as the registers allow
+// Tiles of a run.  (8 up to rank 32: one token 6 us instead of 4.8, 32 / 128 / 256 rows of 48 adapters, 4096 ->
+// 4096, both kernels 10 / 11.8 / 13.5 instead of 9.1 / 11.1 / 12.3.)
+constexpr int kFewTiles = 4;
 
 template <int DT, int RT, int MODE>
 __device__ __forceinline__ void few_y(const FewArgs &A, const FewRows &R,
                                       u32x4 (*us)[Expand<DT, frag_count<DT>(RT), false, MODE>::UF][64], int lane, int wave) {
   using T = Tile<DT>;
   using X = Expand<DT, frag_count<DT>(RT), false, MODE>;
-  constexpr int F = X::F, TILES = few_tiles(RT), COLS = 16 * TILES;
+  constexpr int F = X::F, TILES = kFewTiles, COLS = 16 * TILES;
   const int i = lane & 15, q = lane >> 4, own = R.own, n = R.n;
   const int64_t runs = (A.out + COLS - 1) / COLS;
   const int64_t first = blockIdx.y * kFewWaves + wave, step = kFewWaves * A.parts;
@@ -352,7 +355,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void adapter_few_y_kernel(FewArgs A
 }
 
 // Few rows, and few of an adapter: up to 16 on average, one tile; the weights' reading is all there is.
-// (4096 -> 4096, rank 16, 48 adapters: 32 / 256 / 512 rows take 10 / 13.2 / 21.1 us, as many rows 42 /
+// (4096 -> 4096, rank 16, 48 adapters: 32 / 256 / 512 rows take 9.1 / 12.3 / 21.1 us, as many rows 42 /
 // 25.7 / 20.5; one adapter: 32 / 256 rows 14.3 / 24.9, as many 13.1 / 12.9; 4096 -> 14336, rank 64, 8
 // adapters: 128 / 256 rows 24 / 40.6, as many 27.1 / 24.  A's rows are reached by 32-bit distances.)
 bool few_rows(const AdapterLaunch &L) {
@@ -366,17 +369,19 @@ int few_splits(const AdapterLaunch &L) {
   const int64_t useful = (L.in * L.rank * (L.dtype == kBF16 ? 2 : 4) + 8192 * kFewWaves - 1) / (8192 * kFewWaves);
   int64_t s = most > 0 ? 512 / most : 1;
   if (s > useful) s = useful;
-  const int cap = L.rank <= 32 ? 4 : 12;  // (y's kernel adds the parts up)
+  // y's kernel adds the parts up (48 adapters, rank 16, 8192 -> 28672: u + y 7 + 18.7 us, up to 8 parts
+  // 6.8 + 20.8, 2 parts 8 + 18.1; one token 3.6 + 6, 3.6 + 6, 4.6 + 5.6)
+  const int cap = L.rank <= 32 ? 4 : 12;
   if (s > cap) s = cap;
   return s < 1 ? 1 : (int)s;
 }
 
 template <int DT>
 hipError_t launch_few(const AdapterLaunch &L, hipStream_t stream) {
-  const int cols = 16 * few_tiles((L.rank + 15) / 16);
+  const int cols = 16 * kFewTiles;
   const int64_t most = L.adapters < L.tokens ? L.adapters : L.tokens;
   const int64_t useful = ((L.out + cols - 1) / cols + kFewWaves - 1) / kFewWaves;
-  int64_t parts = 2048 / most;
+  int64_t parts = 2048 / most;  // (48 adapters, out 28672: 19 us; twice as many 20.4, two thirds 20.5)
   if (parts > useful) parts = useful;
   if (parts < 1) parts = 1;
   const int splits = few_splits(L), mode = piece_mode(DT, L.tokens, L.in, L.out, L.rank);
