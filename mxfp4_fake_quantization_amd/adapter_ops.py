@@ -213,7 +213,8 @@ def _items(grads, outs, write):
         _pack = pack
     if isinstance(grads, torch.Tensor) or isinstance(outs, torch.Tensor):
         raise TypeError("grads and outs are lists of tensors")
-    return _pack(grads, outs, torch.cuda.current_device() if torch.cuda.is_available() else -1, write)
+    gpu = torch.cuda.is_initialized() or torch.cuda.is_available()  # (the second one asks the driver)
+    return _pack(grads, outs, torch.cuda.current_device() if gpu else -1, write)
 
 
 def _norm_type(p) -> int:
