@@ -178,7 +178,9 @@ __device__ __forceinline__ int64_t xcd_share(int64_t id, int64_t total) {
 // rank's weights at a time go through LDS (two buffers, the next block's loads in
 // flight during a block's products): global reads are 256 consecutive bytes of a
 // row, and the weights are read once for all four waves.  Piece p of LDS row r lies
-// at p ^ (r % 16), which spreads a fragment's 16 rows over all banks.
+// at p ^ (r % 16), which spreads a fragment's 16 rows over all banks.  Bound by reading x
+// (8192 x 7168 bf16, 16 adapters of rank 32: 35 us, 3.6 TB/s; 4096 x 4096 fp32, rank 8:
+// 14.4 us, 4.7 TB/s).
 //
 // Windows of several adapters: workgroup `slot` of a window takes every slots-th of
 // its adapters.
@@ -384,6 +386,8 @@ __device__ __forceinline__ float parts_sum(const float *u, int64_t part, int spl
 // (the wave's 16 KB) and u, of which wave w makes the fragments of rows 16 w to 16 w +
 // 15 for all.  Then the adapters of the window pass one after the other; a row takes
 // the result of its own one, so that no other adapter's values (an infinity, say) reach it.
+// Bound by the bytes of base and y: 8192 x 7168 bf16, rank 32 50.5 us (4.8 TB/s), 4096 x 4096
+// fp32, rank 8 27.5 us (4.9 TB/s), both with their base.
 // Rows of a workgroup: 64, with the 16-byte pieces of 128 columns a row; 32 in fp32, whose registers
 // then leave room for a wave more (4096 rows, 4096 columns, rank 8: 28.8 us, with 64 rows 31.2;
 // bf16, 8192 rows, 7168 columns, rank 32: 59.4 with 32 rows, 55.2 with 64).
@@ -557,7 +561,8 @@ inline int shrink_splits(int64_t tokens, int64_t K) {
   return s < 1 ? 1 : (int)s;
 }
 
-// Workgroups that share a window's adapters.
+// Workgroups that share a window's adapters: up to 2048 workgroups in all, of which those beyond a
+// window's adapters end at once (1531 rows of 24 adapters 13.6 us, with 1024 13.2; 8192 rows of 16 alike).
 inline int shrink_slots(int64_t tokens, int adapters, int splits) {
   const int64_t windows = window_count(tokens);
   int64_t s = 2048 / ((windows > 0 ? windows : 1) * splits);

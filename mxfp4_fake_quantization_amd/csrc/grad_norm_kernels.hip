@@ -3,7 +3,8 @@
 //     norm = (sum over all tensors of |g|^p)^(1/p), p = 1 or 2, or max |g|;
 //     out  = g * min(1, max_norm / (norm + 1e-6)).
 // Bound by the bytes: the gradients once for the norm, once more (from the 256 MB
-// cache, where they fit) and written once for clipping.  Sums are held in 64 bits
+// cache, where they fit) and written once for clipping (235 MB 38 us, 6.2 TB/s; 1.9 GB in
+// and out 281 + 773 us, 6.7 and 4.9 TB/s).  Sums are held in 64 bits
 // throughout: the squares of any fp32 values neither overflow nor vanish, and the
 // matrix-free arithmetic of two double operations an element hides behind the
 // loads.  A workgroup sums a contiguous run of chunks and writes one partial sum;
