@@ -16,7 +16,7 @@ namespace {
 // every fourth step of KF rows.  The sum runs down the rows of both operands, so a
 // lane loads PE rows of 16 bytes and turns them in registers (one v_perm per two
 // bf16 elements, no LDS): its 16 bytes are then column PE l + j of fragment j.
-// v, in fp32, is split into two bf16 operands as in the other products.  Bound by the
+// v, in fp32, is split into three bf16 operands as in the other products.  Bound by the
 // bytes of x and grad_y: 16384 tokens, 4096 -> 4096, rank 16 50 us (5.4 TB/s); 8191
 // tokens, 7168 -> 2048, rank 64 55 us (2.8 TB/s: v, split for four tiles of ranks, takes the
 // rest of the time).
@@ -88,26 +88,26 @@ __global__ __launch_bounds__(64 * kGradWaves) void adapter_grad_kernel(GradArgs 
           for (int r = 0; r < RT; ++r) v[r][e] = 0.0f;
         }
     }
-    u32x4 hi[RT], lo[RT];
+    u32x4 vf[DT == kBF16 ? 3 : 1][RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int r = 0; r < RT; ++r) {
+      if constexpr (DT == kBF16) {
+        const Parts p = parts_of(v[r]);
+        vf[0][r] = p.hi;
+        vf[1][r] = p.mid;
+        vf[2][r] = p.lo;
+      } else {
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        if constexpr (DT == kBF16) {
-          hi[r][d] = pack_hi(v[r][2 * d], v[r][2 * d + 1]);
-          lo[r][d] = pack_lo(v[r][2 * d], v[r][2 * d + 1]);
-        } else {
-          hi[r][d] = __builtin_bit_cast(uint32_t, v[r][d]);
-        }
+        for (int d = 0; d < 4; ++d) vf[0][r][d] = __builtin_bit_cast(uint32_t, v[r][d]);
       }
+    }
 #pragma unroll
     for (int j = 0; j < T::PE; ++j) {
       const u32x4 zf = turned<DT>(z, j);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        acc[r][j] = mma<DT>(hi[r], zf, acc[r][j]);
-        if constexpr (DT == kBF16) acc[r][j] = mma<DT>(lo[r], zf, acc[r][j]);
-      }
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (auto &part : vf) acc[r][j] = mma<DT>(part[r], zf, acc[r][j]);
     }
   }
   // the waves' sums, 16 ranks at a time

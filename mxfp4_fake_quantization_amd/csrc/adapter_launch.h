@@ -501,13 +501,11 @@ __global__ __launch_bounds__(64 * kExpandWaves, (kExpandOccupancy<DT, NF>)) void
     for (int j = 0; j < TILES; ++j) {
       const uint32_t here = (uint32_t)(match >> (16 * j)) & 0xFFFFu;
       if (!here) continue;
-      u32x4 uf[X::UF];
-#pragma unroll
-      for (int f = 0; f < X::UF; ++f) uf[f] = us[j][f][lane];
 #pragma unroll
       for (int h = 0; h < T::PE; h += 4) {  // four tiles at a time, for the registers
+        __builtin_amdgcn_sched_barrier(0);  // (fragments of several tiles at once: up to five registers spilled)
         f32x4 acc[4];
-        W.product(acc, uf, h);
+        W.product(acc, h, [&](int f) { return us[j][f][lane]; });
         if (here == 0xFFFFu) {
 #pragma unroll
           for (int v = 0; v < 4; ++v) add_products<DT>(out[j][v], acc, h, v);
