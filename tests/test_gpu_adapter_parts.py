@@ -125,3 +125,74 @@ def test_weight_gradients(size, dt):
     M.mxfp4_adapter_bwd(dev(gy_u), a, b, u=u.float().cuda(), ids=ids, grad_b=gb)
     want, bound = want_b.cuda(), size_b.cuda()
     within(gb, want, 8 * E * bound + half(dt) * want.abs())
+
+
+def as_formula(got, terms, base=0.0):
+    """The infinities and NaN of the sum of the last dimension's terms (in 64 bits), and its finite values
+    within 2^-8 of a bf16 result and (6 m + 64) 2^-23 of the m terms' magnitudes: three products a term,
+    each an addition and its rounding, and the waves' parts."""
+    want = base + terms.sum(-1)
+    got, m = got.double().cpu(), terms.shape[-1]
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.isinf(), want.isinf()) and torch.equal(got[want.isinf()], want[want.isinf()])
+    ok = want.isfinite()
+    bound = 2.0 ** -8 * want.abs() + (6 * m + 64) * E * (abs(base) + terms.abs().sum(-1))
+    assert bool(((got - want).abs()[ok] <= bound[ok]).all())
+
+
+@pytest.mark.parametrize("dt", [bf16, f32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("size", [(5, 64, 72, 16, 2), (40, 136, 65, 7, 3), (30, 72, 130, 24, 4), (50, 128, 128, 100, 4),
+                                  (300, 64, 130, 16, 3), (300, 96, 136, 24, 2), (150, 130, 66, 40, 3), (200, 192, 96, 96, 2)], ids=str)
+def test_infinite_operands(size, dt):
+    """Infinities in weights and rows beside values of few bits, whose lower parts are 0 if nothing is
+    borrowed: y, grad_x, grad_a and grad_b are what the formula gives."""
+    tokens, n_in, n_out, rank, adapters = size
+    g = torch.Generator().manual_seed(tokens + rank)
+    ids = torch.randint(0, adapters, (tokens,), generator=g)
+    dev = lambda m: m.to(dt).cuda()  # noqa: E731
+
+    def few_bits(*shape):
+        return torch.tensor([0.0, 1.0, -2.0, 0.5, 3.0, 1.0, -1.0, 0.125])[torch.randint(0, 8, shape, generator=g)].double()
+
+    def with_infinities(*shape, rate):
+        v = few_bits(*shape)
+        at = torch.rand(*shape, generator=g)
+        v[at < rate] = float("inf")
+        v[at > 1 - rate] = -float("inf")
+        return v
+
+    def ones(cols):  # [adapters, rank, cols]: rank r takes column r (from the first again past the last)
+        w = torch.zeros(adapters, rank, cols).double()
+        w[:, torch.arange(rank), torch.arange(rank) % cols] = 1
+        return w
+
+    def picked(v):   # v times ones() of the same columns
+        return v[:, torch.arange(rank) % v.shape[1]]
+
+    rate = 0.6 / rank
+    i = ids.to(torch.int32).cuda()
+    x, base, b = few_bits(tokens, n_in), few_bits(tokens, n_out), with_infinities(adapters, n_out, rank, rate=rate)
+    y = torch.empty(tokens, n_out, dtype=dt, device="cuda")
+    M.mxfp4_adapter_fwd(dev(x), dev(ones(n_in)), dev(b), y, ids=i, base=dev(base))
+    as_formula(y, picked(x)[:, None, :] * b[ids], base)
+    gy, a = few_bits(tokens, n_out), with_infinities(adapters, rank, n_in, rate=rate)
+    one = ones(n_out).transpose(1, 2).contiguous()
+    gx = torch.empty(tokens, n_in, dtype=dt, device="cuda")
+    M.mxfp4_adapter_bwd(dev(gy), dev(a), dev(one), ids=i, grad_x=gx)
+    as_formula(gx, picked(gy)[:, None, :] * a[ids].transpose(1, 2))
+    # a weight gradient's infinities: values that are not 0, that they stay infinities
+    v = few_bits(tokens, n_out)
+    v[v == 0] = 1
+    rows = with_infinities(tokens, n_in, rate=0.3 / tokens)
+    ga = torch.empty(adapters, rank, n_in, dtype=dt, device="cuda")
+    M.mxfp4_adapter_bwd(dev(v), dev(a), dev(one), x=dev(rows), ids=i, grad_a=ga)
+    u = few_bits(tokens, rank)
+    u[u == 0] = 1
+    gr = with_infinities(tokens, n_out, rate=0.3 / tokens)
+    gb = torch.empty(adapters, n_out, rank, dtype=dt, device="cuda")
+    M.mxfp4_adapter_bwd(dev(gr), dev(a), dev(one), u=u.float().cuda(), ids=i, grad_b=gb)
+    for e in range(adapters):
+        at = ids == e
+        as_formula(ga[e], (picked(v)[at][:, :, None] * rows[at][:, None, :]).movedim(0, -1))
+        as_formula(gb[e], (gr[at][:, :, None] * u[at][:, None, :]).movedim(0, -1))
+    assert ga.isinf().any() and gb.isinf().any() and y.isinf().any() and gx.isinf().any()
