@@ -129,12 +129,30 @@ class _PackedProduct(torch.autograd.Function):
         return gx.view(*gy.shape[:-1], layer.in_features), None
 
 
-class PackedLinear(nn.Module):
+class _Float32Kept(nn.Module):
+    """A module whose buffers named in ``_kept`` stay float32 when it is cast: the
+    library takes them in float32."""
+
+    _kept = ()
+
+    def _apply(self, fn, recurse=True):
+        before = {name: getattr(self, name) for name in self._kept}
+        super()._apply(fn, recurse)
+        for name, t in before.items():
+            now = getattr(self, name)
+            if now is not None and now.dtype != torch.float32:
+                setattr(self, name, t.to(now.device, torch.float32))
+        return self
+
+
+class PackedLinear(_Float32Kept):
     """A linear layer with its weight in MXFP4 along the inputs, quantized once;
     inputs go through MXFP8 (W4A8).  The weight is not trained.  With ``backward``
     a second copy, quantized along the outputs, gives the gradient of the input as
     the mixture-of-experts layer does (gradients through MXFP8).  in and out features
-    are multiples of 32; x is bfloat16."""
+    are multiples of 32; x is bfloat16.  The bias stays float32 through casts."""
+
+    _kept = ("bias",)
 
     def __init__(self, weight, bias=None, backward: bool = False):
         super().__init__()

@@ -1,0 +1,35 @@
+"""The adapters' modules as programs hold them: cast to another type, built under another
+default type, under autocast.  On the CPU what needs no kernel, on the GPU the rest."""
+import pytest
+import torch
+from torch import nn
+
+import mxfp4_fake_quantization_amd as M
+from mxfp4_fake_quantization_amd import adapters as AD
+
+bf16, f32 = torch.bfloat16, torch.float32
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    M._load()
+
+
+@gpu
+@pytest.mark.parametrize("cast", ["bfloat16", "half", "double", "to"])
+def test_packed_bias_through_casts(lib, cast):
+    """The bias is the float32 one before and after a cast: the same bits."""
+    torch.manual_seed(3)
+    layer = AD.PackedLinear.pack(nn.Linear(64, 96, device="cuda", dtype=f32), backward=True)
+    x = torch.randn(5, 64, device="cuda").to(bf16)
+    want, bias = layer(x), layer.bias.clone()
+    same = layer.to(bf16) if cast == "to" else getattr(layer, cast)()
+    assert same is layer and layer.bias.dtype == f32 and torch.equal(layer.bias, bias)
+    assert torch.equal(layer(x), want)
+    layer.cpu().cuda()
+    assert torch.equal(layer(x), want)
+    no_bias = AD.PackedLinear.pack(nn.Linear(64, 96, bias=False, device="cuda")).to(bf16)
+    assert no_bias.bias is None and no_bias(x).shape == (5, 96)
