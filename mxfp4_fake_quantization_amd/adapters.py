@@ -88,9 +88,28 @@ def adapter_add(x, base, a, b, ids: Optional[torch.Tensor] = None, scale: Option
     return _AdapterAdd.apply(x, base, a.to(x.dtype), b.to(x.dtype), ids, scale)
 
 
-class Adapters(nn.Module):
+class _Float32Kept(nn.Module):
+    """A module whose buffers named in ``_kept`` stay float32 when it is cast: the
+    library takes them in float32."""
+
+    _kept = ()
+
+    def _apply(self, fn, recurse=True):
+        before = {name: getattr(self, name) for name in self._kept}
+        super()._apply(fn, recurse)
+        for name, t in before.items():
+            now = getattr(self, name)
+            if now is not None and now.dtype != torch.float32:
+                setattr(self, name, t.to(now.device, torch.float32))
+        return self
+
+
+class Adapters(_Float32Kept):
     """``adapters`` low-rank adapters of one projection.  A starts random, B at 0, so
-    that a fresh adapter adds nothing; the scales alpha / rank are a buffer."""
+    that a fresh adapter adds nothing; the scales alpha / rank are a buffer, float32
+    through casts."""
+
+    _kept = ("scale",)
 
     def __init__(self, in_features: int, out_features: int, adapters: int = 1, rank: int = 16,
                  alpha: Optional[float] = None, *, device=None, dtype=torch.bfloat16):
@@ -127,22 +146,6 @@ class _PackedProduct(torch.autograd.Function):
         if g.shape[0]:
             mxfp4_grouped_matmul(*_mxfp8(g), codes, scales, gx, K=layer.out_features)
         return gx.view(*gy.shape[:-1], layer.in_features), None
-
-
-class _Float32Kept(nn.Module):
-    """A module whose buffers named in ``_kept`` stay float32 when it is cast: the
-    library takes them in float32."""
-
-    _kept = ()
-
-    def _apply(self, fn, recurse=True):
-        before = {name: getattr(self, name) for name in self._kept}
-        super()._apply(fn, recurse)
-        for name, t in before.items():
-            now = getattr(self, name)
-            if now is not None and now.dtype != torch.float32:
-                setattr(self, name, t.to(now.device, torch.float32))
-        return self
 
 
 class PackedLinear(_Float32Kept):

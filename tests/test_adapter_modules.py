@@ -33,3 +33,14 @@ def test_packed_bias_through_casts(lib, cast):
     assert torch.equal(layer(x), want)
     no_bias = AD.PackedLinear.pack(nn.Linear(64, 96, bias=False, device="cuda")).to(bf16)
     assert no_bias.bias is None and no_bias(x).shape == (5, 96)
+
+
+@pytest.mark.parametrize("cast", ["bfloat16", "half", "double", "to"])
+def test_scale_through_casts(cast):
+    """alpha / rank, 4 / 3 here, stays the float32 value."""
+    layer = nn.Sequential(AD.Adapters(16, 24, adapters=3, rank=12, alpha=16.0, dtype=f32))
+    layer.to(bf16) if cast == "to" else getattr(layer, cast)()
+    scale = layer[0].scale
+    assert scale.dtype == f32 and scale.tolist() == [torch.tensor(16 / 12, dtype=f32).item()] * 3
+    assert layer[0].a.dtype == {"bfloat16": bf16, "to": bf16, "half": torch.float16, "double": torch.float64}[cast]
+    assert dict(layer.named_buffers())["0.scale"] is scale and "0.scale" in layer.state_dict()
