@@ -49,7 +49,9 @@ class _AdapterAdd(torch.autograd.Function):
         xr, br = _rows(x), _rows(base)
         a, b = a.contiguous(), b.contiguous()
         y = torch.empty(br.shape, dtype=base.dtype, device=base.device)
-        u = torch.empty(xr.shape[0], a.shape[1], device=x.device) if ctx.needs_input_grad[3] else None
+        u = None
+        if ctx.needs_input_grad[3]:
+            u = torch.empty(xr.shape[0], a.shape[1], dtype=torch.float32, device=x.device)
         mxfp4_adapter_fwd(xr, a, b, y, ids=ids, scale=scale, base=br, u=u)
         ctx.shape = x.shape
         ctx.save_for_backward(xr if ctx.needs_input_grad[2] else None, a, b, ids, scale, u)
@@ -118,7 +120,8 @@ class Adapters(_Float32Kept):
         self.a = nn.Parameter(torch.empty(adapters, rank, in_features, device=device, dtype=dtype))
         self.b = nn.Parameter(torch.zeros(adapters, out_features, rank, device=device, dtype=dtype))
         scale = (rank if alpha is None else alpha) / rank
-        self.register_buffer("scale", torch.full((adapters,), float(scale), device=device))
+        self.register_buffer("scale", torch.full((adapters,), float(scale), dtype=torch.float32,
+                                                  device=device))
         nn.init.kaiming_uniform_(self.a.view(adapters * rank, in_features), a=math.sqrt(5))
 
     def forward(self, x, base, ids: Optional[torch.Tensor] = None):

@@ -270,8 +270,8 @@ def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0,
         parameters = [parameters]
     grads = [p.grad for p in parameters if p.grad is not None]
     if not grads:
-        return torch.tensor(0.0)
-    norm = torch.empty((), device=grads[0].device)
+        return torch.tensor(0.0, dtype=torch.float32)
+    norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
     if error_if_nonfinite:
         mxfp4_grad_norm(grads, norm, norm_type=norm_type)
         if not bool(torch.isfinite(norm)):

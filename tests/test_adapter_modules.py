@@ -44,3 +44,43 @@ def test_scale_through_casts(cast):
     assert scale.dtype == f32 and scale.tolist() == [torch.tensor(16 / 12, dtype=f32).item()] * 3
     assert layer[0].a.dtype == {"bfloat16": bf16, "to": bf16, "half": torch.float16, "double": torch.float64}[cast]
     assert dict(layer.named_buffers())["0.scale"] is scale and "0.scale" in layer.state_dict()
+
+
+@pytest.fixture(params=[bf16, torch.float64], ids=["bf16", "f64"])
+def default_type(request):
+    """Another default type, as programs set it while they build a model."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(request.param)
+    yield request.param
+    torch.set_default_dtype(before)
+
+
+def test_scale_under_a_default_type(default_type):
+    scale = AD.Adapters(16, 24, adapters=2, rank=12, alpha=16.0).scale
+    assert scale.dtype == f32 and scale.tolist() == [torch.tensor(16 / 12, dtype=f32).item()] * 2
+
+
+def test_no_gradients_under_a_default_type(default_type):
+    from mxfp4_fake_quantization_amd import qat
+    norm = qat.clip_grad_norm_([nn.Parameter(torch.zeros(3))], 1.0)
+    assert norm.dtype == f32 and float(norm) == 0.0
+
+
+@gpu
+def test_training_under_a_default_type(lib, default_type):
+    """Gradients and clipping are what they are under float32, bit for bit."""
+    from mxfp4_fake_quantization_amd import qat
+
+    def step():
+        torch.manual_seed(6)
+        layer = AD.AdapterLinear(nn.Linear(64, 96, device="cuda", dtype=bf16), adapters=2, rank=12, alpha=16.0)
+        nn.init.normal_(layer.adapters.b, std=0.3)
+        x = torch.randn(9, 64, device="cuda", dtype=f32).to(bf16)
+        layer(x, torch.arange(9, device="cuda", dtype=torch.int32) % 3 - 1).float().square().sum().backward()
+        norm = qat.clip_grad_norm_(layer.parameters(), 0.5)
+        assert norm.dtype == f32
+        return [norm, *(p.grad for p in layer.parameters())]
+
+    got = step()
+    torch.set_default_dtype(f32)
+    assert all(torch.equal(a, b) for a, b in zip(got, step()))
