@@ -112,7 +112,7 @@ def _mxfp8_t(x, group_list):
 
 def _route(logits, spec, balance):
     tokens, experts = logits.shape
-    weights = torch.empty(tokens, spec.k, device=logits.device)
+    weights = torch.empty(tokens, spec.k, dtype=torch.float32, device=logits.device)
     ids = torch.empty(tokens, spec.k, dtype=torch.int32, device=logits.device)
     mxfp4_moe_route(logits, weights, ids, bias=balance, score=spec.score, num_groups=spec.num_groups,
                     topk_groups=spec.topk_groups, renormalize=spec.renormalize, scale=spec.scale)
@@ -194,8 +194,8 @@ class _MoEFFN(torch.autograd.Function):
             dlogits = torch.empty_like(logits)
             mxfp4_moe_route_bwd(dweights, logits, ids, dlogits, score=spec.score, renormalize=spec.renormalize,
                                 scale=spec.scale)
-        db1 = torch.empty(experts, w1.shape[1], device=dy.device) if need_b1 else None
-        db2 = torch.empty(experts, w2.shape[1], device=dy.device) if need_b2 else None
+        db1 = torch.empty(experts, w1.shape[1], dtype=torch.float32, device=dy.device) if need_b1 else None
+        db2 = torch.empty(experts, w2.shape[1], dtype=torch.float32, device=dy.device) if need_b2 else None
         if need_b2:
             mxfp4_act_bwd(dh, h, dh, act="none", grad_bias=db2, group_list=group_list)
 
@@ -246,8 +246,8 @@ class MoELayer(nn.Module):
         self.router = nn.Linear(hidden, experts, bias=False, device=device, dtype=dtype)
         self.w1 = nn.Parameter(torch.empty(experts, rows, hidden, device=device, dtype=dtype))
         self.w2 = nn.Parameter(torch.empty(experts, hidden, inner, device=device, dtype=dtype))
-        self.b1 = nn.Parameter(torch.zeros(experts, rows, device=device)) if bias else None
-        self.b2 = nn.Parameter(torch.zeros(experts, hidden, device=device)) if bias else None
+        self.b1 = nn.Parameter(torch.zeros(experts, rows, device=device, dtype=torch.float32)) if bias else None
+        self.b2 = nn.Parameter(torch.zeros(experts, hidden, device=device, dtype=torch.float32)) if bias else None
         nn.init.normal_(self.w1, std=hidden ** -0.5)
         nn.init.normal_(self.w2, std=inner ** -0.5)
 
