@@ -254,12 +254,16 @@ class MoELayer(nn.Module):
     def forward(self, x):
         flat = x.reshape(-1, x.shape[-1])
         logits = F.linear(flat.to(self.router.weight.dtype), self.router.weight)
-        y = moe_ffn(flat, logits, self.w1, self.w2, self.spec, self.b1, self.b2)
+        y = moe_ffn(flat, logits, self.w1, self.w2, self.spec, *self._biases())
         return x + y.view(x.shape)
 
     def packed(self) -> PackedExperts:
         """The experts' present weights, quantized for serving."""
-        return PackedExperts(self.w1.detach(), self.w2.detach(), self.spec, self.b1, self.b2)
+        return PackedExperts(self.w1.detach(), self.w2.detach(), self.spec, *self._biases())
+
+    def _biases(self):
+        """As the products take them, whatever type a cast of the module gave them."""
+        return (None if b is None else b.float() for b in (self.b1, self.b2))
 
     def extra_repr(self) -> str:
         return f"experts={self.w1.shape[0]}, spec={self.spec}"

@@ -44,3 +44,24 @@ def test_under_a_default_type(default):
     finally:
         torch.set_default_dtype(before)
     assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+def test_biases_after_a_cast():
+    """A layer cast to bfloat16 is the layer of the rounded biases; their gradients are theirs, rounded."""
+    torch.manual_seed(9)
+    layer = MOE.MoELayer(64, 96, 4, MOE.MoESpec(k=2), bias=True, device="cuda", dtype=bf16)
+    for b in (layer.b1, layer.b2):
+        b.data.copy_(torch.randn(b.shape, device="cuda").to(bf16))
+    x = torch.randn(13, 64, device="cuda").to(bf16)
+    y = layer(x)
+    y.float().square().sum().backward()
+    want = [p.grad.clone() for p in layer.parameters()]
+    packed = layer.packed()(x, x @ layer.router.weight.t())
+    layer.zero_grad(set_to_none=True)
+    layer.to(bf16)
+    assert layer.b1.dtype == bf16
+    again = layer(x)
+    again.float().square().sum().backward()
+    assert torch.equal(again, y)
+    assert all(torch.equal(p.grad, g.to(bf16)) for p, g in zip(layer.parameters(), want))
+    assert torch.equal(layer.packed()(x, x @ layer.router.weight.t()), packed)
