@@ -76,9 +76,12 @@ def adapter_add(x, base, a, b, ids: Optional[torch.Tensor] = None, scale: Option
     x's leading shape; None: adapter 0; outside [0, adapters): none).  base is
     [..., out] of x's type, a [adapters, rank, in], b [adapters, out, rank], scale
     float32 [adapters].  Gradients reach x, base, a and b (of up to 1024 adapters);
-    second derivatives, and a scale that wants a gradient, are refused."""
+    second derivatives, and a scale that wants a gradient, are refused.  Under autocast
+    x is taken in base's type."""
     if x.dim() < 1 or base.dim() != x.dim() or base.shape[:-1] != x.shape[:-1]:
         raise ValueError(f"base must have x's leading shape {list(x.shape[:-1])}, got {list(base.shape)}")
+    if base.dtype != x.dtype and torch.is_autocast_enabled("cuda"):
+        x = x.to(base.dtype)  # as the projection took it
     if base.dtype != x.dtype:
         raise ValueError(f"base must have x's type {x.dtype}, got {base.dtype}")
     if scale is not None and scale.requires_grad and torch.is_grad_enabled():
@@ -191,6 +194,8 @@ class PackedLinear(_Float32Kept):
         return y.view(*x.shape[:-1], self.out_features)
 
     def forward(self, x):
+        if torch.is_autocast_enabled("cuda") and torch.get_autocast_dtype("cuda") == torch.bfloat16:
+            x = x.to(torch.bfloat16)  # as a projection in float does
         if x.dtype != torch.bfloat16 or x.shape[-1] != self.in_features:
             raise ValueError(f"x must be a bfloat16 tensor [..., {self.in_features}]")
         return _PackedProduct.apply(x, self)

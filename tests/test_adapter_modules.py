@@ -84,3 +84,56 @@ def test_training_under_a_default_type(lib, default_type):
     got = step()
     torch.set_default_dtype(f32)
     assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+def projection(name, n_in, n_out, dtype):
+    from mxfp4_fake_quantization_amd import qat
+    torch.manual_seed(4)
+    linear = nn.Linear(n_in, n_out, device="cuda", dtype=dtype)
+    if name == "linear":
+        return linear
+    return AD.PackedLinear.pack(linear, backward=True) if name == "packed" else qat.QATLinear.wrap(linear, qat.QATPolicy.w4a4())
+
+
+@gpu
+@pytest.mark.parametrize("name", ["linear", "qat", "packed"])
+def test_autocast(lib, name):
+    """Under autocast a projection makes bfloat16 of a float32 input; the adapters beside it take the input so too:
+    the bits and gradients of the call on the rounded input, the input's gradient in its type."""
+    layer = AD.AdapterLinear(projection(name, 64, 96, f32), adapters=2, rank=8, dtype=f32)
+    nn.init.normal_(layer.adapters.b, std=0.3)
+    x = torch.randn(3, 7, 64, device="cuda", requires_grad=True)
+    ids = (torch.arange(21, device="cuda", dtype=torch.int32) % 3 - 1).view(3, 7)
+    adapters = list(layer.adapters.parameters())
+    with torch.autocast("cuda", dtype=bf16):
+        y = layer(x, ids)
+    assert y.dtype == bf16
+    gy = torch.randn(3, 7, 96, device="cuda").to(bf16)
+    grads = torch.autograd.grad(y, [x, *adapters], gy)
+    assert [g.dtype for g in grads] == [f32, f32, f32]
+    # by hand: the projection under autocast, the adapters on the rounded input
+    v = x.detach().requires_grad_()
+    with torch.autocast("cuda", dtype=bf16):
+        base = layer.base(v.to(bf16) if name == "packed" else v)
+    want = layer.adapters(v.to(bf16), base, ids)
+    assert torch.equal(y, want)
+    for a, b in zip(grads, torch.autograd.grad(want, [v, *adapters], gy)):
+        assert torch.equal(a, b)
+    # mixed types outside autocast are still refused
+    with pytest.raises(ValueError):
+        layer.adapters(v, base, ids)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [bf16, f32], ids=["bf16", "f32"])
+def test_beside_a_fake_quantized_projection(lib, dt):
+    """QATLinear as the base: its output and gradients, and the adapters' beside them."""
+    layer = AD.AdapterLinear(projection("qat", 64, 96, dt), adapters=3, rank=4, dtype=dt)
+    x = torch.randn(11, 64, device="cuda").to(dt).requires_grad_()
+    ids = torch.arange(11, device="cuda", dtype=torch.int32) % 3
+    gy = torch.randn(11, 96, device="cuda").to(dt)
+    gw, gx = torch.autograd.grad(layer.base(x), [layer.base.weight, x], gy)
+    y = layer(x, ids)                               # B is 0: it adds nothing
+    assert torch.equal(y, layer.base(x))
+    got = torch.autograd.grad(y, [layer.base.weight, x, layer.adapters.b], gy)
+    assert torch.equal(got[0], gw) and torch.equal(got[1], gx) and got[2].abs().sum() > 0
