@@ -201,6 +201,14 @@ def mxfp4_adapter_bwd(grad_y, a, b, x=None, u=None, ids=None, scale=None, grad_x
 _pack = None
 
 
+def _listed(tensors):
+    """A list that the caller holds until the kernels are under way: a generator's tensors
+    would be freed once their addresses are taken, and the workspace allocated over them."""
+    if isinstance(tensors, torch.Tensor):
+        raise TypeError("grads and outs are lists of tensors")
+    return tensors if tensors is None or isinstance(tensors, (list, tuple)) else list(tensors)
+
+
 def _items(grads, outs, write):
     """mxfp4_grad_item_t of every tensor, checked, and the number of elements."""
     global _pack
@@ -211,8 +219,6 @@ def _items(grads, outs, write):
             raise RuntimeError("_tensor_list is not built; build it with "
                                "`python -m mxfp4_fake_quantization_amd.build`") from e
         _pack = pack
-    if isinstance(grads, torch.Tensor) or isinstance(outs, torch.Tensor):
-        raise TypeError("grads and outs are lists of tensors")
     gpu = torch.cuda.is_initialized() or torch.cuda.is_available()  # (the second one asks the driver)
     return _pack(grads, outs, torch.cuda.current_device() if gpu else -1, write)
 
@@ -242,7 +248,7 @@ def mxfp4_grad_norm(grads, norm, norm_type=2.0, workspace=None):
     """norm (one float32 element) = the 1-, 2- or inf-norm over all elements of a
     list of gradients, summed in 64 bits.  workspace: a uint8 tensor of
     mxfp4_grad_norm_workspace bytes; allocated from torch when None."""
-    order, pn = _norm_type(norm_type), _norm_out(norm)
+    order, pn, grads = _norm_type(norm_type), _norm_out(norm), _listed(grads)
     items, elements = _items(grads, None, False)
     _here(norm, workspace)
     lib, n = _lib(), len(items) // _ITEM.size
@@ -257,7 +263,7 @@ def mxfp4_grad_clip(grads, max_norm, norm, outs=None, norm_type=2.0, compute_nor
     ``outs``.  norm (one float32 element) receives the norm of ``grads``; without
     ``compute_norm`` it is read instead (a norm over several processes).  What is
     written may overlap nothing else: a tensor given twice is refused."""
-    order, pn = _norm_type(norm_type), _norm_out(norm)
+    order, pn, grads, outs = _norm_type(norm_type), _norm_out(norm), _listed(grads), _listed(outs)
     items, elements = _items(grads, outs, True)
     _here(norm, workspace)
     lib, n = _lib(), len(items) // _ITEM.size
