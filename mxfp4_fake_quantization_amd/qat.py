@@ -18,8 +18,8 @@ twice changes nothing).  Here every step runs in libmxfp4's HIP kernels:
 - ``quantize_model``: swaps every Linear of a model (outside the excluded
   paths) for a QATLinear.
 - ``clip_grad_norm_``: the norm over all gradients of a training step, and clipping,
-  with torch.nn.utils.clip_grad_norm_'s arguments (two launches for a model's hundreds
-  of tensors, sums in 64 bits).
+  with torch.nn.utils.clip_grad_norm_'s arguments (a launch each for norm and clipping of up
+  to 284 tensors or stretches of tensors that lie end to end, sums in 64 bits).
 
 The names of the PR's interface (``mxfp4_fake_quant``, ``MXFP4FakeQuantizer``,
 ``MXFP4QATConfig``, ``MXFP4QATLinear``, ``convert_to_mxfp4_qat``) are kept as
@@ -260,12 +260,13 @@ def quantize_model(model: nn.Module, policy: Optional[QATPolicy] = None,
 
 @torch.no_grad()
 def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0,
-                    error_if_nonfinite: bool = False) -> torch.Tensor:
+                    error_if_nonfinite: bool = False, foreach: Optional[bool] = None) -> torch.Tensor:
     """Scale the gradients of ``parameters`` (tensors, or one) in place by min(1,
     max_norm / (norm + 1e-6)), norm being the 1-, 2- or inf-norm over all of them
     together; returns the norm (float32, on the GPU).  Gradients are contiguous
     bfloat16 or float32 tensors on one GPU, each given once.  With ``error_if_nonfinite`` a norm that
-    is no finite number raises before anything is scaled (and the host waits for it)."""
+    is no finite number raises before anything is scaled (and the host waits for it).
+    ``foreach`` is torch's choice between its loops and means nothing here."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads = [p.grad for p in parameters if p.grad is not None]

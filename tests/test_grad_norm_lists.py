@@ -68,3 +68,15 @@ def test_generators():
     M.mxfp4_grad_clip([2 * t for t in grads], 1.0, norm, outs=want)
     M.mxfp4_grad_clip((2 * t for t in grads), 1.0, got, outs=(t for t in outs))
     assert torch.equal(norm, got) and all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_clip_takes_torchs_arguments():
+    """Every argument of torch.nn.utils.clip_grad_norm_, by name and in its place."""
+    import inspect
+
+    from mxfp4_fake_quantization_amd import qat
+    theirs = inspect.signature(torch.nn.utils.clip_grad_norm_).parameters
+    ours = inspect.signature(qat.clip_grad_norm_).parameters
+    assert list(ours) == list(theirs) and all(ours[k].default == theirs[k].default for k in theirs)
+    for foreach in (None, True, False):
+        assert float(qat.clip_grad_norm_([torch.nn.Parameter(torch.zeros(2))], 1.0, foreach=foreach)) == 0.0
