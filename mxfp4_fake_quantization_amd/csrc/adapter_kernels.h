@@ -9,6 +9,8 @@ namespace mxfp4 {
 
 constexpr int kAdapterMaxRank = 128;
 constexpr int kAdapterMaxTrained = 1024;  // adapters of a backward pass
+// The second product's smallest tile, of 256 threads: what bounds a call's size (the kernel asserts it).
+constexpr int kAdapterLeastRows = 32, kAdapterLeastCols = 256;
 
 // y = base + s u B^T, u = x A^T, with the adapter of each row.
 struct AdapterLaunch {

@@ -393,6 +393,9 @@ __device__ __forceinline__ float parts_sum(const float *u, int64_t part, int spl
 // bf16, 8192 rows, 7168 columns, rank 32: 59.4 with 32 rows, 55.2 with 64).
 template <int DT>
 constexpr int kExpandRows = DT == kBF16 ? 64 : 32;
+static_assert(kExpandRows<kBF16> >= kAdapterLeastRows && kExpandRows<kF32> >= kAdapterLeastRows &&
+                  kExpandWaves * 16 * Tile<kF32>::PE >= kAdapterLeastCols && 64 * kExpandWaves == 256,
+              "the check of a call's size counts these tiles");
 // Waves a SIMD; what lets the weights stay in registers. (bf16 of rank 65 to 128, 1000 rows and columns:
 // 41 us with one wave, 46 with two and 124 registers spilled; fp32 is faster with two and 35 spilled, 4096
 // rows and columns 180 us, else 201.)

@@ -32,9 +32,11 @@ mxfp4_status_t check_adapter(const mxfp4_adapter_t *d) {
                 (long long)d->out_features);
   if (d->in_features > kMostFeatures || d->out_features > kMostFeatures)
     return fail(MXFP4_EUNSUPPORTED, "in_features and out_features above 2^24 are not supported");
-  // a launch has below 2^32 threads: 256 for 64 rows by at least 256 columns
+  // A launch has below 2^32 threads: 256 for each of the second product's tiles.  (The first
+  // product has a workgroup for each 64 rows, or some 2048 where that is more.)
   const int64_t most = d->in_features > d->out_features ? d->in_features : d->out_features;
-  if ((d->tokens / 64 + 1) * (most / 256 + 1) >= (int64_t)1 << 23)
+  const int64_t rows = mxfp4::kAdapterLeastRows, cols = mxfp4::kAdapterLeastCols;
+  if ((d->tokens + rows - 1) / rows * ((most + cols - 1) / cols) >= (int64_t)1 << 24)
     return fail(MXFP4_EUNSUPPORTED, "%lld tokens of %lld features are more than one call takes", (long long)d->tokens,
                 (long long)most);
   return MXFP4_OK;
