@@ -558,8 +558,10 @@ typedef struct mxfp4_adapter {
  * order; an adapter's weights are read once for each 64 consecutive rows that hold
  * it, so tokens of one adapter next to one another are fastest.  u [tokens,
  * rank] fp32 is written when given (the backward pass reads it).  Sums and u in
- * fp32; y is rounded once.  Elements of any alignment, rows ld apart; a row's
- * values depend on that row alone.  workspace: mxfp4_adapter_workspace bytes (-1
+ * fp32; y is rounded once.  Elements of any alignment, rows ld apart.  What stands in
+ * other rows, NaN and infinities too, never reaches a row; the order of its fp32 sums, and
+ * so their last bits, follows from the call's sizes, the row's place and how many rows
+ * beside it have its adapter.  workspace: mxfp4_adapter_workspace bytes (-1
  * for refused arguments), 16-byte aligned, in use until the call's kernels are done.
  */
 int64_t mxfp4_adapter_workspace(const mxfp4_adapter_t *desc);
