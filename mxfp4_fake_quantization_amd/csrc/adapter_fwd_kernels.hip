@@ -369,9 +369,11 @@ int few_splits(const AdapterLaunch &L) {
   const int64_t useful = (L.in * L.rank * (L.dtype == kBF16 ? 2 : 4) + 8192 * kFewWaves - 1) / (8192 * kFewWaves);
   int64_t s = most > 0 ? 512 / most : 1;
   if (s > useful) s = useful;
-  // y's kernel adds the parts up (48 adapters, rank 16, 8192 -> 28672: u + y 7 + 18.7 us, up to 8 parts
-  // 6.8 + 20.8, 2 parts 8 + 18.1; one token 3.6 + 6, 3.6 + 6, 4.6 + 5.6)
-  const int cap = L.rank <= 32 ? 4 : 12;
+  // y's kernel adds the parts up (up to 1 / 2 / 4 / 8 / 12 parts, 4096 -> 4096: one token of rank 16 10.6 / 8.8 /
+  // 8.3 / 8.3 / 8.3 us, rank 64 23.4 / 16.1 / 12.9 / 13.0 / 15.2, rank 128 40.6 / 26.7 / 20.2 / 18.8 / 21.7; 64 tokens
+  // of 48 adapters, rank 16, 8192 -> 28672 28.8 / 25.6 / 25.0 / 27.1 / 27.1, rank 64, 4096 -> 4096
+  // 30.2 / 22.6 / 19.9 / 21.7 / 23.1)
+  constexpr int cap = 4;
   if (s > cap) s = cap;
   return s < 1 ? 1 : (int)s;
 }
