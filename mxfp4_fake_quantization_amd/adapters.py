@@ -17,8 +17,10 @@ adapter's gradients over its own tokens.
       y.sum().backward()                      # gradients of x and the adapters
       clip_grad_norm_(layer.parameters(), 1.0)  # qat.clip_grad_norm_
 
-x is [..., in] bfloat16 or float32 (PackedLinear: bfloat16), ids has x's leading
-shape.  Adapters kept in another type than x's are rounded to x's for the call.
+x is [..., in] bfloat16 or float32 (PackedLinear: bfloat16; under autocast each takes x
+in the projection's type), ids has x's leading shape.  Adapters kept in another type
+than x's are rounded to x's for the call; their gradients, summed in float32, are
+rounded to x's type once and then take the adapters' (as autocast's products do).
 """
 from __future__ import annotations
 

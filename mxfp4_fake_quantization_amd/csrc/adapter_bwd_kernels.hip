@@ -18,8 +18,8 @@ namespace {
 // bf16 elements, no LDS): its 16 bytes are then column PE l + j of fragment j.
 // v, in fp32, is split into three bf16 operands as in the other products.  Bound by the
 // bytes of x and grad_y: 16384 tokens, 4096 -> 4096, rank 16 50 us (5.4 TB/s); 8191
-// tokens, 7168 -> 2048, rank 64 55 us (2.8 TB/s: v, split for four tiles of ranks, takes the
-// rest of the time).
+// tokens, 7168 -> 2048, rank 64 60 us (2.5 TB/s: v, split for four tiles of ranks, and three
+// products of each take the rest of the time).
 
 constexpr int kGradWaves = 4;
 
@@ -216,8 +216,8 @@ __global__ __launch_bounds__(256) void adapter_parts_kernel(const float *parts, 
 // ---- host ------------------------------------------------------------------------------
 
 // Rows of a piece: about 512 workgroups over the columns of both gradients.  (Gradients of A and B, 4096 ->
-// 4096, rank 16: 16384 tokens 79 us, with 1024 workgroups 82.5, 256 83; 2048 tokens 26.6, 29.4, 26.3; 8192
-// tokens, 7168 -> 2048, rank 64, 4 adapters: 77, 81.4, 75.6.)
+// 4096, rank 16: 16384 tokens 79 us, with 1024 workgroups 82.3, 256 83.1; 2048 tokens 26.9, 29.8, 26.6;
+// 8192 tokens, 7168 -> 2048, rank 64, 4 adapters: 82, 84.9, 83.9.)
 int piece_rows(int64_t tokens, int64_t in, int64_t out) {
   const int64_t groups = (in + 127) / 128 + (out + 127) / 128;
   const int64_t per = (tokens * groups / 512 + 127) / 128 * 128;

@@ -16,8 +16,8 @@ namespace {
 // at once) and a part of the long dimension (u) or of the columns (y).
 // One launch that computed u again for every part of the columns read A once a part
 // through each CU's L1 at 64 bytes a clock: 64 tokens of 48 adapters, 8192 -> 28672, rank
-// 16 took 51 us (two launches 7 + 19, 46 MB of B at 2.5 TB/s), one token 4096 -> 4096 9.4
-// (3.6 + 4.8).
+// 16 took 51 us (two launches 6.9 + 19.6, 46 MB of B at 2.3 TB/s), one token 4096 -> 4096
+// 9.4 (3.7 + 5.1).
 
 struct FewArgs {
   const uint8_t *x, *a, *b;
@@ -199,8 +199,9 @@ struct Quad {  // four consecutive elements of a row
   }
 };
 
-// Tiles of a run.  (8 up to rank 32: one token 6 us instead of 4.8, 32 / 128 / 256 rows of 48 adapters, 4096 ->
-// 4096, both kernels 10 / 11.8 / 13.5 instead of 9.1 / 11.1 / 12.3.)
+// Tiles of a run.  (With 8, both kernels: one token of rank 16 9.3 us instead of 8.4, 32 / 128 / 256 rows of 48
+// adapters, 4096 -> 4096, 10.4 / 12.5 / 14.4 instead of 9.5 / 12.0 / 13.4, 32 rows of 8 adapters of rank 64, 4096 ->
+// 14336, 21.3 instead of 18.6.)
 constexpr int kFewTiles = 4;
 
 template <int DT, int RT, int MODE>
@@ -355,9 +356,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void adapter_few_y_kernel(FewArgs A
 }
 
 // Few rows, and few of an adapter: up to 16 on average, one tile; the weights' reading is all there is.
-// (4096 -> 4096, rank 16, 48 adapters: 32 / 256 / 512 rows take 9.1 / 12.3 / 21.1 us, as many rows 42 /
-// 25.7 / 20.5; one adapter: 32 / 256 rows 14.3 / 24.9, as many 13.1 / 12.9; 4096 -> 14336, rank 64, 8
-// adapters: 128 / 256 rows 24 / 40.6, as many 27.1 / 24.  A's rows are reached by 32-bit distances.)
+// (4096 -> 4096, rank 16, 48 adapters: 32 / 256 / 512 rows take 9.5 / 13.4 / 22.0 us, as many rows 42.9 /
+// 29.1 / 23.7; one adapter: 16 / 32 / 256 rows 9.5 / 12.2 / 19.7, as many 13.1 / 13.6 / 13.7; 4096 -> 14336, rank
+// 64, 8 adapters: 128 / 256 rows 22.7 / 37.3, as many 29.5 / 26.1.  A's rows are reached by 32-bit distances.)
 bool few_rows(const AdapterLaunch &L) {
   return L.tokens <= 256 && L.tokens <= 16 * (int64_t)L.adapters && L.rank * L.in < (int64_t)1 << 29;
 }
@@ -383,7 +384,7 @@ hipError_t launch_few(const AdapterLaunch &L, hipStream_t stream) {
   const int cols = 16 * kFewTiles;
   const int64_t most = L.adapters < L.tokens ? L.adapters : L.tokens;
   const int64_t useful = ((L.out + cols - 1) / cols + kFewWaves - 1) / kFewWaves;
-  int64_t parts = 2048 / most;  // (48 adapters, out 28672: 19 us; twice as many 20.4, two thirds 20.5)
+  int64_t parts = 2048 / most;  // (48 adapters, 8192 -> 28672, both kernels: 26.1 us; twice as many 27.7, two thirds 24.0; 4096 -> 14336 alike)
   if (parts > useful) parts = useful;
   if (parts < 1) parts = 1;
   const int splits = few_splits(L), mode = piece_mode(DT, L.tokens, L.in, L.out, L.rank);

@@ -386,19 +386,21 @@ __device__ __forceinline__ float parts_sum(const float *u, int64_t part, int spl
 // (the wave's 16 KB) and u, of which wave w makes the fragments of rows 16 w to 16 w +
 // 15 for all.  Then the adapters of the window pass one after the other; a row takes
 // the result of its own one, so that no other adapter's values (an infinity, say) reach it.
-// Bound by the bytes of base and y: 8192 x 7168 bf16, rank 32 50.5 us (4.8 TB/s), 4096 x 4096
-// fp32, rank 8 27.5 us (4.9 TB/s), both with their base.
+// Bound by the bytes of base and y: 8192 x 7168 bf16, rank 32 51.5 us (4.7 TB/s), 4096 x 4096
+// fp32, rank 8 27.1 us (5.0 TB/s), both with their base.
 // Rows of a workgroup: 64, with the 16-byte pieces of 128 columns a row; 32 in fp32, whose registers
-// then leave room for a wave more (4096 rows, 4096 columns, rank 8: 28.8 us, with 64 rows 31.2;
-// bf16, 8192 rows, 7168 columns, rank 32: 59.4 with 32 rows, 55.2 with 64).
+// then leave room for a wave more.  (Both kernels of the forward, 4096 rows and columns, bf16 of rank 64 /
+// 128: 36.9 / 69.1 us, with 32 rows 43.6 / 88.3.  fp32 of rank 8 41.7 us and, now that the tiles are
+// kept apart below, 40.4 with 64 rows; rank 64 / 128 91.5 / 161.6, and 79.6 / 140.4.)
 template <int DT>
 constexpr int kExpandRows = DT == kBF16 ? 64 : 32;
 static_assert(kExpandRows<kBF16> >= kAdapterLeastRows && kExpandRows<kF32> >= kAdapterLeastRows &&
                   kExpandWaves * 16 * Tile<kF32>::PE >= kAdapterLeastCols && 64 * kExpandWaves == 256,
               "the check of a call's size counts these tiles");
-// Waves a SIMD; what lets the weights stay in registers. (bf16 of rank 65 to 128, 1000 rows and columns:
-// 41 us with one wave, 46 with two and 124 registers spilled; fp32 is faster with two and 35 spilled, 4096
-// rows and columns 180 us, else 201.)
+// Waves a SIMD; what lets the weights stay in registers.  (bf16 of rank 65 to 128, 1000 rows and columns:
+// 41 us with one wave, 46 with two and registers spilled; 4096 rows and columns 69 and 62.  fp32 is
+// faster with two and 12 to 19 spilled, 4096 rows and columns 162 us, else 193; 209 for the weights across
+// ragged rows.)
 template <int DT, int NF>
 constexpr int kExpandOccupancy = NF <= 1 ? (DT == kBF16 ? 3 : 4) : DT == kBF16 && NF >= 4 ? 1 : 2;
 
@@ -550,9 +552,10 @@ __global__ __launch_bounds__(64 * kExpandWaves, (kExpandOccupancy<DT, NF>)) void
 inline int window_count(int64_t tokens) { return (int)((tokens + kWindow - 1) / kWindow); }
 
 // Parts of the long dimension: as many as put a workgroup on each of the 256 CUs. The second kernel
-// adds the parts up once a tile of columns, so fewer are better there (8192 tokens, 7168 columns,
-// rank 64, both kernels of the backward: 23 + 61 us; with two workgroups a CU 31 + 70, and with half a
-// workgroup 24 + 54; but 4096 tokens of fp32, rank 8: 14.4 + 28, two 15.2 + 28.8, half 21.7 + 27.2).
+// adds the parts up once a tile of columns, so fewer are better there (both kernels, with one workgroup a CU,
+// two, and half a one: 8192 tokens, 7168 -> 7168, rank 32 80.2 / 85.7 / 86.5 us; gradient of x, rank 64 73 / 80
+// / 89; 4096 tokens of fp32, rank 8 41.7 / 44.8 / 47.9; all gradients of 8191 tokens, 7168 -> 2048, rank 64 149.5 /
+// 161.6 / 143).
 inline int shrink_splits(int64_t tokens, int64_t K) {
   const int64_t windows = window_count(tokens);
   const int64_t most = (K + 511) / 512;

@@ -4,7 +4,8 @@
 //     out  = g * min(1, max_norm / (norm + 1e-6)).
 // Bound by the bytes: the gradients once for the norm, once more (from the 256 MB
 // cache, where they fit) and written once for clipping (235 MB 38 us, 6.2 TB/s; 1.9 GB in
-// and out 281 + 773 us, 6.7 and 4.9 TB/s).  Sums are held in 64 bits
+// and out 277 + 770 us, 6.8 and 4.9 TB/s).  448 tensors of odd sizes that lie apart, 115 MB in
+// fp32: norm 31.5 us, clipping in place 85.7 (end to end, and so one tensor: 21.5 and 60).  Sums are held in 64 bits
 // throughout: the squares of any fp32 values neither overflow nor vanish, and the
 // matrix-free arithmetic of two double operations an element hides behind the
 // loads.  A workgroup sums a contiguous run of chunks and writes one partial sum;
@@ -136,8 +137,10 @@ __device__ __forceinline__ int item_of(const Batch<OUT> &B, uint32_t chunk) {
 }
 
 // partial: one double a workgroup; or, NULL, the norm itself.  NT: the gradients are not read
-// again, or too many for the 256 MB cache: they pass by it (235 MB 38 us, else 43; before
-// clipping, 117 MB 70 us instead of 62 for both passes, 1.9 GB 1041 instead of 1056).
+// again, or too many for the 256 MB cache: they pass by it.  (A norm of 235 MB 38 us, else 43.
+// Norm and clipping, through the cache / by it: in place 128 MB 69 / 74 us, 192 MB 118 / 118, 256 MB 160 /
+// 161, 320 MB 203 / 198, 512 MB 318 / 299, 1.8 GB 1101 / 1056; out of place 128 MB 67 / 79, 256 MB 133 / 153,
+// 320 MB 172 / 190, 512 MB 282 / 295, 1 GB 578 / 581, 1.8 GB 1061 / 1053.)
 template <int P, bool NT>
 __global__ __launch_bounds__(kNormThreads) void grad_norm_kernel(Batch<false> B, double *partial, float *norm) {
   __shared__ double lds[kNormThreads / 64];
