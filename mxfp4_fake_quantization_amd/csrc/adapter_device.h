@@ -15,11 +15,12 @@
 // row 4 q + v (v = 0..3) of the first operand and row l % 16 of the second.
 //
 // u is kept in fp32.  As an operand of a bf16 product it is split into three parts,
-// u = hi + mid + lo: 8 bits toward 0 of u, of the rest, and what is left then, at most 8 of u's
-// 24 bits, so nothing is lost (but below 2^-133) and y is rounded once, to its type.  All
-// three have u's sign and are 0 for 0 alone, so an infinite weight or row gives what u does.  (Two parts lose 2^-16 of u, more than y itself where the terms cancel.  The
-// third costs 1 to 4 % of the products' time, 4096 rows and columns of rank 128 8 % of all
-// gradients': 144 -> 157 us.)
+// u = hi + mid + lo: 8 bits toward 0 of u, of the rest, and what is left then, at most 8 of
+// u's 24 bits, so nothing is lost (but below 2^-133) and y is rounded once, to its type.
+// All three have u's sign and are 0 for 0 alone, so an infinite weight or row gives what u
+// does.  (Two parts lose 2^-16 of u, more than y itself where the terms cancel.  The third
+// costs 1 to 4 % of the products' time, 8 % of all gradients' of 4096 rows and columns of
+// rank 128: 144 -> 157 us.)
 #pragma once
 
 #include "adapter_kernels.h"
